@@ -390,6 +390,163 @@ kda_status kda_state_combine(int32_t count, int32_t dk, int32_t dv,
                              void* stream);
 
 /*
+ * ---- The draft step: operators around a tree of drafted tokens per sequence ----
+ *
+ * (llm-atlas K3_RESEARCH.md, Q28: draft tokens verified by the target; Q03 and Q31: KDA
+ * layers beside attention layers with a paged cache.)  They share one description of the
+ * trees, `parents` [B, K] int32, 1 <= K <= KDA_TREE_MAX_NODES:
+ *   parents[b][i] = -1            node i follows the context
+ *   0 <= parents[b][i] < i        node i follows that node
+ *   parents[b][i] = KDA_TREE_PAD  there is no node i (trees of a batch may differ in size);
+ *                                 no node may follow an absent one
+ * A chain is parents[b][i] = i - 1.  A tree that breaks these rules is found on the device:
+ * its sequence is skipped and kda_last_device_status() returns KDA_ERR_INVALID_ARG.
+ */
+#define KDA_TREE_MAX_NODES 64
+#define KDA_TREE_PAD (-2)
+
+/*
+ * kda_page_tables -- pages and slots for the tokens that a step appends to a paged cache,
+ * built on the device from request lengths.  Request b has context_lens[b] tokens in the
+ * cache, appends new_lens[b], and holds its first pages_held[b] table entries; the pages it
+ * lacks are taken from free_pages in request order.
+ *
+ *   context_lens, new_lens, pages_held  [B] int32; pages_held covers the context
+ *   block_table    [B, table_cols] int32, in place: the new pages' ids are written after the
+ *                  held ones, nothing else is
+ *   free_pages     [num_free] int32 page ids, taken from index 0 on (may be NULL when 0)
+ *   slot_map       [max_tokens] int64: slot (page * page_size + offset) of every appended
+ *                  token, request after request; -1 for a refused request's tokens and past the last
+ *   cu_seqlens     [B + 1] int32: first appended token of each request (kda_prefill's layout)
+ *   pages_held_out [B] int32;  pages_taken [1] int32: free_pages entries used up
+ * A request whose tokens exceed its table row, or for which the free pages do not reach, is
+ * refused: its pages_held_out is pages_held and its slots are -1.  Once the free pages have
+ * not reached for one request, no later one takes any.  Negative lengths, or pages_held
+ * that do not cover the context or exceed table_cols, make the request append nothing; more than max_tokens tokens leave
+ * the rest without slots; both make kda_last_device_status() return KDA_ERR_INVALID_ARG.
+ * No output may overlap an input or another output.  batch <= KDA_PAGE_TABLES_MAX_BATCH.
+ */
+#define KDA_PAGE_TABLES_MAX_BATCH 16384
+
+kda_status kda_page_tables(int32_t batch, int32_t table_cols, int32_t num_free, int32_t page_size, int32_t max_tokens,
+                           const int32_t* context_lens, const int32_t* new_lens, const int32_t* pages_held,
+                           int32_t* block_table, const int32_t* free_pages,
+                           int64_t* slot_map, int32_t* cu_seqlens, int32_t* pages_held_out, int32_t* pages_taken,
+                           void* stream);
+
+/* Shape of one kda_tree_attention call. */
+typedef struct kda_tree_attention_desc {
+    int32_t batch;          /* B >= 0 */
+    int32_t nodes;          /* K, 1 .. KDA_TREE_MAX_NODES */
+    int32_t num_heads;      /* query heads Hq, a multiple of num_kv_heads */
+    int32_t num_kv_heads;   /* cache heads Hk >= 1 */
+    int32_t dim;            /* channels per head: 64 or 128 */
+    int32_t dtype;          /* a kda_dtype, of q, the caches and out */
+    int32_t num_pages;      /* pages of the caches */
+    int32_t page_size;      /* tokens of a page >= 1 */
+    int32_t table_cols;     /* pages a sequence's table row can hold */
+    float scale;            /* factor of the scores, finite */
+    int64_t k_page_stride;  /* elements from one page to the next, >= page_size * Hk * dim, */
+    int64_t v_page_stride;  /*   a multiple of 16 bytes */
+} kda_tree_attention_desc;
+
+/* Bytes of device scratch kda_tree_attention needs for `desc`; 0 for one it would reject. */
+size_t kda_tree_attention_workspace_bytes(const kda_tree_attention_desc* desc);
+
+/*
+ * kda_tree_attention -- softmax attention of every node of every draft tree over a paged
+ * key/value cache.  Node i of sequence b attends to the sequence's context_lens[b] cached
+ * tokens and to the nodes on its own path from the context, itself included; node j's key
+ * and value lie in the cache at logical position context_lens[b] + j.  K = 1 with parent -1
+ * is single-token decode.
+ *
+ *   q             [B, K, Hq, dim] dtype
+ *   k_cache, v_cache  page p, offset s, head h at p * page_stride + (s * Hk + h) * dim; query
+ *                 head h reads cache head h / (Hq / Hk)
+ *   block_table   [B, table_cols] int32: page of logical positions [j page_size, (j + 1) page_size)
+ *   context_lens  [B] int32;  parents [B, K] int32
+ *   out           [B, K, Hq, dim] dtype; zeros for absent nodes
+ *   workspace     kda_tree_attention_workspace_bytes(desc) bytes, 16-byte aligned, clobbered;
+ *                 two calls in flight at once need two
+ * Whatever lies in the cache where a node may not look (past the last node, pages of others,
+ * nodes of other paths) does not change its output, NaN included.  A sequence whose
+ * context_lens is negative, or exceeds its table row with the K nodes added, or whose tree is
+ * bad, gets zeros; a token whose page id is outside [0, num_pages) is left out; both make
+ * kda_last_device_status() return KDA_ERR_INVALID_ARG.  bf16: the softmax's weights are
+ * rounded to bf16 before they meet the values (their sum is kept in fp32), fp32: fp32 throughout.
+ */
+kda_status kda_tree_attention(const kda_tree_attention_desc* desc,
+                              const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_table, const int32_t* context_lens, const int32_t* parents,
+                              void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_tree_decode -- KDA for every node of every draft tree from one read of the state: node
+ * i's state is its parent's (the context's for parent -1) after one kda_decode step with its
+ * own inputs.  The state is not changed; kda_tree_commit moves it.
+ *
+ *   q, k    [B, K, H, dk] qkv_dtype;  v [B, K, H, dv] qkv_dtype
+ *   g       [B, K, H, dk] fp32;       beta [B, K, H] fp32
+ *   parents [B, K] int32
+ *   gate    [B, K, H, dv] fp32 logits of the output gate, or NULL
+ *   state   [B, H, dk, dv] fp32, only read
+ *   out     [B, K, H, dv] fp32, S_i^T q_i (gated);  zeros for absent nodes
+ *   writes  [B, K, H, dv] fp32, beta_i (v_i - S'_i^T k_i) with S'_i the decayed state of
+ *           the parent: what kda_tree_commit needs;  zeros for absent nodes
+ * prologue as kda_decode.  out and writes overlap nothing.  Depth is not limited below K.
+ */
+kda_status kda_tree_decode(int32_t batch, int32_t nodes, int32_t num_heads, int32_t dk, int32_t dv,
+                           int32_t qkv_dtype, int32_t prologue,
+                           const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const int32_t* parents, const float* gate,
+                           const float* state, float* out, float* writes, void* stream);
+
+/*
+ * kda_tree_commit -- each state moved to the end of an accepted path: after kda_tree_decode
+ * on the same state with the same k, g and prologue, the state of node path[b][n_accept[b] - 1].
+ *
+ *   k [B, K, H, dk] qkv_dtype;  g [B, K, H, dk] fp32;  writes [B, K, H, dv] fp32
+ *   path     [B, K] int32: the accepted nodes from the context on, in its first n_accept[b] entries
+ *   n_accept [B] int32, 0 .. K; 0 leaves the state untouched
+ *   state    [B, H, dk, dv] fp32 in place; overlaps nothing else
+ * A path entry outside [0, K) or a count out of range leaves that state untouched and makes
+ * kda_last_device_status() return KDA_ERR_INVALID_ARG.  prologue: the QK_L2NORM and G_LOGITS
+ * bits (BETA_LOGITS is accepted and has no effect here).
+ */
+kda_status kda_tree_commit(int32_t batch, int32_t nodes, int32_t num_heads, int32_t dk, int32_t dv,
+                           int32_t qkv_dtype, int32_t prologue,
+                           const void* k, const float* g, const float* writes,
+                           const int32_t* path, const int32_t* n_accept, float* state, void* stream);
+
+/*
+ * kda_verify_drafts -- which drafted tokens the target's probabilities keep, and the token
+ * that follows them, from given random numbers.  From the context on, the children of the
+ * current node are looked at in index order; child c with token x is kept when
+ *     uniforms[c] * draft[c][x] < p[x]                             (draft given)
+ *     uniforms[c] * m < p[x],  m = 1 - (p of the children before it)   (draft NULL)
+ * with p the target's row of the current node; the walk goes on from a kept child.  Where
+ * none is kept the next token is the argmax (lowest index first) of rest / noise: rest =
+ * max(p - draft[c], 0) after a turned-down child c (draft given), p without the turned-down tokens
+ * (draft NULL), p itself when there is none or nothing is left.  With noise ~ Exp(1) and
+ * uniforms ~ U[0, 1) the kept tokens and the next one are distributed as the target's.
+ * Every step is one IEEE fp32 operation per element.  A child whose token was turned down
+ * at the same node before is passed over (draft NULL).
+ *
+ *   target   [B, K + 1, V] fp32: row 0 after the context, row i + 1 after node i; >= 0
+ *   draft    [B, K, V] fp32: row i the distribution that node i's token was drawn from; then no
+ *            two nodes may have the same parent.  NULL: tokens picked by rank or any other rule
+ *   tokens, parents  [B, K] int32;  uniforms [B, K] fp32;  noise [B, V] fp32, > 0
+ *   path     [B, K] int32: kept nodes in order, then -1;  n_accept [B] int32;  next_token [B] int32
+ * path and n_accept are kda_tree_commit's; for chains n_accept is kda_decode_multi's n_apply.
+ * A bad tree, or a token outside [0, V): path -1, n_accept 0, next_token -1, and
+ * kda_last_device_status() returns KDA_ERR_INVALID_ARG.
+ */
+kda_status kda_verify_drafts(int32_t batch, int32_t nodes, int32_t vocab,
+                             const float* target, const float* draft, const int32_t* tokens, const int32_t* parents,
+                             const float* uniforms, const float* noise,
+                             int32_t* path, int32_t* n_accept, int32_t* next_token, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word of the
  * current device: KDA_OK, KDA_ERR_INVALID_ARG (bad cu_seqlens seen on the
  * device) or KDA_ERR_TIMEOUT (a bounded wait gave up).  KDA_ERR_CUDA if the

@@ -34,9 +34,14 @@ KDA_PROLOGUE_ALL = 7
 EXPORTED = ("kda_abi_version", "kda_status_string", "kda_prefill_workspace_bytes", "kda_prefill_query",
             "kda_prefill", "kda_prefill_gated", "kda_prefill_checkpointed", "kda_prefill_host_workspace_bytes",
             "kda_prefill_host", "kda_prefill_host_static", "kda_decode", "kda_decode_gated", "kda_decode_multi",
-            "kda_decode_multi_gated", "kda_state_combine", "kda_last_device_status")
+            "kda_decode_multi_gated", "kda_state_combine", "kda_last_device_status", "kda_page_tables",
+            "kda_tree_attention_workspace_bytes", "kda_tree_attention", "kda_tree_decode", "kda_tree_commit",
+            "kda_verify_drafts")
 KDA_DECODE_MULTI_MAX_TOKENS = 64
 KDA_STATIC_SCRATCH_BYTES = 64 << 20
+KDA_TREE_MAX_NODES = 64
+KDA_TREE_PAD = -2          # parents entry of an absent node
+KDA_PAGE_TABLES_MAX_BATCH = 16384
 
 
 class KDAError(RuntimeError):
@@ -49,6 +54,12 @@ class PrefillDesc(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("qkv_dtype", ctypes.c_int32),
                 ("prologue", ctypes.c_int32)]
+
+
+class TreeAttentionDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "nodes", "num_heads", "num_kv_heads", "dim", "dtype", "num_pages",
+                                              "page_size", "table_cols")] + \
+               [("scale", ctypes.c_float), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64)]
 
 
 class PrefillPlan(ctypes.Structure):
@@ -104,6 +115,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                            vp]
     lib.kda_state_combine.restype = ctypes.c_int
     lib.kda_state_combine.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.kda_page_tables.restype = ctypes.c_int
+    lib.kda_page_tables.argtypes = [i32] * 5 + [vp] * 10
+    lib.kda_tree_attention_workspace_bytes.restype = sz
+    lib.kda_tree_attention_workspace_bytes.argtypes = [ctypes.POINTER(TreeAttentionDesc)]
+    lib.kda_tree_attention.restype = ctypes.c_int
+    lib.kda_tree_attention.argtypes = [ctypes.POINTER(TreeAttentionDesc)] + [vp] * 8 + [sz, vp]
+    lib.kda_tree_decode.restype = ctypes.c_int
+    lib.kda_tree_decode.argtypes = [i32] * 7 + [vp] * 11
+    lib.kda_tree_commit.restype = ctypes.c_int
+    lib.kda_tree_commit.argtypes = [i32] * 7 + [vp] * 7
+    lib.kda_verify_drafts.restype = ctypes.c_int
+    lib.kda_verify_drafts.argtypes = [i32] * 3 + [vp] * 10
     lib.kda_last_device_status.restype = ctypes.c_int
     lib.kda_last_device_status.argtypes = [vp]
     if path is None:
@@ -348,6 +371,183 @@ def state_combine(transition, state_in, state_add, out=None, *, stream=None, che
     if check and st != KDA_OK:
         raise KDAError(st, "kda_state_combine")
     return out
+
+
+# ---- the draft step (include/kda.h) -----------------------------------------------------
+def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    """The C calls know pointers only: a wrong type, shape or device is found here."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def page_tables(context_lens, new_lens, pages_held, block_table, free_pages, *, page_size: int, max_tokens: int,
+                stream=None, check=True):
+    """Pages and slots for the tokens a step appends to a paged cache, through ``kda_page_tables``:
+    context_lens, new_lens, pages_held [B] int32; block_table [B, cols] int32, updated in place;
+    free_pages [F] int32, taken from index 0 on; ``max_tokens``: length of the slot map (>= the sum
+    of new_lens).  Returns (slot_map [max_tokens] int64, cu_seqlens [B+1] int32, pages_held after
+    the call [B] int32, pages_taken [1] int32)."""
+    dev, (B, cols) = block_table.device, block_table.shape
+    i32 = torch.int32
+    for name, t in (("context_lens", context_lens), ("new_lens", new_lens), ("pages_held", pages_held)):
+        _expect(name, t, i32, (B,), dev)
+    _expect("block_table", block_table, i32, (B, cols), dev)
+    _expect("free_pages", free_pages, i32, (free_pages.numel(),), dev)
+    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+    cu = torch.empty(B + 1, dtype=i32, device=dev)
+    held = torch.empty(B, dtype=i32, device=dev)
+    taken = torch.empty(1, dtype=i32, device=dev)
+    if stream is not None:
+        for t in (slots, cu, held, taken):
+            _keep_until_done(t, stream)
+    st = load().kda_page_tables(B, cols, free_pages.numel(), int(page_size), int(max_tokens), _ptr(context_lens),
+                                _ptr(new_lens), _ptr(pages_held), _ptr(block_table), _ptr(free_pages), _ptr(slots),
+                                _ptr(cu), _ptr(held), _ptr(taken), _stream_handle(stream))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_page_tables")
+    return slots, cu, held, taken
+
+
+def _cache_stride(name: str, c: torch.Tensor) -> int:
+    """Elements from page to page of a cache [pages, page_size, heads, dim] whose pages are contiguous."""
+    _, ps, h, d = c.shape
+    if c.stride()[1:] != (h * d, d, 1) and c.numel() > 0 and not c[0].is_contiguous():
+        raise ValueError(f"{name}: each page must be contiguous")
+    return c.stride(0) if c.shape[0] > 1 else ps * h * d
+
+
+def make_tree_attention_desc(batch, nodes, num_heads, num_kv_heads, dim, dtype, num_pages, page_size, table_cols,
+                             scale, k_page_stride, v_page_stride) -> TreeAttentionDesc:
+    return TreeAttentionDesc(batch, nodes, num_heads, num_kv_heads, dim, dtype, num_pages, page_size, table_cols,
+                             scale, k_page_stride, v_page_stride)
+
+
+def tree_attention_workspace_bytes(desc: TreeAttentionDesc) -> int:
+    return int(load().kda_tree_attention_workspace_bytes(ctypes.byref(desc)))
+
+
+def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents, out=None, *, scale: Optional[float] = None,
+                   workspace=None, stream=None, check=True):
+    """Attention of draft trees over a paged cache, through ``kda_tree_attention``.
+
+    q [B,K,Hq,D] (fp32 or bf16); k_cache, v_cache [pages, page_size, Hk, D] of q's type, each page
+    contiguous (the pages themselves may be strided, as in views of one [pages, 2, ...] tensor);
+    block_table [B, cols] int32; context_lens [B] int32; parents [B,K] int32; ``scale`` defaults
+    to 1 / sqrt(D).  Node j's key and value lie at logical position context_lens + j.  Returns
+    out [B,K,Hq,D] of q's type."""
+    B, K, H, D = q.shape
+    P, ps, Hk, _ = k_cache.shape
+    dev = q.device
+    _expect("k_cache", k_cache, q.dtype, (P, ps, Hk, D), dev)
+    _expect("v_cache", v_cache, q.dtype, (P, ps, Hk, D), dev)
+    _expect("block_table", block_table, torch.int32, (B, block_table.shape[-1]), dev)
+    _expect("context_lens", context_lens, torch.int32, (B,), dev)
+    _expect("parents", parents, torch.int32, (B, K), dev)
+    desc = TreeAttentionDesc(B, K, H, Hk, D, _dtype_code(q), P, ps, block_table.shape[1],
+                             D ** -0.5 if scale is None else scale, _cache_stride("k_cache", k_cache),
+                             _cache_stride("v_cache", v_cache))
+    if out is None:
+        out = torch.empty((B, K, H, D), dtype=q.dtype, device=dev)
+        _keep_until_done(out, stream)
+    else:
+        _expect("out", out, q.dtype, (B, K, H, D), dev)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.kda_tree_attention_workspace_bytes(ctypes.byref(desc)), dtype=torch.uint8, device=dev)
+        _keep_until_done(workspace, stream)
+    at = lambda c: ctypes.c_void_p(c.data_ptr()) if c.numel() > 0 else None
+    st = lib.kda_tree_attention(ctypes.byref(desc), _ptr(q), at(k_cache), at(v_cache), _ptr(block_table),
+                                _ptr(context_lens), _ptr(parents), _ptr(out), _ptr(workspace),
+                                workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_tree_attention")
+    return out
+
+
+def tree_decode(q, k, v, g, beta, parents, state, out=None, writes=None, *, stream=None, check=True,
+                prologue: int = 0, gate=None):
+    """KDA for every node of draft trees through ``kda_tree_decode``: q, k [B,K,H,dk], v
+    [B,K,H,dv] (fp32 or bf16); g [B,K,H,dk], beta [B,K,H] fp32; parents [B,K] int32; ``state``
+    [B,H,dk,dv] fp32 is only read; ``prologue``: KDA_PROLOGUE_* bits; ``gate``: output gate logits
+    [B,K,H,dv] fp32.  Returns (out, writes), both [B,K,H,dv] fp32; ``tree_commit`` takes writes."""
+    B, K, H, dk = q.shape
+    dv, dev, f32 = v.shape[3], q.device, torch.float32
+    _expect("k", k, q.dtype, (B, K, H, dk), dev)
+    _expect("v", v, q.dtype, (B, K, H, dv), dev)
+    _expect("g", g, f32, (B, K, H, dk), dev)
+    _expect("beta", beta, f32, (B, K, H), dev)
+    _expect("parents", parents, torch.int32, (B, K), dev)
+    _expect("state", state, f32, (B, H, dk, dv), dev)
+    if gate is not None:
+        _expect("gate", gate, f32, (B, K, H, dv), dev)
+    if out is None:
+        out = torch.empty((B, K, H, dv), dtype=f32, device=dev)
+        _keep_until_done(out, stream)
+    else:
+        _expect("out", out, f32, (B, K, H, dv), dev)
+    if writes is None:
+        writes = torch.empty((B, K, H, dv), dtype=f32, device=dev)
+        _keep_until_done(writes, stream)
+    else:
+        _expect("writes", writes, f32, (B, K, H, dv), dev)
+    st = load().kda_tree_decode(B, K, H, dk, dv, _dtype_code(q), int(prologue), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                _ptr(beta), _ptr(parents), _ptr(gate), _ptr(state), _ptr(out), _ptr(writes),
+                                _stream_handle(stream))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_tree_decode")
+    return out, writes
+
+
+def tree_commit(k, g, writes, path, n_accept, state, *, stream=None, check=True, prologue: int = 0):
+    """``state`` [B,H,dk,dv] fp32 moved in place to the end of each accepted path, through
+    ``kda_tree_commit``: k, g and ``prologue`` as given to ``tree_decode``, ``writes`` as it returned
+    them; path [B,K] and n_accept [B] int32 as ``verify_drafts`` returns them.  Returns state."""
+    B, K, H, dk = k.shape
+    dv, dev = state.shape[3], k.device
+    _expect("g", g, torch.float32, (B, K, H, dk), dev)
+    _expect("writes", writes, torch.float32, (B, K, H, dv), dev)
+    _expect("path", path, torch.int32, (B, K), dev)
+    _expect("n_accept", n_accept, torch.int32, (B,), dev)
+    _expect("state", state, torch.float32, (B, H, dk, dv), dev)
+    st = load().kda_tree_commit(B, K, H, dk, dv, _dtype_code(k), int(prologue), _ptr(k), _ptr(g), _ptr(writes),
+                                _ptr(path), _ptr(n_accept), _ptr(state), _stream_handle(stream))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_tree_commit")
+    return state
+
+
+def verify_drafts(target_probs, tokens, parents, uniforms, noise, draft_probs=None, *, stream=None, check=True):
+    """Which drafted tokens are kept and what follows them, through ``kda_verify_drafts``:
+    target_probs [B,K+1,V] fp32 (row 0 after the context, row i+1 after node i); tokens, parents
+    [B,K] int32; uniforms [B,K] fp32 in [0, 1); noise [B,V] fp32 ~ Exp(1); ``draft_probs``
+    [B,K,V] fp32 for chains drawn from a draft model, None for drafts picked by any other rule.
+    Returns (path [B,K] int32 with -1 after the kept nodes, n_accept [B] int32, next_token [B]
+    int32)."""
+    B, K1, V = target_probs.shape
+    K, dev, i32, f32 = K1 - 1, target_probs.device, torch.int32, torch.float32
+    _expect("target_probs", target_probs, f32, (B, K1, V), dev)
+    _expect("tokens", tokens, i32, (B, K), dev)
+    _expect("parents", parents, i32, (B, K), dev)
+    _expect("uniforms", uniforms, f32, (B, K), dev)
+    _expect("noise", noise, f32, (B, V), dev)
+    if draft_probs is not None:
+        _expect("draft_probs", draft_probs, f32, (B, K, V), dev)
+    path = torch.empty((B, K), dtype=i32, device=dev)
+    n_accept = torch.empty(B, dtype=i32, device=dev)
+    next_token = torch.empty(B, dtype=i32, device=dev)
+    if stream is not None:
+        for t in (path, n_accept, next_token):
+            _keep_until_done(t, stream)
+    st = load().kda_verify_drafts(B, K, V, _ptr(target_probs), _ptr(draft_probs), _ptr(tokens), _ptr(parents),
+                                  _ptr(uniforms), _ptr(noise), _ptr(path), _ptr(n_accept), _ptr(next_token),
+                                  _stream_handle(stream))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_verify_drafts")
+    return path, n_accept, next_token
 
 
 def last_device_status(stream=None) -> int:

@@ -6,6 +6,7 @@
 
 #include "../../include/kda.h"
 #include "kda_common.cuh"
+#include "kda_draft_launch.h"
 #include "kda_launch.h"
 
 namespace {
@@ -237,6 +238,8 @@ kda_status prefill_impl(const kda_prefill_desc* desc, const void* q, const void*
 }  // namespace
 
 namespace kda {
+
+int* device_status_ptr() { return status_ptr_for_current_device(); }
 
 // kda_prefill restricted to the kernels that need no workspace (the host-buffer path's rounds)
 kda_status prefill_no_workspace(const kda_prefill_desc* desc, const void* q, const void* k, const void* v,

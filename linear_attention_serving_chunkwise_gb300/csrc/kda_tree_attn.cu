@@ -1,0 +1,239 @@
+// Softmax attention of a draft tree's tokens over a paged key/value cache, on the CUDA cores
+// (fp32 throughout): node i of sequence b attends to the sequence's context_lens[b] cached
+// tokens and to the nodes on its own path, whose keys and values lie in the cache at the
+// logical positions context + j.  One pass over the tokens with the running maximum and sum
+// of the softmax; query heads of one group share each loaded tile.
+//
+// A tile's values are zeroed where no row may see the token (past the last node, a page out
+// of range): a masked weight is 0, and 0 times whatever lies there must not be NaN.  In the
+// tiles that hold draft nodes, where each row sees other nodes, a weight of 0 is skipped.
+#include "kda_tree_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBN = 64;
+
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// TM rows and 4 tokens (then D / 16 channels) per thread of a 16 x 16 grid
+template <typename Tin, int D, int TM>
+__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a, attn::Shape sh)
+{
+    constexpr int BM = 16 * TM, CD = D / 16, LD = D + 4, LP = kBN + 4;
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;                   // [BM][LD]
+    float* sk = sq + BM * LD;         // [BN][LD]
+    float* sv = sk + kBN * LD;        // [BN][LD]
+    float* sp = sv + kBN * LD;        // [BM][LP]
+    __shared__ TreeSmem ts;
+    __shared__ long long s_total, s_start;
+    __shared__ int s_seq;
+    __shared__ unsigned char s_on[kBN];   // the tile's tokens that exist
+
+    const int t = threadIdx.x, lane = t & 31, ty = t >> 4, tx = t & 15;
+    const int G = a.heads / a.kv_heads, rb = attn::row_blocks(a, BM), per_seq = rb * a.kv_heads, R = a.nodes * G;
+    const float sc = a.scale * 1.4426950408889634f;     // scores in powers of two
+
+    if (t < 32) {
+        const long long T = attn::line_total(a, kBN, per_seq, lane);
+        int seq;
+        long long start;
+        attn::line_find(a, kBN, per_seq, attn::line_start(T, blockIdx.x, sh.ctas), lane, seq, start);
+        if (lane == 0) { s_total = T; s_seq = seq; s_start = start; }
+    }
+    __syncthreads();
+    const long long T = s_total, lo = attn::line_start(T, blockIdx.x, sh.ctas), hi = attn::line_start(T, blockIdx.x + 1, sh.ctas);
+    int b = s_seq, masks_of = -1;
+    long long b0 = s_start;
+    bool bad_page = false;
+
+    for (long long at = lo; at < hi;) {
+        int tiles = attn::seq_tiles(a, b, kBN);
+        while (at >= b0 + (long long)tiles * per_seq) {
+            b0 += (long long)tiles * per_seq;
+            ++b;
+            tiles = attn::seq_tiles(a, b, kBN);
+        }
+        const int u = (int)((at - b0) / tiles);
+        const long long us = b0 + (long long)u * tiles, ue = us + tiles;
+        const int first = (int)(at - us), last = (int)(min(hi, ue) - us);
+        const int hk = u / rb, r0 = (u % rb) * BM;
+        bool ok;
+        const int n = attn::seq_tokens(a, b, ok), ctx = n - a.nodes;
+
+        __syncthreads();              // the last unit's reads of shared memory are done
+        if (masks_of != b) {
+            if (t < 32) tree_masks(ts, a.parents + (size_t)b * a.nodes, a.nodes, lane);
+            masks_of = b;
+        }
+        for (int idx = t; idx < BM * D; idx += kThreads) {
+            const int r = idx / D, c = idx - r * D, row = r0 + r;
+            sq[r * LD + c] = row < R ? to_f32(static_cast<const Tin*>(a.q)[(((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D + c]) : 0.f;
+        }
+        __syncthreads();
+        const bool live = ok && ts.ok;
+        if (!live && t == 0) report_status(a.status, kDevBadSeqlens);
+
+        float m[TM], l[TM], o[TM][CD];
+        uint64_t see[TM];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int row = r0 + ty * TM + i;
+            see[i] = live && row < R ? ts.anc[row / G] : 0ull;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < CD; ++k) o[i][k] = 0.f;
+        }
+        for (int tile = first; live && tile < last; ++tile) {
+            const int t0 = tile * kBN;
+            if (tile != first) __syncthreads();
+            for (int idx = t; idx < kBN * (D / 4); idx += kThreads) {
+                const int j = idx / (D / 4), c = 4 * (idx - j * (D / 4)), pos = t0 + j;
+                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
+                bool on = false;
+                if (pos < n) {
+                    const int pg = pos / a.page_size, id = a.block_table[(size_t)b * a.table_cols + pg];
+                    on = id >= 0 && id < a.num_pages;
+                    if (on) {
+                        const size_t off = ((size_t)(pos - pg * a.page_size) * a.kv_heads + hk) * D + c;
+                        k4 = load4(static_cast<const Tin*>(a.k_cache) + (size_t)id * a.k_page_stride + off);
+                        v4 = load4(static_cast<const Tin*>(a.v_cache) + (size_t)id * a.v_page_stride + off);
+                    } else {
+                        bad_page = true;
+                    }
+                }
+                if (c == 0) s_on[j] = on;
+                *reinterpret_cast<float4*>(sk + j * LD + c) = k4;
+                *reinterpret_cast<float4*>(sv + j * LD + c) = v4;
+            }
+            __syncthreads();
+            float s[TM][4] = {};
+            for (int c = 0; c < D; c += 4) {
+                float4 k4[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + c);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(sq + (ty * TM + i) * LD + c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[i][j] = fmaf(q4.x, k4[j].x, fmaf(q4.y, k4[j].y, fmaf(q4.z, k4[j].z, fmaf(q4.w, k4[j].w, s[i][j]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int pos = t0 + tx + 16 * j, node = pos - ctx;
+                    const bool on = s_on[tx + 16 * j] && see[i] != 0 && (node < 0 || (see[i] >> node & 1));
+                    s[i][j] = on ? s[i][j] * sc : -INFINITY;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float nm = fmaxf(m[i], top), base = nm == -INFINITY ? 0.f : nm;
+                const float f = exp2f(m[i] - base);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(s[i][j] - base);
+                    sum += p;
+                    sp[(ty * TM + i) * LP + tx + 16 * j] = p;
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[i] = l[i] * f + sum;
+                m[i] = nm;
+#pragma unroll
+                for (int k = 0; k < CD; ++k) o[i][k] *= f;
+            }
+            __syncwarp();             // a row's weights are written and read by the same half warp
+            const bool nodes_here = t0 + kBN > ctx;
+            for (int j = 0; j < kBN; ++j) {
+                float v[CD];
+#pragma unroll
+                for (int k = 0; k < CD; k += 4) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(sv + j * LD + tx * 4 + 16 * k);
+                    v[k] = v4.x; v[k + 1] = v4.y; v[k + 2] = v4.z; v[k + 3] = v4.w;
+                }
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const float p = sp[(ty * TM + i) * LP + j];
+                    if (nodes_here && p == 0.f) continue;
+#pragma unroll
+                    for (int k = 0; k < CD; ++k) o[i][k] = fmaf(p, v[k], o[i][k]);
+                }
+            }
+        }
+        // the unit is done here, or its part goes to the workspace
+        const bool whole = us >= lo && ue <= hi;
+        float* ws = static_cast<float*>(a.workspace) + attn::slot_floats(BM, D) * (2 * (size_t)blockIdx.x + (us < lo ? 0 : 1));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = ty * TM + i, row = r0 + r;
+            if (row >= R) continue;
+            if (whole) {
+                Tin* dst = static_cast<Tin*>(a.out) + (((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D;
+                const float inv = 1.f / l[i];
+#pragma unroll
+                for (int k = 0; k < CD; ++k) put(dst + tx * 4 + 16 * (k & ~3) + (k & 3), l[i] == 0.f ? 0.f : o[i][k] * inv);
+            } else {
+                if (tx == 0) { ws[r] = m[i]; ws[BM + r] = l[i]; }
+#pragma unroll
+                for (int k = 0; k < CD; ++k) ws[2 * BM + (size_t)r * D + tx * 4 + 16 * (k & ~3) + (k & 3)] = o[i][k];
+            }
+        }
+        at = us + last;
+    }
+    if (bad_page) report_status(a.status, kDevBadSeqlens);
+}
+
+constexpr int kSimtCtas = 304;        // two to an SM
+
+template <int D, int TM>
+constexpr size_t simt_smem() { return (size_t)(16 * TM * (D + 4) + 2 * kBN * (D + 4) + 16 * TM * (kBN + 4)) * 4; }
+
+template <typename Tin, int D, int TM>
+cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
+{
+    const attn::Shape sh = {16 * TM, kBN, kSimtCtas};
+    constexpr size_t smem = simt_smem<D, TM>();
+    cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<Tin, D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    tree_attn_simt_kernel<Tin, D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attn::join_kernel<Tin, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
+    return cudaGetLastError();
+}
+
+// rows of a unit: 16 while the whole (sequence, head) fits them (the other rows of a larger
+// block would be computed for nothing), 64 otherwise (each loaded tile serves four times the rows)
+bool small_rows(int nodes, int group) { return nodes * group <= 16; }
+
+template <typename Tin>
+cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
+{
+    const bool small = small_rows(a.nodes, a.heads / a.kv_heads);
+    if (a.dim == 128) return small ? launch_simt<Tin, 128, 1>(a, stream) : launch_simt<Tin, 128, 4>(a, stream);
+    return small ? launch_simt<Tin, 64, 1>(a, stream) : launch_simt<Tin, 64, 4>(a, stream);
+}
+
+}  // namespace
+
+size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16)
+{
+    const int BM = small_rows(nodes, heads / kv_heads) ? 16 : 64;
+    return attn::slot_floats(BM, dim) * 2 * kSimtCtas * sizeof(float);
+}
+
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream)
+{
+    return a.bf16 ? launch_simt_dim<__nv_bfloat16>(a, stream) : launch_simt_dim<float>(a, stream);
+}
+
+}  // namespace kda
