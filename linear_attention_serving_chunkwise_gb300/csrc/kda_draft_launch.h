@@ -68,7 +68,10 @@ cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_decode(const TreeDecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t stream);
+// bf16 on the tensor cores (kda_tree_attn_tc.cu), fp32 on the CUDA cores
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream);
+size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim);
 size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16);
 
 }  // namespace kda

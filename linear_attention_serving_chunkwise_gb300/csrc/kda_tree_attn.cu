@@ -1,5 +1,5 @@
-// Softmax attention of a draft tree's tokens over a paged key/value cache, on the CUDA cores
-// (fp32 throughout): node i of sequence b attends to the sequence's context_lens[b] cached
+// Softmax attention of a draft tree's tokens over a paged fp32 key/value cache, on the
+// CUDA cores (fp32 throughout; bf16 runs in kda_tree_attn_tc.cu): node i of sequence b attends to the sequence's context_lens[b] cached
 // tokens and to the nodes on its own path, whose keys and values lie in the cache at the
 // logical positions context + j.  One pass over the tokens with the running maximum and sum
 // of the softmax; query heads of one group share each loaded tile.
@@ -15,11 +15,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBN = 64;
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
 // TM rows and 4 tokens (then D / 16 channels) per thread of a 16 x 16 grid
-template <typename Tin, int D, int TM>
+template <int D, int TM>
 __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a, attn::Shape sh)
 {
     constexpr int BM = 16 * TM, CD = D / 16, LD = D + 4, LP = kBN + 4;
@@ -29,40 +26,20 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
     float* sv = sk + kBN * LD;        // [BN][LD]
     float* sp = sv + kBN * LD;        // [BM][LP]
     __shared__ TreeSmem ts;
-    __shared__ long long s_total, s_start;
-    __shared__ int s_seq;
     __shared__ unsigned char s_on[kBN];   // the tile's tokens that exist
 
     const int t = threadIdx.x, lane = t & 31, ty = t >> 4, tx = t & 15;
-    const int G = a.heads / a.kv_heads, rb = attn::row_blocks(a, BM), per_seq = rb * a.kv_heads, R = a.nodes * G;
+    const int G = a.heads / a.kv_heads, R = a.nodes * G;
     const float sc = a.scale * 1.4426950408889634f;     // scores in powers of two
 
-    if (t < 32) {
-        const long long T = attn::line_total(a, kBN, per_seq, lane);
-        int seq;
-        long long start;
-        attn::line_find(a, kBN, per_seq, attn::line_start(T, blockIdx.x, sh.ctas), lane, seq, start);
-        if (lane == 0) { s_total = T; s_seq = seq; s_start = start; }
-    }
-    __syncthreads();
-    const long long T = s_total, lo = attn::line_start(T, blockIdx.x, sh.ctas), hi = attn::line_start(T, blockIdx.x + 1, sh.ctas);
-    int b = s_seq, masks_of = -1;
-    long long b0 = s_start;
+    attn::Line line;
+    line.begin(a, sh, blockIdx.x, lane);
+    attn::Piece pc;
+    int masks_of = -1;
     bool bad_page = false;
 
-    for (long long at = lo; at < hi;) {
-        int tiles = attn::seq_tiles(a, b, kBN);
-        while (at >= b0 + (long long)tiles * per_seq) {
-            b0 += (long long)tiles * per_seq;
-            ++b;
-            tiles = attn::seq_tiles(a, b, kBN);
-        }
-        const int u = (int)((at - b0) / tiles);
-        const long long us = b0 + (long long)u * tiles, ue = us + tiles;
-        const int first = (int)(at - us), last = (int)(min(hi, ue) - us);
-        const int hk = u / rb, r0 = (u % rb) * BM;
-        bool ok;
-        const int n = attn::seq_tokens(a, b, ok), ctx = n - a.nodes;
+    while (line.next(a, sh, blockIdx.x, pc)) {
+        const int b = pc.b, hk = pc.hk, r0 = pc.r0, n = pc.n, ctx = pc.ctx;
 
         __syncthreads();              // the last unit's reads of shared memory are done
         if (masks_of != b) {
@@ -71,10 +48,10 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
         }
         for (int idx = t; idx < BM * D; idx += kThreads) {
             const int r = idx / D, c = idx - r * D, row = r0 + r;
-            sq[r * LD + c] = row < R ? to_f32(static_cast<const Tin*>(a.q)[(((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D + c]) : 0.f;
+            sq[r * LD + c] = row < R ? (static_cast<const float*>(a.q)[(((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D + c]) : 0.f;
         }
         __syncthreads();
-        const bool live = ok && ts.ok;
+        const bool live = pc.seq_ok && ts.ok;
         if (!live && t == 0) report_status(a.status, kDevBadSeqlens);
 
         float m[TM], l[TM], o[TM][CD];
@@ -88,9 +65,9 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
 #pragma unroll
             for (int k = 0; k < CD; ++k) o[i][k] = 0.f;
         }
-        for (int tile = first; live && tile < last; ++tile) {
+        for (int tile = pc.first; live && tile < pc.last; ++tile) {
             const int t0 = tile * kBN;
-            if (tile != first) __syncthreads();
+            if (tile != pc.first) __syncthreads();
             for (int idx = t; idx < kBN * (D / 4); idx += kThreads) {
                 const int j = idx / (D / 4), c = 4 * (idx - j * (D / 4)), pos = t0 + j;
                 float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
@@ -100,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
                     on = id >= 0 && id < a.num_pages;
                     if (on) {
                         const size_t off = ((size_t)(pos - pg * a.page_size) * a.kv_heads + hk) * D + c;
-                        k4 = load4(static_cast<const Tin*>(a.k_cache) + (size_t)id * a.k_page_stride + off);
-                        v4 = load4(static_cast<const Tin*>(a.v_cache) + (size_t)id * a.v_page_stride + off);
+                        k4 = load4(static_cast<const float*>(a.k_cache) + (size_t)id * a.k_page_stride + off);
+                        v4 = load4(static_cast<const float*>(a.v_cache) + (size_t)id * a.v_page_stride + off);
                     } else {
                         bad_page = true;
                     }
@@ -171,24 +148,22 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
             }
         }
         // the unit is done here, or its part goes to the workspace
-        const bool whole = us >= lo && ue <= hi;
-        float* ws = static_cast<float*>(a.workspace) + attn::slot_floats(BM, D) * (2 * (size_t)blockIdx.x + (us < lo ? 0 : 1));
+        float* ws = static_cast<float*>(a.workspace) + attn::slot_floats(BM, D) * (size_t)pc.slot;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = ty * TM + i, row = r0 + r;
             if (row >= R) continue;
-            if (whole) {
-                Tin* dst = static_cast<Tin*>(a.out) + (((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D;
+            if (pc.whole) {
+                float* dst = static_cast<float*>(a.out) + (((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D;
                 const float inv = 1.f / l[i];
 #pragma unroll
-                for (int k = 0; k < CD; ++k) put(dst + tx * 4 + 16 * (k & ~3) + (k & 3), l[i] == 0.f ? 0.f : o[i][k] * inv);
+                for (int k = 0; k < CD; ++k) dst[tx * 4 + 16 * (k & ~3) + (k & 3)] = l[i] == 0.f ? 0.f : o[i][k] * inv;
             } else {
                 if (tx == 0) { ws[r] = m[i]; ws[BM + r] = l[i]; }
 #pragma unroll
                 for (int k = 0; k < CD; ++k) ws[2 * BM + (size_t)r * D + tx * 4 + 16 * (k & ~3) + (k & 3)] = o[i][k];
             }
         }
-        at = us + last;
     }
     if (bad_page) report_status(a.status, kDevBadSeqlens);
 }
@@ -198,16 +173,16 @@ constexpr int kSimtCtas = 304;        // two to an SM
 template <int D, int TM>
 constexpr size_t simt_smem() { return (size_t)(16 * TM * (D + 4) + 2 * kBN * (D + 4) + 16 * TM * (kBN + 4)) * 4; }
 
-template <typename Tin, int D, int TM>
+template <int D, int TM>
 cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 {
     const attn::Shape sh = {16 * TM, kBN, kSimtCtas};
     constexpr size_t smem = simt_smem<D, TM>();
-    cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<Tin, D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    tree_attn_simt_kernel<Tin, D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
+    tree_attn_simt_kernel<D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn::join_kernel<Tin, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
+    attn::join_kernel<float, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
     return cudaGetLastError();
 }
 
@@ -215,25 +190,25 @@ cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 // block would be computed for nothing), 64 otherwise (each loaded tile serves four times the rows)
 bool small_rows(int nodes, int group) { return nodes * group <= 16; }
 
-template <typename Tin>
 cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
 {
     const bool small = small_rows(a.nodes, a.heads / a.kv_heads);
-    if (a.dim == 128) return small ? launch_simt<Tin, 128, 1>(a, stream) : launch_simt<Tin, 128, 4>(a, stream);
-    return small ? launch_simt<Tin, 64, 1>(a, stream) : launch_simt<Tin, 64, 4>(a, stream);
+    if (a.dim == 128) return small ? launch_simt<128, 1>(a, stream) : launch_simt<128, 4>(a, stream);
+    return small ? launch_simt<64, 1>(a, stream) : launch_simt<64, 4>(a, stream);
 }
 
 }  // namespace
 
 size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16)
 {
+    if (bf16) return tree_attn_tc_workspace_bytes(nodes, heads / kv_heads, dim);
     const int BM = small_rows(nodes, heads / kv_heads) ? 16 : 64;
     return attn::slot_floats(BM, dim) * 2 * kSimtCtas * sizeof(float);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream)
 {
-    return a.bf16 ? launch_simt_dim<__nv_bfloat16>(a, stream) : launch_simt_dim<float>(a, stream);
+    return a.bf16 ? launch_tree_attn_tc(a, stream) : launch_simt_dim(a, stream);
 }
 
 }  // namespace kda

@@ -85,6 +85,53 @@ __device__ __forceinline__ void line_find(const TreeAttnArgs& a, int BN, int per
     start = base;
 }
 
+// A CTA's part of one unit: tiles [first, last) of the unit's tiles.
+struct Piece {
+    int b, hk, r0;          // sequence, cache head, first query row
+    int first, last;
+    int n, ctx;             // tokens of the sequence (0: skipped) and how many of them are context
+    bool seq_ok, whole;     // whole: the unit lies within this CTA's range
+    int slot;               // workspace slot of the part, when not whole
+};
+
+// Walks a CTA's range piece by piece.  begin() needs a full warp; next() any thread.
+struct Line {
+    long long hi, lo, at, b0;
+    int b, per_seq, rb;
+
+    __device__ __forceinline__ void begin(const TreeAttnArgs& a, const Shape& sh, int cta, int lane)
+    {
+        rb = row_blocks(a, sh.BM);
+        per_seq = rb * a.kv_heads;
+        const long long T = line_total(a, sh.BN, per_seq, lane);
+        lo = at = line_start(T, cta, sh.ctas);
+        hi = line_start(T, cta + 1, sh.ctas);
+        line_find(a, sh.BN, per_seq, lo, lane, b, b0);
+    }
+    __device__ __forceinline__ bool next(const TreeAttnArgs& a, const Shape& sh, int cta, Piece& p)
+    {
+        if (at >= hi) return false;
+        long long tiles = seq_tiles(a, b, sh.BN);
+        while (at >= b0 + tiles * per_seq) {
+            b0 += tiles * per_seq;
+            tiles = seq_tiles(a, ++b, sh.BN);
+        }
+        const int u = (int)((at - b0) / tiles);
+        const long long us = b0 + u * tiles, ue = us + tiles;
+        p.b = b;
+        p.hk = u / rb;
+        p.r0 = (u % rb) * sh.BM;
+        p.first = (int)(at - us);
+        p.last = (int)(min(hi, ue) - us);
+        p.n = seq_tokens(a, b, p.seq_ok);
+        p.ctx = p.n - a.nodes;
+        p.whole = us >= lo && ue <= hi;
+        p.slot = 2 * cta + (us < lo ? 0 : 1);
+        at = us + p.last;
+        return true;
+    }
+};
+
 // workspace: for each of 2 * ctas slots, BM maxima, BM sums, then BM x D outputs
 __host__ __device__ __forceinline__ size_t slot_floats(int BM, int D) { return (size_t)BM * (D + 2); }
 
