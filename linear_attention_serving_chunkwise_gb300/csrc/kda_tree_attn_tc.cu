@@ -3,8 +3,8 @@
 // over the tokens, running maximum and sum per row, parts of split units joined afterwards.
 //
 // The query rows of a (sequence, cache head) -- K nodes x G heads -- fill the 128 lanes of an
-// accumulator: S = Q K^T per tile of 128 tokens, the weights overwrite S in tensor memory as
-// the bf16 A operand of O += P V, and O stays in tensor memory for the whole piece.  Two
+// accumulator: S = Q K^T per tile of 128 tokens, the weights overwrite half of S in tensor
+// memory as the bf16 A operand of O += P V, and O stays in tensor memory for the whole piece.  Two
 // streams of S and O share the tensor core, so that one stream's softmax runs under the
 // other's products:
 //     up to 128 rows   the streams take the tiles in turn over the same rows, and their two
@@ -14,8 +14,13 @@
 // (until then the weights are at most 2^8, which bf16 and the fp32 sums hold as well).
 //
 // Warps 0-3 and 4-7: softmax and epilogue of stream 0 and 1, a row to a thread.  Warps 8-11:
-// the cache rows, gathered page by page with 16-byte asynchronous copies into a ring of K
-// and V tiles (any page size: the copies need no box).  Warp 12 issues the products, warp 13 copies Q.
+// the cache rows, into a ring of K and V tiles.  Warp 12 issues the products, warp 13 copies Q
+// (14 and 15 only complete the warpgroup that gives its registers to the softmax).
+//
+// The cache rows come by TMA where the page size is a multiple of 8: a tile is a stack of boxes
+// of 8 to 128 rows (the largest power of two in the page size), and 8 rows are one swizzle
+// atom, so boxes of any pages stack into the tile the products read.  Other page sizes are
+// gathered with 16-byte asynchronous copies, a row to half a warp.
 // Every wait is bounded; a thread that gave up goes through the rest of its schedule without
 // waiting and without touching the tensor core, and the status word says so.
 //
@@ -23,6 +28,11 @@
 // of range are zero in shared memory.  A draft node's values may be seen by some rows only, so
 // non-finite ones are replaced by zero in the tile and added back in the epilogue of the
 // rows that see the node (a positive weight times infinity or NaN is itself).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "kda_sm100.cuh"
 #include "kda_tree_attn.cuh"
 
@@ -32,7 +42,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kBN = 128;
-constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmaxThreads + kProducerThreads + 64;
+constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmaxThreads + kProducerThreads + 128;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // a thread; 512 threads start with 128 each
+static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
 constexpr int kCtas = 152;                          // one to an SM
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -52,12 +64,17 @@ struct Layout {
     static constexpr int kTile = kBN * D * 2;                   // bytes of a K or V tile, and of 128 rows of Q
     static constexpr int kQ = kTile * (kWide ? 2 : 1);
     static constexpr int kSlots = D == 128 ? 5 : 10;            // ring: K and V tiles in turn
-    static constexpr int kLag = kSlots - 2;                     // copies in flight before the oldest is waited for
+    static constexpr int kLag = kSlots - 2;                     // gathered: slots in flight before the oldest is waited for
     static constexpr int kStats = kQ + kSlots * kTile;          // both streams' maxima and sums (streams in turn)
     static constexpr int kShared = kStats + (kWide ? 0 : 2 * 2 * 128 * 4);
     static constexpr int kBytes = kShared + (int)sizeof(Shared);
     static constexpr uint32_t kColS = 0, kColO = 256;           // stream w: S at 128 w, O at 256 + D w
     static_assert(kBytes <= 232448, "shared memory");
+};
+
+struct Maps {
+    CUtensorMap k, v;       // [pages][page_size][kv_heads][D], boxes of box_rows x 64 channels
+    int box_rows;
 };
 
 struct Waiter {
@@ -96,12 +113,145 @@ __device__ __forceinline__ float ex2(float x)
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7f80u) != 0x7f80u; }
 
 // ------------------------------------------------------------------ the cache rows
+// Where a tile's tokens lie: lane l of producer warp w has token 32 w + l.
+struct Rows {
+    size_t koff, voff;      // elements from the caches' starts
+    unsigned exists, lost;  // of the warp's 32 tokens: on a page; without one although the sequence has them
+};
+
+__device__ __forceinline__ Rows rows_of(const TreeAttnArgs& a, const attn::Piece& pc, int pos, int id, size_t row_stride, int D)
+{
+    const bool there = id >= 0 && id < a.num_pages;
+    const size_t in_page = (size_t)(pos % a.page_size) * row_stride + (size_t)pc.hk * D;
+    Rows r;
+    r.lost = __ballot_sync(0xffffffffu, !there && pos < pc.n);
+    r.exists = __ballot_sync(0xffffffffu, there);
+    r.koff = there ? (size_t)id * a.k_page_stride + in_page : 0;
+    r.voff = there ? (size_t)id * a.v_page_stride + in_page : 0;
+    return r;
+}
+
+// The warp's 32 rows of a tile through registers; rows that do not exist become zero.  From
+// token `clean` of the tile on, non-finite values become zero too and their nodes are noted.
+template <int D>
+__device__ __forceinline__ void copy_rows(uint8_t* dst, const __nv_bfloat16* src, size_t off, unsigned exists, int w, int lane,
+                                          int clean, uint64_t* bad_nodes)
+{
+    constexpr int CH = D / 8, RPI = 32 / CH;        // 16-byte chunks of a row; rows a warp copies at once
+    const int sub = lane / CH, chunk = lane % CH;
+    uint32_t bad = 0;
+    for (int i0 = 0; i0 < 32; i0 += 8 * RPI) {
+        uint4 x[8];                                 // eight loads in flight
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = i0 + k * RPI + sub;
+            const size_t o = __shfl_sync(0xffffffffu, off, r);
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (exists >> r & 1) x[k] = *(reinterpret_cast<const uint4*>(src + o) + chunk);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = i0 + k * RPI + sub;
+            if (32 * w + r >= clean) {
+                uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool lo = finite_bf16(h[e]), hi = finite_bf16(h[e] >> 16);
+                    if (!(lo && hi)) bad |= 1u << r;
+                    h[e] = (lo ? h[e] & 0xffffu : 0u) | (hi ? h[e] & 0xffff0000u : 0u);
+                }
+                x[k] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            *reinterpret_cast<uint4*>(dst + sw128_chunk(32 * w + r, chunk, 128)) = x[k];
+        }
+    }
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (bad && lane == 0) {
+        for (int r = 0; r < 32; ++r)
+            if (bad >> r & 1) atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (32 * w + r - clean));
+    }
+}
+
+// By TMA.  Warp 0 of the four issues the boxes, a lane to a box.  Tiles with draft nodes (their
+// values) or with tokens that have no page pass through registers, by all four warps.
 template <int D, bool kWide>
-__device__ __forceinline__ void produce(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t)
+__device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn::Shape& sh, const Maps& maps, Shared& sm, uint8_t* base, int t)
 {
     using L = Layout<D, kWide>;
-    constexpr int CH = D / 8;                       // 16-byte chunks of a row
-    constexpr int RPI = 32 / CH;                    // rows a warp copies at once
+    const int lane = t & 31, w = t >> 5, box = maps.box_rows;
+    const size_t row_stride = (size_t)a.kv_heads * D;
+    Waiter wait{a.status};
+    attn::Line line;
+    line.begin(a, sh, blockIdx.x, lane);
+    attn::Piece pc;
+    uint32_t fill = 0;
+    bool bad_page = false;
+    for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
+        const int32_t* table = a.block_table + (size_t)pc.b * a.table_cols;
+        auto look_up = [&](int tile) {              // box `lane` of the tile
+            const int pos = tile * kBN + lane * box;
+            return tile < pc.last && lane * box < kBN && pos < pc.n ? __ldg(table + pos / a.page_size) : -1;
+        };
+        int next = look_up(pc.first);
+        for (int tile = pc.first; tile < pc.last; ++tile) {
+            const int t0 = tile * kBN, pos = t0 + lane * box, id = next;
+            const bool wanted = lane * box < kBN && pos < pc.n, there = wanted && id >= 0 && id < a.num_pages;
+            const bool lost = __any_sync(0xffffffffu, wanted && !there);
+            const int boxes = __popc(__ballot_sync(0xffffffffu, there));
+            next = look_up(tile + 1);
+            const bool slow[2] = {lost, lost || t0 + kBN > pc.ctx};
+            Rows rows = {};
+            if (slow[1]) {
+                const int p = t0 + 32 * w + lane;
+                rows = rows_of(a, pc, p, p < pc.n ? __ldg(table + p / a.page_size) : -1, row_stride, D);
+                bad_page |= rows.lost != 0;
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++fill) {
+                const uint32_t s = fill % L::kSlots;
+                uint8_t* dst = base + L::kQ + s * L::kTile;
+                if (w == 0 && fill >= (uint32_t)L::kSlots) wait(&sm.kv_empty[s], (fill / L::kSlots - 1) & 1);
+                if (!slow[kv]) {
+                    if (w != 0) continue;
+                    const bool go = __all_sync(0xffffffffu, wait.alive);
+                    if (kv == 0 && lane < 4) sm.missing[fill / 2 & 7][lane] = 0;
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (go) mbar_arrive_expect_tx(&sm.kv_full[s], boxes * box * D * 2);
+                        else mbar_arrive(&sm.kv_full[s]);
+                    }
+                    __syncwarp();
+                    if (go && there) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 64)
+                            tma_load_4d(dst + (c / 64) * (kBN * 128) + lane * box * 128, kv ? &maps.v : &maps.k, &sm.kv_full[s], c, pc.hk,
+                                        pos % a.page_size, id);
+                    }
+                    continue;
+                }
+                bar_sync(2, kProducerThreads);      // the slot is free
+                if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = rows.lost;
+                copy_rows<D>(dst, static_cast<const __nv_bfloat16*>(kv ? a.v_cache : a.k_cache), kv ? rows.voff : rows.koff, rows.exists, w, lane,
+                             kv ? max(0, pc.ctx - t0) : kBN, &sm.bad_nodes[piece & 7]);
+                fence_proxy_async_smem();
+                bar_sync(2, kProducerThreads);
+                if (t == 0) mbar_arrive(&sm.kv_full[s]);
+            }
+        }
+    }
+    // no load is in flight when the block ends, whatever became of its reader
+    if (w == 0)
+        for (uint32_t i = fill > (uint32_t)L::kSlots ? fill - L::kSlots : 0; i < fill; ++i)
+            mbar_wait_bounded(&sm.kv_full[i % L::kSlots], (i / L::kSlots) & 1, kWaitNs);
+    if (bad_page && lane == 0) report_status(a.status, kDevBadSeqlens);
+}
+
+// By 16-byte asynchronous copies, all four warps.
+template <int D, bool kWide>
+__device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t)
+{
+    using L = Layout<D, kWide>;
+    constexpr int CH = D / 8, RPI = 32 / CH;
     const int lane = t & 31, w = t >> 5;
     // (a cache without pages may be a null pointer: copies of no bytes then start at q)
     const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.num_pages ? a.k_cache : a.q);
@@ -120,85 +270,42 @@ __device__ __forceinline__ void produce(const TreeAttnArgs& a, const attn::Shape
         mbar_arrive(&sm.kv_full[sent % L::kSlots]);
         ++sent;
     };
-    // one slot's copies are issued: hand over the one kLag before it
-    auto filled = [&]() {
-        cp_commit();
-        ++fill;
-        if (fill - sent > L::kLag) {
-            cp_wait<L::kLag>();
-            hand_over();
-        }
-    };
-
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         const int32_t* table = a.block_table + (size_t)pc.b * a.table_cols;
-        // lane l of warp w looks up token 32 w + l of a tile, one tile ahead
-        auto look_up = [&](int tile) {
+        auto look_up = [&](int tile) {              // one tile ahead
             const int pos = tile * kBN + 32 * w + lane;
             return tile < pc.last && pos < pc.n ? __ldg(table + pos / a.page_size) : -1;
         };
         int id = look_up(pc.first);
         for (int tile = pc.first; tile < pc.last; ++tile) {
-            const int t0 = tile * kBN, pos = t0 + 32 * w + lane;
-            const bool there = id >= 0 && id < a.num_pages;
-            const unsigned lost = __ballot_sync(0xffffffffu, !there && pos < pc.n);
-            bad_page |= lost != 0;
-            const size_t in_page = (size_t)(pos % a.page_size) * row_stride + (size_t)pc.hk * D;
-            const size_t koff = there ? (size_t)id * a.k_page_stride + in_page : 0;
-            const size_t voff = there ? (size_t)id * a.v_page_stride + in_page : 0;
-            const unsigned exists = __ballot_sync(0xffffffffu, there);
+            const int t0 = tile * kBN;
+            const Rows rows = rows_of(a, pc, t0 + 32 * w + lane, id, row_stride, D);
+            bad_page |= rows.lost != 0;
             id = look_up(tile + 1);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 const uint32_t s = fill % L::kSlots;
                 if (fill >= (uint32_t)L::kSlots) wait(&sm.kv_empty[s], (fill / L::kSlots - 1) & 1);
                 uint8_t* dst = base + L::kQ + s * L::kTile;
-                if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = lost;
+                if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = rows.lost;
                 const __nv_bfloat16* src = kv ? vc : kc;
-                const size_t off = kv ? voff : koff;
+                const size_t off = kv ? rows.voff : rows.koff;
                 if (kv == 1 && t0 + kBN > pc.ctx) {
-                    // draft nodes in the tile: their values pass through registers
-                    uint32_t bad = 0;               // of this warp's 32 tokens
-                    for (int i0 = 0; i0 < 32; i0 += 8 * RPI) {
-                        uint4 x[8];                 // eight loads in flight
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = i0 + k * RPI + sub;
-                            const size_t o = __shfl_sync(0xffffffffu, off, r);
-                            x[k] = make_uint4(0, 0, 0, 0);
-                            if (exists >> r & 1) x[k] = *(reinterpret_cast<const uint4*>(src + o) + chunk);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = i0 + k * RPI + sub;
-                            if (t0 + 32 * w + r >= pc.ctx) {
-                                uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const bool lo = finite_bf16(h[e]), hi = finite_bf16(h[e] >> 16);
-                                    if (!(lo && hi)) bad |= 1u << r;
-                                    h[e] = (lo ? h[e] & 0xffffu : 0u) | (hi ? h[e] & 0xffff0000u : 0u);
-                                }
-                                x[k] = make_uint4(h[0], h[1], h[2], h[3]);
-                            }
-                            *reinterpret_cast<uint4*>(dst + sw128_chunk(32 * w + r, chunk, 128)) = x[k];
-                        }
-                    }
-                    bad = __reduce_or_sync(0xffffffffu, bad);
-                    if (bad && lane == 0) {
-                        for (int r = 0; r < 32; ++r)
-                            if (bad >> r & 1)
-                                atomicOr(reinterpret_cast<unsigned long long*>(&sm.bad_nodes[piece & 7]), 1ull << (t0 + 32 * w + r - pc.ctx));
-                    }
+                    copy_rows<D>(dst, src, off, rows.exists, w, lane, max(0, pc.ctx - t0), &sm.bad_nodes[piece & 7]);
                 } else {
 #pragma unroll 4
                     for (int i = 0; i < 32; i += RPI) {
                         const int r = i + sub;
                         const size_t o = __shfl_sync(0xffffffffu, off, r);
-                        cp16(smem_u32(dst + sw128_chunk(32 * w + r, chunk, 128)), src + o + 8 * chunk, exists >> r & 1);
+                        cp16(smem_u32(dst + sw128_chunk(32 * w + r, chunk, 128)), src + o + 8 * chunk, rows.exists >> r & 1);
                     }
                 }
-                filled();
+                cp_commit();
+                ++fill;
+                if (fill - sent > L::kLag) {        // hand over the slot kLag before this one
+                    cp_wait<L::kLag>();
+                    hand_over();
+                }
             }
         }
     }
@@ -244,7 +351,6 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
     Waiter wait{a.status};
     attn::Line line;
     line.begin(a, sh, blockIdx.x, lane);
-    if (lane != 0) return;
     attn::Piece pc;
     const uint32_t tm = sm.tmem, q0 = smem_u32(base), ring = q0 + L::kQ;
     const uint32_t id_s = idesc_bf16_f32(128, kBN, 0, 0, a.scale < 0.f), id_o = idesc_bf16_f32(128, D, 0, 1);
@@ -259,7 +365,9 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             const uint32_t at = kv + 2 * tile, s = at % L::kSlots;
             if (!kWide || w == 0) wait(&sm.kv_full[s], (at / L::kSlots) & 1);
             tc_fence_after_sync();
-            if (wait.alive) {
+            const bool go = __all_sync(0xffffffffu, wait.alive);
+            if (!elect_one()) return;
+            if (go) {
                 const uint64_t qd = kmajor_base(q0 + (kWide ? w * L::kTile : 0)), kd = kmajor_base(ring + s * L::kTile);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
@@ -268,7 +376,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             if (!kWide || w == 1) umma_commit(&sm.kv_empty[s]);
             if (i == items - 1) umma_commit(&sm.q_empty);
             umma_commit(&sm.s_full[w]);
-        };
+        };                                          // (the whole warp walks the schedule, one lane issues)
         auto values = [&](int i) {
             const int w = i & 1, tile = kWide ? i >> 1 : i;
             const uint32_t at = kv + 2 * tile + 1, s = at % L::kSlots;
@@ -277,11 +385,13 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
             tc_fence_after_sync();
-            if (wait.alive) {
+            const bool go = __all_sync(0xffffffffu, wait.alive);
+            if (!elect_one()) return;
+            if (go) {
                 const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
 #pragma unroll
                 for (int ks = 0; ks < kBN / 16; ++ks)
-                    umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
+                    umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 64 + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
             }
             if (!kWide || w == 1) umma_commit(&sm.kv_empty[s]);
             if (i == items - 1) umma_commit(&sm.o_done);
@@ -352,22 +462,42 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                 const uint32_t* missing = sm.missing[(done + i) & 7];
                 const bool all = t0 + kBN <= pc.ctx && !(missing[0] | missing[1] | missing[2] | missing[3]);
                 tile_mask(see, t0, pc.ctx, missing, mw);
-                auto load = [&](int c, float (&x)[32]) {
-                    tmem_ld32(tS + 32 * c, x);
-                    tmem_wait_ld();
-                    if (!all) {
+                // The weights' place (columns 64-127) covers the scores of words 2 and 3, which
+                // stay in registers from the maximum on; words 0 and 1 are read a second time,
+                // under the work on the others: 96 registers of scores, not 128.
+                auto read = [&](int c, float (&x)[32]) { tmem_ld32(tS + 32 * c, x); };
+                auto mask = [&](int c, float (&x)[32]) {
+                    if (all) return;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = mw[c] >> k & 1 ? x[k] : -INFINITY;
-                    }
+                    for (int k = 0; k < 32; ++k) x[k] = mw[c] >> k & 1 ? x[k] : -INFINITY;
                 };
-                float top = -INFINITY;
+                auto max_of = [&](const float (&x)[32]) {
+                    float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[32];
-                    load(c, x);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) top = fmaxf(top, x[k]);
+                    for (int k = 0; k < 32; k += 4) {
+                        a0 = fmaxf(a0, fmaxf(x[k], x[k + 1]));
+                        a1 = fmaxf(a1, fmaxf(x[k + 2], x[k + 3]));
+                    }
+                    return fmaxf(a0, a1);
+                };
+                float x0[32], x2[32], x3[32], top;
+                {
+                    float x1[32];
+                    read(0, x0);
+                    read(1, x1);
+                    tmem_wait_ld();
+                    mask(0, x0);
+                    mask(1, x1);
+                    top = fmaxf(max_of(x0), max_of(x1));
                 }
+                read(2, x2);
+                read(3, x3);
+                read(0, x0);
+                tmem_wait_ld();
+                mask(2, x2);
+                mask(3, x3);
+                mask(0, x0);
+                top = fmaxf(top, fmaxf(max_of(x2), max_of(x3)));
                 const bool grow = (top - m) * sc > kGrow;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float nm = grow ? top : m;
@@ -389,10 +519,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                 // (x - m) sc in this order: the difference is exact where it matters, however large the scores
                 const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), sc2 = make_float2(sc, sc);
                 float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float x[32];
-                    load(c, x);
+                auto weigh = [&](int c, const float (&x)[32]) {
                     uint32_t p[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -401,8 +528,15 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                         sum = __fadd2_rn(sum, e);
                         p[k] = pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st16u(tS + 16 * c, p);
-                }
+                    tmem_st16u(tS + 64 + 16 * c, p);
+                };
+                weigh(2, x2);
+                read(1, x2);
+                weigh(0, x0);
+                weigh(3, x3);
+                tmem_wait_ld();
+                mask(1, x2);
+                weigh(1, x2);
                 l += sum.x + sum.y;
                 begun = true;
                 tmem_wait_st();
@@ -500,8 +634,8 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
     }
 }
 
-template <int D, bool kWide>
-__global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs a, attn::Shape sh)
+template <int D, bool kWide, bool kBoxes>
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs a, attn::Shape sh, const __grid_constant__ Maps maps)
 {
     using L = Layout<D, kWide>;
     extern __shared__ __align__(1024) uint8_t base[];   // all of it: the swizzled tiles start at 0
@@ -513,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     }
     if (t == 0) {
         for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(&sm.kv_full[i], kProducerThreads);
+            mbar_init(&sm.kv_full[i], kBoxes ? 1 : kProducerThreads);
             mbar_init(&sm.kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -530,10 +664,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp < 8) softmax<D, kWide>(a, sh, sm, base, t);
-    else if (warp < 12) produce<D, kWide>(a, sh, sm, base, t - kSoftmaxThreads);
-    else if (warp == 12) multiply<D, kWide>(a, sh, sm, base, t & 31);
-    else query<D, kWide>(a, sh, sm, base, t & 31);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax<D, kWide>(a, sh, sm, base, t);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < 12) {
+            if constexpr (kBoxes) produce_boxes<D, kWide>(a, sh, maps, sm, base, t - kSoftmaxThreads);
+            else produce_gather<D, kWide>(a, sh, sm, base, t - kSoftmaxThreads);
+        } else if (warp == 12) {
+            multiply<D, kWide>(a, sh, sm, base, t & 31);
+        } else if (warp == 13) {
+            query<D, kWide>(a, sh, sm, base, t & 31);
+        }
+    }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
@@ -543,16 +687,71 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
 
 bool wide_rows(int nodes, int group) { return nodes * group > 128; }
 
-template <int D, bool kWide>
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// Whether the cache can be read in boxes: see the top; a map holds strides below 2^40 bytes.
+bool in_boxes(const TreeAttnArgs& a)
+{
+    const size_t most = ((size_t)1 << 40) / 2 - 1;
+    return a.page_size % 8 == 0 && a.num_pages > 0 && a.k_page_stride <= most && a.v_page_stride <= most;
+}
+
+bool make_map(CUtensorMap* m, const void* cache, size_t page_stride, const TreeAttnArgs& a, int rows)
+{
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t D = (cuuint64_t)a.dim, H = (cuuint64_t)a.kv_heads;
+    const cuuint64_t dims[4] = {D, H, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {D * 2, H * D * 2, (cuuint64_t)page_stride * 2};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kWide, bool kBoxes>
 cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
 {
+    using L = Layout<D, kWide>;
+    const auto kernel = tree_attn_tc_kernel<D, kWide, kBoxes>;
     const attn::Shape sh = {kWide ? 256 : 128, kBN, kCtas};
-    cudaError_t e = cudaFuncSetAttribute(tree_attn_tc_kernel<D, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D, kWide>::kBytes);
+    Maps maps = {};
+    if (kBoxes) {
+        maps.box_rows = min(a.page_size & -a.page_size, kBN);
+        if (!make_map(&maps.k, a.k_cache, a.k_page_stride, a, maps.box_rows) || !make_map(&maps.v, a.v_cache, a.v_page_stride, a, maps.box_rows))
+            return cudaErrorInvalidValue;
+    }
+    // the register split needs the block to start with all 128 registers a thread
+    cudaFuncAttributes at;
+    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
     if (e != cudaSuccess) return e;
-    tree_attn_tc_kernel<D, kWide><<<sh.ctas, kThreads, Layout<D, kWide>::kBytes, stream>>>(a, sh);
+    if (at.numRegs != 128) return cudaErrorLaunchOutOfResources;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<sh.ctas, kThreads, L::kBytes, stream>>>(a, sh, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     attn::join_kernel<__nv_bfloat16, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_dim(const TreeAttnArgs& a, cudaStream_t stream)
+{
+    const bool wide = wide_rows(a.nodes, a.heads / a.kv_heads);
+    if (in_boxes(a)) return wide ? launch<D, true, true>(a, stream) : launch<D, false, true>(a, stream);
+    return wide ? launch<D, true, false>(a, stream) : launch<D, false, false>(a, stream);
 }
 
 }  // namespace
@@ -564,9 +763,7 @@ size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim)
 
 cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream)
 {
-    const bool wide = wide_rows(a.nodes, a.heads / a.kv_heads);
-    if (a.dim == 128) return wide ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
-    return wide ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
+    return a.dim == 128 ? launch_dim<128>(a, stream) : launch_dim<64>(a, stream);
 }
 
 }  // namespace kda
