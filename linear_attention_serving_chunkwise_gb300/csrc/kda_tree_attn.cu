@@ -35,11 +35,14 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
     attn::Line line;
     line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
+    attn::Recorder rec;
     int masks_of = -1;
     bool bad_page = false;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     while (line.next(a, sh, blockIdx.x, pc)) {
         const int b = pc.b, hk = pc.hk, r0 = pc.r0, n = pc.n, ctx = pc.ctx;
+        rec.see(pc);
 
         __syncthreads();              // the last unit's reads of shared memory are done
         if (masks_of != b) {
@@ -148,12 +151,12 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
             }
         }
         // the unit is done here, or its part goes to the workspace
-        float* ws = static_cast<float*>(a.workspace) + attn::slot_floats(BM, D) * (size_t)pc.slot;
+        float* ws = attn::slot_of(a, sh, D, pc.slot);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = ty * TM + i, row = r0 + r;
             if (row >= R) continue;
-            if (pc.whole) {
+            if (pc.whole()) {
                 float* dst = static_cast<float*>(a.out) + (((size_t)b * a.nodes + row / G) * a.heads + hk * G + row % G) * D;
                 const float inv = 1.f / l[i];
 #pragma unroll
@@ -161,10 +164,12 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
             } else {
                 if (tx == 0) { ws[r] = m[i]; ws[BM + r] = l[i]; }
 #pragma unroll
-                for (int k = 0; k < CD; ++k) ws[2 * BM + (size_t)r * D + tx * 4 + 16 * (k & ~3) + (k & 3)] = o[i][k];
+                for (int k = 0; k < CD; k += 4)
+                    attn::slot_out(ws, BM)[(size_t)(tx + 4 * k) * BM + r] = make_float4(o[i][k], o[i][k + 1], o[i][k + 2], o[i][k + 3]);
             }
         }
     }
+    if (t == 0) rec.leave(a, blockIdx.x);
     if (bad_page) report_status(a.status, kDevBadSeqlens);
 }
 
@@ -177,13 +182,13 @@ template <int D, int TM>
 cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 {
     const attn::Shape sh = {16 * TM, kBN, kSimtCtas};
+    if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     constexpr size_t smem = simt_smem<D, TM>();
     cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     tree_attn_simt_kernel<D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn::join_kernel<float, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
-    return cudaGetLastError();
+    return attn::launch_join<float, D>(a, sh, stream);
 }
 
 // rows of a unit: 16 while the whole (sequence, head) fits them (the other rows of a larger
@@ -203,7 +208,7 @@ size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, 
 {
     if (bf16) return tree_attn_tc_workspace_bytes(nodes, heads / kv_heads, dim);
     const int BM = small_rows(nodes, heads / kv_heads) ? 16 : 64;
-    return attn::slot_floats(BM, dim) * 2 * kSimtCtas * sizeof(float);
+    return attn::workspace_bytes({BM, kBN, kSimtCtas}, dim);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream)

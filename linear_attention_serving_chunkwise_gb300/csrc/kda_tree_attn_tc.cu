@@ -43,7 +43,7 @@ using namespace sm100;
 
 constexpr int kBN = 128;
 constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmaxThreads + kProducerThreads + 128;
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;  // a thread; 512 threads start with 128 each
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads start with 128 each
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
 constexpr int kCtas = 152;                          // one to an SM
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -53,7 +53,7 @@ constexpr float kGrow = 8.f;                        // powers of two a maximum m
 struct Shared {
     uint64_t kv_full[10], kv_empty[10], s_full[2], p_full[2], q_full, q_empty, o_done, o_free;
     uint64_t bad_nodes[8];                          // by piece: nodes with non-finite values
-    uint32_t missing[8][4];                         // by tile: its tokens without a page (a V tile is freed after its softmax, so the
+    alignas(16) uint32_t missing[8][4];                         // by tile: its tokens without a page (a V tile is freed after its softmax, so the
                                                     // copies are never more than 6 tiles past the one the softmax is at)
     TreeSmem tree;
     uint32_t tmem;
@@ -328,7 +328,9 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
     attn::Line line;
     line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
+    attn::Recorder rec;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
+        rec.see(pc);
         if (piece) wait(&sm.q_empty, (piece - 1) & 1);
         for (int idx = lane; idx < sh.BM * CH; idx += 32) {
             const int r = idx / CH, c = idx % CH, row = pc.r0 + r;
@@ -341,6 +343,7 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
         fence_proxy_async_smem();
         mbar_arrive(&sm.q_full);
     }
+    if (lane == 0) rec.leave(a, blockIdx.x);
 }
 
 // ------------------------------------------------------------------ the products
@@ -354,63 +357,74 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
     attn::Piece pc;
     const uint32_t tm = sm.tmem, q0 = smem_u32(base), ring = q0 + L::kQ;
     const uint32_t id_s = idesc_bf16_f32(128, kBN, 0, 0, a.scale < 0.f), id_o = idesc_bf16_f32(128, D, 0, 1);
-    uint32_t kv = 0, used[2] = {0, 0};              // ring position of the piece's first K tile; items of each stream so far
+    // ring slot and phase of the next K and V tile; items of each stream so far
+    uint32_t ks_ = 0, kp = 0, vs_ = 1, vp = 0, used[2] = {0, 0};
+    auto advance = [](uint32_t& s, uint32_t& phase) {
+        s += 2;
+        if (s >= (uint32_t)L::kSlots) { s -= L::kSlots; phase ^= 1; }
+    };
     uint32_t piece = 0;
     for (; line.next(a, sh, blockIdx.x, pc); ++piece) {
         const int tiles = pc.last - pc.first, items = kWide ? 2 * tiles : tiles;
         wait(&sm.q_full, piece & 1);
         // item i: stream i % 2; its tile is i (streams in turn) or i / 2 (each tile for both)
-        auto scores = [&](int i) {
-            const int w = i & 1, tile = kWide ? i >> 1 : i;
-            const uint32_t at = kv + 2 * tile, s = at % L::kSlots;
-            if (!kWide || w == 0) wait(&sm.kv_full[s], (at / L::kSlots) & 1);
+        auto scores = [&](int i, int w) {
+            const bool first = !kWide || w == 0, last = !kWide || w == 1;   // to use the tile
+            const uint32_t s = ks_;
+            if (first) wait(&sm.kv_full[s], kp);
+            if (last) advance(ks_, kp);
             tc_fence_after_sync();
-            const bool go = __all_sync(0xffffffffu, wait.alive);
-            if (!elect_one()) return;
-            if (go) {
-                const uint64_t qd = kmajor_base(q0 + (kWide ? w * L::kTile : 0)), kd = kmajor_base(ring + s * L::kTile);
+            if (elect_one()) {
+                if (wait.alive) {
+                    const uint64_t qd = kmajor_base(q0 + (kWide ? w * L::kTile : 0)), kd = kmajor_base(ring + s * L::kTile);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    umma_bf16(tm + L::kColS + 128 * w, desc_off(qd, kmajor_off(128, ks)), desc_off(kd, kmajor_off(128, ks)), id_s, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        umma_bf16(tm + L::kColS + 128 * w, desc_off(qd, kmajor_off(128, ks)), desc_off(kd, kmajor_off(128, ks)), id_s, ks > 0);
+                }
+                umma_commit(&sm.s_full[w]);
+                if (last) umma_commit(&sm.kv_empty[s]);
+                if (i == items - 1) umma_commit(&sm.q_empty);
             }
-            if (!kWide || w == 1) umma_commit(&sm.kv_empty[s]);
-            if (i == items - 1) umma_commit(&sm.q_empty);
-            umma_commit(&sm.s_full[w]);
-        };                                          // (the whole warp walks the schedule, one lane issues)
-        auto values = [&](int i) {
-            const int w = i & 1, tile = kWide ? i >> 1 : i;
-            const uint32_t at = kv + 2 * tile + 1, s = at % L::kSlots;
-            if (!kWide || w == 0) wait(&sm.kv_full[s], (at / L::kSlots) & 1);
+            __syncwarp();
+        };
+        auto values = [&](int i, int w) {
+            const bool first = !kWide || w == 0, last = !kWide || w == 1;
+            const uint32_t s = vs_;
+            if (first) wait(&sm.kv_full[s], vp);
+            if (last) advance(vs_, vp);
             if (i == 0 && piece) wait(&sm.o_free, (piece - 1) & 1);
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
             tc_fence_after_sync();
-            const bool go = __all_sync(0xffffffffu, wait.alive);
-            if (!elect_one()) return;
-            if (go) {
-                const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
+            if (elect_one()) {
+                if (wait.alive) {
+                    const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
 #pragma unroll
-                for (int ks = 0; ks < kBN / 16; ++ks)
-                    umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 64 + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
+                    for (int ks = 0; ks < kBN / 16; ++ks)
+                        umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
+                }
+                if (last) umma_commit(&sm.kv_empty[s]);
+                if (i == items - 1) umma_commit(&sm.o_done);
             }
-            if (!kWide || w == 1) umma_commit(&sm.kv_empty[s]);
-            if (i == items - 1) umma_commit(&sm.o_done);
+            __syncwarp();
         };
-        scores(0);
-        if (items > 1) scores(1);
-        for (int i = 0; i < items; ++i) {
-            values(i);
-            if (i + 2 < items) scores(i + 2);
+        scores(0, 0);
+        if (items > 1) scores(1, 1);
+        for (int i = 0; i < items; i += 2) {        // both streams in turn
+            values(i, 0);
+            if (i + 2 < items) scores(i + 2, 0);
+            if (i + 1 < items) values(i + 1, 1);
+            if (i + 3 < items) scores(i + 3, 1);
         }
-        kv += 2 * tiles;
     }
     if (piece) wait(&sm.o_done, (piece - 1) & 1);   // no product or commit is in flight after this
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
 // What row sees of the tile at t0: 128 bits, four words.
-__device__ __forceinline__ void tile_mask(uint64_t see, int t0, int ctx, const uint32_t* missing, uint32_t (&mw)[4])
+__device__ __forceinline__ void tile_mask(uint64_t see, int t0, int ctx, uint4 lost, uint32_t (&mw)[4])
 {
+    const uint32_t missing[4] = {lost.x, lost.y, lost.z, lost.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int at = t0 + 32 * k - ctx;           // node of the word's first token
@@ -422,6 +436,17 @@ __device__ __forceinline__ void tile_mask(uint64_t see, int t0, int ctx, const u
         }
         mw[k] = x & ~missing[k];
     }
+}
+
+__device__ __forceinline__ float max_of(const float (&x)[32])
+{
+    float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        a0 = fmaxf(a0, fmaxf(x[k], x[k + 1]));
+        a1 = fmaxf(a1, fmaxf(x[k + 2], x[k + 3]));
+    }
+    return fmaxf(a0, a1);
 }
 
 template <int D, bool kWide>
@@ -439,11 +464,14 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
     line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
     uint32_t used = 0, done = 0;                    // items of this stream, and tiles, so far
+    int masks_of = -1;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         const int tiles = pc.last - pc.first;
-        bar_sync(1, kSoftmaxThreads);               // everyone is done with the last piece's tree and statistics
-        if (warp == 0) tree_masks(sm.tree, a.parents + (size_t)pc.b * a.nodes, a.nodes, lane);
-        bar_sync(1, kSoftmaxThreads);
+        if (pc.b != masks_of) {                     // (everyone is done with the last piece's tree: the epilogue's barrier)
+            if (warp == 0) tree_masks(sm.tree, a.parents + (size_t)pc.b * a.nodes, a.nodes, lane);
+            masks_of = pc.b;
+            bar_sync(1, kSoftmaxThreads);
+        }
         if (!(pc.seq_ok && sm.tree.ok) && t == 0) report_status(a.status, kDevBadSeqlens);
         const int row = pc.r0 + (kWide ? 128 * w : 0) + r;
         const uint64_t see = pc.seq_ok && sm.tree.ok && row < R ? sm.tree.anc[row / G] : 0ull;
@@ -458,69 +486,11 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             __syncwarp();
             tc_fence_after_sync();
             if (busy) {
-                uint32_t mw[4];
-                const uint32_t* missing = sm.missing[(done + i) & 7];
-                const bool all = t0 + kBN <= pc.ctx && !(missing[0] | missing[1] | missing[2] | missing[3]);
-                tile_mask(see, t0, pc.ctx, missing, mw);
-                // The weights' place (columns 64-127) covers the scores of words 2 and 3, which
-                // stay in registers from the maximum on; words 0 and 1 are read a second time,
-                // under the work on the others: 96 registers of scores, not 128.
-                auto read = [&](int c, float (&x)[32]) { tmem_ld32(tS + 32 * c, x); };
-                auto mask = [&](int c, float (&x)[32]) {
-                    if (all) return;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = mw[c] >> k & 1 ? x[k] : -INFINITY;
-                };
-                auto max_of = [&](const float (&x)[32]) {
-                    float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        a0 = fmaxf(a0, fmaxf(x[k], x[k + 1]));
-                        a1 = fmaxf(a1, fmaxf(x[k + 2], x[k + 3]));
-                    }
-                    return fmaxf(a0, a1);
-                };
-                float x0[32], x2[32], x3[32], top;
-                {
-                    float x1[32];
-                    read(0, x0);
-                    read(1, x1);
-                    tmem_wait_ld();
-                    mask(0, x0);
-                    mask(1, x1);
-                    top = fmaxf(max_of(x0), max_of(x1));
-                }
-                read(2, x2);
-                read(3, x3);
-                read(0, x0);
-                tmem_wait_ld();
-                mask(2, x2);
-                mask(3, x3);
-                mask(0, x0);
-                top = fmaxf(top, fmaxf(max_of(x2), max_of(x3)));
-                const bool grow = (top - m) * sc > kGrow;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float nm = grow ? top : m;
-                    const float f = grow ? ex2((m - nm) * sc) : 1.f;   // 0 for the first maximum
-                    l *= f;
-                    m = nm;
-                    if (begun) {                    // the products of the stream's last tile are done: S is ready
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(tO + D * w + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= f;
-                            tmem_st32(tO + D * w + c, o);
-                        }
-                    }
-                }
+                const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
+                const bool all = t0 + kBN <= pc.ctx && !(missing.x | missing.y | missing.z | missing.w);
+                const float2 sc2 = make_float2(sc, sc);
                 // (x - m) sc in this order: the difference is exact where it matters, however large the scores
-                const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), sc2 = make_float2(sc, sc);
-                float2 sum = make_float2(0.f, 0.f);
-                auto weigh = [&](int c, const float (&x)[32]) {
-                    uint32_t p[16];
+                auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), off), sc2);
@@ -528,16 +498,84 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                         sum = __fadd2_rn(sum, e);
                         p[k] = pack_bf16x2(e.x, e.y);
                     }
-                    tmem_st16u(tS + 64 + 16 * c, p);
                 };
-                weigh(2, x2);
-                read(1, x2);
-                weigh(0, x0);
-                weigh(3, x3);
-                tmem_wait_ld();
-                mask(1, x2);
-                weigh(1, x2);
-                l += sum.x + sum.y;
+                bool stored = false;
+                if (all && begun) {
+                    // A tile that every row sees whole, after the first: the weights are formed from the
+                    // last maximum while the tile's own is still being found, and stored over the
+                    // scores once it is known that the maximum may stand (nearly always).
+                    const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+                    float2 sum = make_float2(0.f, 0.f);
+                    float top = -INFINITY;
+                    uint32_t p[4][16];
+                    float xa[32], xb[32];
+                    tmem_ld32(tS, xa);
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 32, xb);
+                    top = fmaxf(top, max_of(xa));
+                    weigh(xa, off, sum, p[0]);
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 64, xa);
+                    top = fmaxf(top, max_of(xb));
+                    weigh(xb, off, sum, p[1]);
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 96, xb);
+                    top = fmaxf(top, max_of(xa));
+                    weigh(xa, off, sum, p[2]);
+                    tmem_wait_ld();
+                    top = fmaxf(top, max_of(xb));
+                    weigh(xb, off, sum, p[3]);
+                    if (!__any_sync(0xffffffffu, (top - m) * sc > kGrow)) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
+                        l += sum.x + sum.y;
+                        stored = true;
+                    }
+                }
+                if (!stored) {
+                    // masks, the first maximum, or one that has grown: the maximum first, then the weights
+                    // (word c's go to columns 16 c, over scores that have been read)
+                    uint32_t mw[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (!all) tile_mask(see, t0, pc.ctx, missing, mw);
+                    auto read = [&](int c, float (&x)[32]) {
+                        const uint32_t on = c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3];
+                        tmem_ld32(tS + 32 * c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
+                    };
+                    float top = -INFINITY, x[32];
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        read(c, x);
+                        top = fmaxf(top, max_of(x));
+                    }
+                    const bool grow = (top - m) * sc > kGrow;
+                    const float nm = grow ? top : m;
+                    const float f = grow ? ex2((m - nm) * sc) : 1.f;   // 0 for the first maximum
+                    l *= f;
+                    m = nm;
+                    if (begun && __any_sync(0xffffffffu, grow)) {      // (S is ready: the stream's last products into O are done)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            tmem_ld32(tO + D * w + c, x);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] *= f;
+                            tmem_st32(tO + D * w + c, x);
+                        }
+                    }
+                    const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
+                        read(c, x);
+                        weigh(x, off, sum, p);
+                        tmem_st16u(tS + 16 * c, p);
+                    }
+                    l += sum.x + sum.y;
+                }
                 begun = true;
                 tmem_wait_st();
             }
@@ -571,10 +609,10 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * sc);
             l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
         }
-        const float norm = pc.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        float* ws = static_cast<float*>(a.workspace) + attn::slot_floats(sh.BM, D) * (size_t)pc.slot;
+        const float norm = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        float* ws = attn::slot_of(a, sh, D, pc.slot);
         const int rl = row - pc.r0;                 // row of the unit
-        if (row < R && !pc.whole && c0 == 0) {
+        if (row < R && !pc.whole() && c0 == 0) {
             ws[rl] = m == -INFINITY ? m : m * sc;
             ws[sh.BM + rl] = l;
         }
@@ -614,7 +652,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                     if (!isfinite(x)) o[k] += x;
                 }
             }
-            if (row < R && pc.whole) {
+            if (row < R && pc.whole()) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
                     *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(pack_bf16x2(o[k], o[k + 1]), pack_bf16x2(o[k + 2], o[k + 3]),
@@ -622,7 +660,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             } else if (row < R) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<float4*>(ws + 2 * sh.BM + (size_t)rl * D + c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    attn::slot_out(ws, sh.BM)[(size_t)((c + k) / 4) * sh.BM + rl] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
             __syncwarp();
         }
@@ -664,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax<D, kWide>(a, sh, sm, base, t);
@@ -717,7 +756,7 @@ bool make_map(CUtensorMap* m, const void* cache, size_t page_stride, const TreeA
     const cuuint64_t strides[3] = {D * 2, H * D * 2, (cuuint64_t)page_stride * 2};
     const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1}, es[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, a.dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -727,6 +766,7 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
     using L = Layout<D, kWide>;
     const auto kernel = tree_attn_tc_kernel<D, kWide, kBoxes>;
     const attn::Shape sh = {kWide ? 256 : 128, kBN, kCtas};
+    if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     Maps maps = {};
     if (kBoxes) {
         maps.box_rows = min(a.page_size & -a.page_size, kBN);
@@ -742,8 +782,7 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     kernel<<<sh.ctas, kThreads, L::kBytes, stream>>>(a, sh, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn::join_kernel<__nv_bfloat16, D><<<dim3(sh.ctas - 1, (sh.BM + 7) / 8), 256, 0, stream>>>(a, sh);
-    return cudaGetLastError();
+    return attn::launch_join<__nv_bfloat16, D>(a, sh, stream);
 }
 
 template <int D>
@@ -758,7 +797,7 @@ cudaError_t launch_dim(const TreeAttnArgs& a, cudaStream_t stream)
 
 size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim)
 {
-    return attn::slot_floats(wide_rows(nodes, group) ? 256 : 128, dim) * 2 * kCtas * sizeof(float);
+    return attn::workspace_bytes({wide_rows(nodes, group) ? 256 : 128, kBN, kCtas}, dim);
 }
 
 cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream)
