@@ -181,7 +181,7 @@ constexpr size_t simt_smem() { return (size_t)(16 * TM * (D + 4) + 2 * kBN * (D 
 template <int D, int TM>
 cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 {
-    const attn::Shape sh = {16 * TM, kBN, kSimtCtas};
+    const attn::Shape sh = {16 * TM, kBN, kSimtCtas, 1};
     if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     constexpr size_t smem = simt_smem<D, TM>();
     cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -208,7 +208,7 @@ size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, 
 {
     if (bf16) return tree_attn_tc_workspace_bytes(nodes, heads / kv_heads, dim);
     const int BM = small_rows(nodes, heads / kv_heads) ? 16 : 64;
-    return attn::workspace_bytes({BM, kBN, kSimtCtas}, dim);
+    return attn::workspace_bytes({BM, kBN, kSimtCtas, 1}, dim);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream)

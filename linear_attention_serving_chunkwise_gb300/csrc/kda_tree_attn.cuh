@@ -1,11 +1,11 @@
 // How the tree-attention kernels share their work, and the join of what was split.
 //
 // A unit is one (sequence, key/value head, block of query rows); its tokens (the context and
-// the draft nodes) are cut into tiles.  All tiles of all units form one line (sequence-major,
-// then head, then row block), and CTA c of N takes the tiles [start(c), start(c + 1)) with
-// start(c) = floor(T c / N): every CTA gets the same number of tiles (one more or less)
-// whatever the mix of lengths, a long sequence is split over many CTAs and a short one is
-// not.  The context lengths live on the device, so each CTA works its cut out for itself.
+// the draft nodes) are cut into tiles.  All units' tiles form one line (sequence-major, then
+// head, then row block; before a unit's tiles a few places stand for its fixed cost), and CTA
+// c of N takes the places [start(c), start(c + 1)) with start(c) = floor(T c / N): every CTA
+// gets the same share (a place more or less) whatever the mix of lengths, a long sequence
+// is split over many CTAs and a short one is not.  The context lengths live on the device, so each CTA works its cut out for itself.
 //
 // A unit that lies within one CTA's range is finished there.  Of any other, each CTA leaves
 // its part (running maximum, sum and unnormalised output per row, fp32) in the workspace:
@@ -23,6 +23,7 @@ struct Shape {
     int BM;        // query rows of a unit
     int BN;        // tokens of a tile
     int ctas;      // CTAs that share the line
+    int head;      // places of the line before a unit's tiles: what a unit costs beyond them, in tiles
 };
 
 // What a CTA left for the join.
@@ -43,7 +44,7 @@ __host__ __device__ __forceinline__ int row_blocks(const TreeAttnArgs& a, int BM
 // tiles of 64 tokens would read a cache of terabytes).
 __host__ __forceinline__ bool line_fits(const TreeAttnArgs& a, const Shape& sh)
 {
-    const double tiles = (double)a.table_cols * a.page_size / sh.BN + 1;
+    const double tiles = (double)a.table_cols * a.page_size / sh.BN + 1 + sh.head;
     return tiles * row_blocks(a, sh.BM) * a.kv_heads * a.batch < 2147483647.0;
 }
 
@@ -55,11 +56,12 @@ __device__ __forceinline__ int seq_tokens(const TreeAttnArgs& a, int b, bool& ok
     return ok ? c + a.nodes : 0;
 }
 __device__ __forceinline__ int tiles_of(int n, int BN) { return n > 0 ? (n - 1) / BN + 1 : 1; }   // a skipped sequence still gets its zero rows
-__device__ __forceinline__ int seq_tiles(const TreeAttnArgs& a, int b, int BN)
+// places of one of its units
+__device__ __forceinline__ int unit_places(int n, const Shape& sh) { return tiles_of(n, sh.BN) + sh.head; }
+__device__ __forceinline__ int unit_places(const TreeAttnArgs& a, int b, const Shape& sh)
 {
     bool ok;
-    const int n = seq_tokens(a, b, ok);
-    return tiles_of(n, BN);
+    return unit_places(seq_tokens(a, b, ok), sh);
 }
 
 // floor(T c / N) without a product past 32 bits
@@ -90,16 +92,17 @@ struct Line {
     {
         rb = row_blocks(a, sh.BM);
         per_seq = rb * a.kv_heads;
-        int sum = 0;
-        for (int i = lane; i < a.batch; i += 32) sum += seq_tiles(a, i, sh.BN);
+        const int mine = lane < a.batch ? unit_places(a, lane, sh) : 0;    // of the first 32 sequences
+        int sum = mine;
+        for (int i = lane + 32; i < a.batch; i += 32) sum += unit_places(a, i, sh);
         const int T = __reduce_add_sync(0xffffffffu, sum) * per_seq;
         lo = at = line_start(T, cta, sh.ctas);
         hi = line_start(T, cta + 1, sh.ctas);
-        // the sequence that holds tile lo, and where it begins
+        // the sequence that holds place lo, and where it begins
         b = a.batch;
         b0 = 0;
         for (int i0 = 0; i0 < a.batch; i0 += 32) {
-            const int i = i0 + lane, n = i < a.batch ? seq_tiles(a, i, sh.BN) * per_seq : 0;
+            const int i = i0 + lane, n = (i0 == 0 ? mine : i < a.batch ? unit_places(a, i, sh) : 0) * per_seq;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -119,26 +122,28 @@ struct Line {
     // any thread
     __device__ __forceinline__ bool next(const TreeAttnArgs& a, const Shape& sh, int cta, Piece& p)
     {
-        if (at >= hi) return false;
-        p.n = seq_tokens(a, b, p.seq_ok);
-        int tiles = tiles_of(p.n, sh.BN);
-        while (at >= b0 + tiles * per_seq) {
-            b0 += tiles * per_seq;
-            p.n = seq_tokens(a, ++b, p.seq_ok);
-            tiles = tiles_of(p.n, sh.BN);
+        while (at < hi) {
+            p.n = seq_tokens(a, b, p.seq_ok);
+            const int places = unit_places(p.n, sh);
+            if (at >= b0 + places * per_seq) {
+                b0 += places * per_seq;
+                ++b;
+                continue;
+            }
+            const int u = (at - b0) / places, us = b0 + u * places, ue = us + places;
+            p.b = b;
+            p.hk = rb == 1 ? u : u / rb;
+            p.r0 = (u - p.hk * rb) * sh.BM;
+            p.first = max(at - us - sh.head, 0);
+            p.last = min(hi, ue) - us - sh.head;
+            p.ctx = p.n - a.nodes;
+            p.begins = us + sh.head >= lo;
+            p.ends = ue <= hi;
+            p.slot = 2 * cta + (p.begins ? 1 : 0);
+            at = min(hi, ue);
+            if (p.last > p.first) return true;      // (else only places of its head are here)
         }
-        const int u = (at - b0) / tiles, us = b0 + u * tiles, ue = us + tiles;
-        p.b = b;
-        p.hk = rb == 1 ? u : u / rb;
-        p.r0 = (u - p.hk * rb) * sh.BM;
-        p.first = at - us;
-        p.last = min(hi, ue) - us;
-        p.ctx = p.n - a.nodes;
-        p.begins = us >= lo;
-        p.ends = ue <= hi;
-        p.slot = 2 * cta + (p.begins ? 1 : 0);
-        at = us + p.last;
-        return true;
+        return false;
     }
 };
 

@@ -14,8 +14,8 @@
 // (until then the weights are at most 2^8, which bf16 and the fp32 sums hold as well).
 //
 // Warps 0-3 and 4-7: softmax and epilogue of stream 0 and 1, a row to a thread.  Warps 8-11:
-// the cache rows, into a ring of K and V tiles.  Warp 12 issues the products, warp 13 copies Q
-// (14 and 15 only complete the warpgroup that gives its registers to the softmax).
+// the cache rows, into a ring of K and V tiles.  Warp 12 issues the products, warps
+// 13-15 copy Q.  The last two groups give registers to the softmax.
 //
 // The cache rows come by TMA where the page size is a multiple of 8: a tile is a stack of boxes
 // of 8 to 128 rows (the largest power of two in the page size), and 8 rows are one swizzle
@@ -46,6 +46,7 @@ constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmax
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads start with 128 each
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
 constexpr int kCtas = 152;                          // one to an SM
+constexpr int kHead = 2;                            // a unit's fixed cost (Q, first tile, epilogue), in tiles
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
@@ -315,14 +316,17 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
 }
 
 // ------------------------------------------------------------------ the query rows
-// One warp, as soon as the last piece's scores are done: rows past the last are zero, and
+// Three warps, as soon as the last piece's scores are done: rows past the last are zero, and
 // scale 0 is a zero Q (every score is then 0).
+constexpr int kQueryThreads = 96;
+
 template <int D, bool kWide>
-__device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int lane)
+__device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t, int lane)
 {
     using L = Layout<D, kWide>;
-    constexpr int CH = D / 8;
-    const int G = a.heads / a.kv_heads, R = a.nodes * G;
+    constexpr int CH = D / 8, STEP = kQueryThreads / CH;   // chunks of a row; rows copied at once
+    const int G = a.heads / a.kv_heads, R = a.nodes * G, c = t % CH;
+    const int step_node = STEP / G, step_head = STEP - step_node * G;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
     Waiter wait{a.status};
     attn::Line line;
@@ -331,19 +335,23 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
     attn::Recorder rec;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         rec.see(pc);
+        int r = t / CH, node = (pc.r0 + r) / G, head = pc.r0 + r - node * G;
+        const __nv_bfloat16* src = q + ((size_t)pc.b * a.nodes * a.heads + pc.hk * G) * D + 8 * c;
         if (piece) wait(&sm.q_empty, (piece - 1) & 1);
-        for (int idx = lane; idx < sh.BM * CH; idx += 32) {
-            const int r = idx / CH, c = idx % CH, row = pc.r0 + r;
-            const bool there = row < R && a.scale != 0.f;
-            const size_t off = there ? (((size_t)pc.b * a.nodes + row / G) * a.heads + pc.hk * G + row % G) * D + 8 * c : 0;
-            cp16(smem_u32(base + (r >> 7) * L::kTile + sw128_chunk(r & 127, c, 128)), q + off, there);
+#pragma unroll 4
+        for (; r < sh.BM; r += STEP) {
+            const bool there = pc.r0 + r < R && a.scale != 0.f;
+            cp16(smem_u32(base + (r >> 7) * L::kTile + sw128_chunk(r & 127, c, 128)), there ? src + ((size_t)node * a.heads + head) * D : q, there);
+            node += step_node;
+            head += step_head;
+            if (head >= G) { head -= G; ++node; }
         }
         cp_commit();
         cp_wait<0>();
         fence_proxy_async_smem();
         mbar_arrive(&sm.q_full);
     }
-    if (lane == 0) rec.leave(a, blockIdx.x);
+    if (t == 0) rec.leave(a, blockIdx.x);
 }
 
 // ------------------------------------------------------------------ the products
@@ -692,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);
         }
-        mbar_init(&sm.q_full, 32);
+        mbar_init(&sm.q_full, kQueryThreads);
         mbar_init(&sm.q_empty, 1);
         mbar_init(&sm.o_done, 1);
         mbar_init(&sm.o_free, kSoftmaxThreads / 32);
@@ -713,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
             else produce_gather<D, kWide>(a, sh, sm, base, t - kSoftmaxThreads);
         } else if (warp == 12) {
             multiply<D, kWide>(a, sh, sm, base, t & 31);
-        } else if (warp == 13) {
-            query<D, kWide>(a, sh, sm, base, t & 31);
+        } else {
+            query<D, kWide>(a, sh, sm, base, t - 13 * 32, t & 31);
         }
     }
     __syncwarp();
@@ -725,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
 }
 
 bool wide_rows(int nodes, int group) { return nodes * group > 128; }
+attn::Shape shape_of(bool wide) { return {wide ? 256 : 128, kBN, kCtas, kHead}; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
@@ -765,7 +774,7 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
 {
     using L = Layout<D, kWide>;
     const auto kernel = tree_attn_tc_kernel<D, kWide, kBoxes>;
-    const attn::Shape sh = {kWide ? 256 : 128, kBN, kCtas};
+    const attn::Shape sh = shape_of(kWide);
     if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     Maps maps = {};
     if (kBoxes) {
@@ -797,7 +806,7 @@ cudaError_t launch_dim(const TreeAttnArgs& a, cudaStream_t stream)
 
 size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim)
 {
-    return attn::workspace_bytes({wide_rows(nodes, group) ? 256 : 128, kBN, kCtas}, dim);
+    return attn::workspace_bytes(shape_of(wide_rows(nodes, group)), dim);
 }
 
 cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream)
