@@ -52,7 +52,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
 
 struct Shared {
-    uint64_t kv_full[10], kv_empty[10], s_full[2], p_full[2], q_full, q_empty, o_done, o_free;
+    uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done, o_free;
     uint64_t bad_nodes[8];                          // by piece: nodes with non-finite values
     alignas(16) uint32_t missing[8][4];                         // by tile: its tokens without a page (a V tile is freed after its softmax, so the
                                                     // copies are never more than 6 tiles past the one the softmax is at)
@@ -132,11 +132,12 @@ __device__ __forceinline__ Rows rows_of(const TreeAttnArgs& a, const attn::Piece
     return r;
 }
 
-// The warp's 32 rows of a tile through registers; rows that do not exist become zero.  From
-// token `clean` of the tile on, non-finite values become zero too and their nodes are noted.
+// The warp's 32 rows of a tile through registers; rows that do not exist become zero.  In the
+// rows of draft nodes (node 0 in row `node0`, which may be negative) non-finite values become
+// zero too and their nodes are noted.
 template <int D>
 __device__ __forceinline__ void copy_rows(uint8_t* dst, const __nv_bfloat16* src, size_t off, unsigned exists, int w, int lane,
-                                          int clean, uint64_t* bad_nodes)
+                                          int node0, uint64_t* bad_nodes)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;        // 16-byte chunks of a row; rows a warp copies at once
     const int sub = lane / CH, chunk = lane % CH;
@@ -153,7 +154,7 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const __nv_bfloat16* src
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int r = i0 + k * RPI + sub;
-            if (32 * w + r >= clean) {
+            if (32 * w + r >= node0) {
                 uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -169,23 +170,53 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const __nv_bfloat16* src
     bad = __reduce_or_sync(0xffffffffu, bad);
     if (bad && lane == 0) {
         for (int r = 0; r < 32; ++r)
-            if (bad >> r & 1) atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (32 * w + r - clean));
+            if (bad >> r & 1) atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (32 * w + r - node0));
     }
 }
 
-// By TMA.  Warp 0 of the four issues the boxes, a lane to a box.  Tiles with draft nodes (their
-// values) or with tokens that have no page pass through registers, by all four warps.
+// The same for a V tile that came by TMA; rows past the last token (from row `rows` on) become zero.
+constexpr int kCleanThreads = 96;
+
+template <int D>
+__device__ __forceinline__ void clean_rows(uint8_t* tile, int node0, int rows, int t, uint64_t* bad_nodes)
+{
+    constexpr int CH = D / 8, STEP = kCleanThreads / CH;
+    const int chunk = t % CH;
+#pragma unroll 4
+    for (int r = max(0, node0) + t / CH; r < kBN; r += STEP) {
+        uint4* at = reinterpret_cast<uint4*>(tile + sw128_chunk(r, chunk, 128));
+        if (r >= rows) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 x = *at;
+        uint32_t h[4] = {x.x, x.y, x.z, x.w};
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool lo = finite_bf16(h[e]), hi = finite_bf16(h[e] >> 16);
+            bad |= !(lo && hi);
+            h[e] = (lo ? h[e] & 0xffffu : 0u) | (hi ? h[e] & 0xffff0000u : 0u);
+        }
+        if (bad) {
+            *at = make_uint4(h[0], h[1], h[2], h[3]);
+            atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (r - node0));
+        }
+    }
+}
+
+// By TMA.  Warp 0 of the four issues the boxes, a lane to a box; a V tile with draft nodes is
+// handed over by the other three once they have cleaned it.  A tile with tokens that have no
+// page passes through registers, by all four.
 template <int D, bool kWide>
-__device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn::Shape& sh, const Maps& maps, Shared& sm, uint8_t* base, int t)
+__device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn::Shape& sh, const Maps& maps, attn::Line line, Shared& sm,
+                                              uint8_t* base, int t)
 {
     using L = Layout<D, kWide>;
     const int lane = t & 31, w = t >> 5, box = maps.box_rows;
-    const size_t row_stride = (size_t)a.kv_heads * D;
     Waiter wait{a.status};
-    attn::Line line;
-    line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
-    uint32_t fill = 0;
+    uint32_t fill = 0, raw_phase = 0;
     bool bad_page = false;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         const int32_t* table = a.block_table + (size_t)pc.b * a.table_cols;
@@ -200,43 +231,49 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
             const bool lost = __any_sync(0xffffffffu, wanted && !there);
             const int boxes = __popc(__ballot_sync(0xffffffffu, there));
             next = look_up(tile + 1);
-            const bool slow[2] = {lost, lost || t0 + kBN > pc.ctx};
-            Rows rows = {};
-            if (slow[1]) {
-                const int p = t0 + 32 * w + lane;
-                rows = rows_of(a, pc, p, p < pc.n ? __ldg(table + p / a.page_size) : -1, row_stride, D);
-                bad_page |= rows.lost != 0;
-            }
+            const bool nodes = t0 + kBN > pc.ctx;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++fill) {
                 const uint32_t s = fill % L::kSlots;
                 uint8_t* dst = base + L::kQ + s * L::kTile;
                 if (w == 0 && fill >= (uint32_t)L::kSlots) wait(&sm.kv_empty[s], (fill / L::kSlots - 1) & 1);
-                if (!slow[kv]) {
-                    if (w != 0) continue;
+                if (lost) {
+                    const int p = t0 + 32 * w + lane;
+                    const Rows rows = rows_of(a, pc, p, p < pc.n ? __ldg(table + p / a.page_size) : -1, (size_t)a.kv_heads * D, D);
+                    bad_page |= rows.lost != 0;
+                    bar_sync(10, kProducerThreads); // the slot is free
+                    if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = rows.lost;
+                    copy_rows<D>(dst, static_cast<const __nv_bfloat16*>(kv ? a.v_cache : a.k_cache), kv ? rows.voff : rows.koff, rows.exists,
+                                 w, lane, kv ? pc.ctx - t0 : kBN, &sm.bad_nodes[piece & 7]);
+                    fence_proxy_async_smem();
+                    bar_sync(10, kProducerThreads);
+                    if (t == 0) mbar_arrive(&sm.kv_full[s]);
+                    continue;
+                }
+                uint64_t* const landed = kv && nodes ? &sm.v_raw[s] : &sm.kv_full[s];
+                if (w == 0) {
                     const bool go = __all_sync(0xffffffffu, wait.alive);
                     if (kv == 0 && lane < 4) sm.missing[fill / 2 & 7][lane] = 0;
                     __syncwarp();
                     if (lane == 0) {
-                        if (go) mbar_arrive_expect_tx(&sm.kv_full[s], boxes * box * D * 2);
-                        else mbar_arrive(&sm.kv_full[s]);
+                        if (go) mbar_arrive_expect_tx(landed, boxes * box * D * 2);
+                        else mbar_arrive(landed);
                     }
                     __syncwarp();
                     if (go && there) {
 #pragma unroll
                         for (int c = 0; c < D; c += 64)
-                            tma_load_4d(dst + (c / 64) * (kBN * 128) + lane * box * 128, kv ? &maps.v : &maps.k, &sm.kv_full[s], c, pc.hk,
+                            tma_load_4d(dst + (c / 64) * (kBN * 128) + lane * box * 128, kv ? &maps.v : &maps.k, landed, c, pc.hk,
                                         pos % a.page_size, id);
                     }
-                    continue;
+                } else if (kv && nodes) {
+                    wait(landed, raw_phase >> s & 1);
+                    raw_phase ^= 1u << s;
+                    clean_rows<D>(dst, pc.ctx - t0, pc.n - t0, t - 32, &sm.bad_nodes[piece & 7]);
+                    fence_proxy_async_smem();
+                    bar_sync(11, kCleanThreads);
+                    if (t == 32) mbar_arrive(&sm.kv_full[s]);
                 }
-                bar_sync(2, kProducerThreads);      // the slot is free
-                if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = rows.lost;
-                copy_rows<D>(dst, static_cast<const __nv_bfloat16*>(kv ? a.v_cache : a.k_cache), kv ? rows.voff : rows.koff, rows.exists, w, lane,
-                             kv ? max(0, pc.ctx - t0) : kBN, &sm.bad_nodes[piece & 7]);
-                fence_proxy_async_smem();
-                bar_sync(2, kProducerThreads);
-                if (t == 0) mbar_arrive(&sm.kv_full[s]);
             }
         }
     }
@@ -249,7 +286,7 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
 
 // By 16-byte asynchronous copies, all four warps.
 template <int D, bool kWide>
-__device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t)
+__device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn::Shape& sh, attn::Line line, Shared& sm, uint8_t* base, int t)
 {
     using L = Layout<D, kWide>;
     constexpr int CH = D / 8, RPI = 32 / CH;
@@ -259,8 +296,6 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
     const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.num_pages ? a.v_cache : a.q);
     const size_t row_stride = (size_t)a.kv_heads * D;
     Waiter wait{a.status};
-    attn::Line line;
-    line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
     uint32_t fill = 0, sent = 0;                    // ring slots begun, and handed over
     bool bad_page = false;
@@ -292,7 +327,7 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
                 const __nv_bfloat16* src = kv ? vc : kc;
                 const size_t off = kv ? rows.voff : rows.koff;
                 if (kv == 1 && t0 + kBN > pc.ctx) {
-                    copy_rows<D>(dst, src, off, rows.exists, w, lane, max(0, pc.ctx - t0), &sm.bad_nodes[piece & 7]);
+                    copy_rows<D>(dst, src, off, rows.exists, w, lane, pc.ctx - t0, &sm.bad_nodes[piece & 7]);
                 } else {
 #pragma unroll 4
                     for (int i = 0; i < 32; i += RPI) {
@@ -321,7 +356,7 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
 constexpr int kQueryThreads = 96;
 
 template <int D, bool kWide>
-__device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t, int lane)
+__device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& sh, attn::Line line, Shared& sm, uint8_t* base, int t)
 {
     using L = Layout<D, kWide>;
     constexpr int CH = D / 8, STEP = kQueryThreads / CH;   // chunks of a row; rows copied at once
@@ -329,8 +364,6 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
     const int step_node = STEP / G, step_head = STEP - step_node * G;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
     Waiter wait{a.status};
-    attn::Line line;
-    line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
     attn::Recorder rec;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
@@ -356,12 +389,10 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
 
 // ------------------------------------------------------------------ the products
 template <int D, bool kWide>
-__device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int lane)
+__device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shape& sh, attn::Line line, Shared& sm, uint8_t* base)
 {
     using L = Layout<D, kWide>;
     Waiter wait{a.status};
-    attn::Line line;
-    line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
     const uint32_t tm = sm.tmem, q0 = smem_u32(base), ring = q0 + L::kQ;
     const uint32_t id_s = idesc_bf16_f32(128, kBN, 0, 0, a.scale < 0.f), id_o = idesc_bf16_f32(128, D, 0, 1);
@@ -457,8 +488,22 @@ __device__ __forceinline__ float max_of(const float (&x)[32])
     return fmaxf(a0, a1);
 }
 
+// One step of the transpose of 4 x 4 pieces over four lanes: lanes that differ in bit `by`
+// exchange the later of two pieces for the earlier one.
+__device__ __forceinline__ void swap_pieces(uint4& lo, uint4& hi, bool upper, int by)
+{
+    uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
+    uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? l[e] : h[e], by);
+        if (upper) l[e] = got;
+        else h[e] = got;
+    }
+}
+
 template <int D, bool kWide>
-__device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape& sh, Shared& sm, uint8_t* base, int t)
+__device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape& sh, attn::Line line, Shared& sm, uint8_t* base, int t)
 {
     using L = Layout<D, kWide>;
     float* stats = reinterpret_cast<float*>(base + L::kStats);        // [stream][m, l][128]
@@ -468,8 +513,6 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
     const uint32_t tS = tmem_addr(sm.tmem, quad, L::kColS + 128 * w), tO = tmem_addr(sm.tmem, quad, L::kColO);
     const float sc = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;  // scores in powers of two
     Waiter wait{a.status};
-    attn::Line line;
-    line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
     uint32_t used = 0, done = 0;                    // items of this stream, and tiles, so far
     int masks_of = -1;
@@ -624,7 +667,11 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             ws[rl] = m == -INFINITY ? m : m * sc;
             ws[sh.BM + rl] = l;
         }
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (((size_t)pc.b * a.nodes + row / G) * a.heads + pc.hk * G + row % G) * D;
+        // out's row of this thread (in rows of D), and of the four rows of its group of four lanes
+        const int orow = row < R ? (int)(((size_t)pc.b * a.nodes + row / G) * a.heads + pc.hk * G + row % G) : -1;
+        int orows[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) orows[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
         for (int c = c0; c < c1; c += 32) {
             float o[32];
             if (busy) {
@@ -660,11 +707,23 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                     if (!isfinite(x)) o[k] += x;
                 }
             }
-            if (row < R && pc.whole()) {
+            if (pc.whole()) {
+                // Four lanes hold four rows of 32 channels, 16 bytes at a time; after the exchange
+                // lane j holds piece j of each row, and a store covers 64 bytes of eight rows
+                // instead of 16 bytes of 32.
+                uint4 x[4];
 #pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                    *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(pack_bf16x2(o[k], o[k + 1]), pack_bf16x2(o[k + 2], o[k + 3]),
-                                                                       pack_bf16x2(o[k + 4], o[k + 5]), pack_bf16x2(o[k + 6], o[k + 7]));
+                for (int k = 0; k < 4; ++k)
+                    x[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                      pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                swap_pieces(x[0], x[1], lane & 1, 1);
+                swap_pieces(x[2], x[3], lane & 1, 1);
+                swap_pieces(x[0], x[2], lane & 2, 2);
+                swap_pieces(x[1], x[3], lane & 2, 2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (orows[k] >= 0)
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)orows[k] * D + c + 8 * (lane & 3)) = x[k];
             } else if (row < R) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
@@ -687,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     extern __shared__ __align__(1024) uint8_t base[];   // all of it: the swizzled tiles start at 0
     Shared& sm = *reinterpret_cast<Shared*>(base + L::kShared);
     const int t = threadIdx.x, warp = t >> 5;
+    attn::Line line;
+    line.begin(a, sh, blockIdx.x, t & 31);
     if (warp == 12) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
@@ -695,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
         for (int i = 0; i < L::kSlots; ++i) {
             mbar_init(&sm.kv_full[i], kBoxes ? 1 : kProducerThreads);
             mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.v_raw[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
@@ -713,16 +775,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax<D, kWide>(a, sh, sm, base, t);
+        softmax<D, kWide>(a, sh, line, sm, base, t);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < 12) {
-            if constexpr (kBoxes) produce_boxes<D, kWide>(a, sh, maps, sm, base, t - kSoftmaxThreads);
-            else produce_gather<D, kWide>(a, sh, sm, base, t - kSoftmaxThreads);
+            if constexpr (kBoxes) produce_boxes<D, kWide>(a, sh, maps, line, sm, base, t - kSoftmaxThreads);
+            else produce_gather<D, kWide>(a, sh, line, sm, base, t - kSoftmaxThreads);
         } else if (warp == 12) {
-            multiply<D, kWide>(a, sh, sm, base, t & 31);
+            multiply<D, kWide>(a, sh, line, sm, base);
         } else {
-            query<D, kWide>(a, sh, sm, base, t - 13 * 32, t & 31);
+            query<D, kWide>(a, sh, line, sm, base, t - 13 * 32);
         }
     }
     __syncwarp();
