@@ -52,11 +52,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
 
 struct Shared {
-    uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done, o_free;
+    uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done[2], o_free[2];
     uint64_t bad_nodes[8];                          // by piece: nodes with non-finite values
     alignas(16) uint32_t missing[8][4];                         // by tile: its tokens without a page (a V tile is freed after its softmax, so the
                                                     // copies are never more than 6 tiles past the one the softmax is at)
-    TreeSmem tree;
+    TreeSmem tree[2];                               // one for each stream: they may be at different pieces
     uint32_t tmem;
 };
 
@@ -66,8 +66,8 @@ struct Layout {
     static constexpr int kQ = kTile * (kWide ? 2 : 1);
     static constexpr int kSlots = D == 128 ? 5 : 10;            // ring: K and V tiles in turn
     static constexpr int kLag = kSlots - 2;                     // gathered: slots in flight before the oldest is waited for
-    static constexpr int kStats = kQ + kSlots * kTile;          // both streams' maxima and sums (streams in turn)
-    static constexpr int kShared = kStats + (kWide ? 0 : 2 * 2 * 128 * 4);
+    static constexpr int kStats = kQ + kSlots * kTile;          // streams in turn: their maxima and sums, by piece parity
+    static constexpr int kShared = kStats + (kWide ? 0 : 2 * 2 * 2 * 128 * 4);
     static constexpr int kBytes = kShared + (int)sizeof(Shared);
     static constexpr uint32_t kColS = 0, kColO = 256;           // stream w: S at 128 w, O at 256 + D w
     static_assert(kBytes <= 232448, "shared memory");
@@ -219,6 +219,7 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
     uint32_t fill = 0, raw_phase = 0;
     bool bad_page = false;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
+        if (t == 0) sm.bad_nodes[piece & 7] = 0;    // (before this warp lets any other see a tile of the piece)
         const int32_t* table = a.block_table + (size_t)pc.b * a.table_cols;
         auto look_up = [&](int tile) {              // box `lane` of the tile
             const int pos = tile * kBN + lane * box;
@@ -307,6 +308,8 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
         ++sent;
     };
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
+        if (t == 0) sm.bad_nodes[piece & 7] = 0;
+        bar_sync(10, kProducerThreads);
         const int32_t* table = a.block_table + (size_t)pc.b * a.table_cols;
         auto look_up = [&](int tile) {              // one tile ahead
             const int pos = tile * kBN + 32 * w + lane;
@@ -397,7 +400,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
     const uint32_t tm = sm.tmem, q0 = smem_u32(base), ring = q0 + L::kQ;
     const uint32_t id_s = idesc_bf16_f32(128, kBN, 0, 0, a.scale < 0.f), id_o = idesc_bf16_f32(128, D, 0, 1);
     // ring slot and phase of the next K and V tile; items of each stream so far
-    uint32_t ks_ = 0, kp = 0, vs_ = 1, vp = 0, used[2] = {0, 0};
+    uint32_t ks_ = 0, kp = 0, vs_ = 1, vp = 0, used[2] = {0, 0}, pieces[2] = {0, 0};   // (and pieces of each stream)
     auto advance = [](uint32_t& s, uint32_t& phase) {
         s += 2;
         if (s >= (uint32_t)L::kSlots) { s -= L::kSlots; phase ^= 1; }
@@ -431,7 +434,10 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             const uint32_t s = vs_;
             if (first) wait(&sm.kv_full[s], vp);
             if (last) advance(vs_, vp);
-            if (i == 0 && piece) wait(&sm.o_free, (piece - 1) & 1);
+            if (i == w) {                           // the stream's first products of the piece overwrite O
+                if (pieces[w]) wait(&sm.o_free[w], (pieces[w] - 1) & 1);
+                ++pieces[w];
+            }
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
             tc_fence_after_sync();
@@ -443,7 +449,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
                         umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
                 }
                 if (last) umma_commit(&sm.kv_empty[s]);
-                if (i == items - 1) umma_commit(&sm.o_done);
+                if (i + 2 >= items) umma_commit(&sm.o_done[w]);
             }
             __syncwarp();
         };
@@ -456,7 +462,8 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             if (i + 3 < items) scores(i + 3, 1);
         }
     }
-    if (piece) wait(&sm.o_done, (piece - 1) & 1);   // no product or commit is in flight after this
+    for (int w = 0; w < 2; ++w)                     // no product or commit is in flight after this
+        if (pieces[w]) wait(&sm.o_done[w], (pieces[w] - 1) & 1);
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
@@ -514,18 +521,20 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
     const float sc = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;  // scores in powers of two
     Waiter wait{a.status};
     attn::Piece pc;
-    uint32_t used = 0, done = 0;                    // items of this stream, and tiles, so far
+    uint32_t used = 0, done = 0, pieces[2] = {0, 0};   // items of this stream, tiles, pieces of each stream so far
     int masks_of = -1;
+    TreeSmem& tree = sm.tree[w];
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         const int tiles = pc.last - pc.first;
-        if (pc.b != masks_of) {                     // (everyone is done with the last piece's tree: the epilogue's barrier)
-            if (warp == 0) tree_masks(sm.tree, a.parents + (size_t)pc.b * a.nodes, a.nodes, lane);
+        if (pc.b != masks_of) {
+            bar_sync(2 + w, 128);                   // the stream's warps have read the last tree
+            if ((warp & 3) == 0) tree_masks(tree, a.parents + (size_t)pc.b * a.nodes, a.nodes, lane);
             masks_of = pc.b;
-            bar_sync(1, kSoftmaxThreads);
+            bar_sync(2 + w, 128);
         }
-        if (!(pc.seq_ok && sm.tree.ok) && t == 0) report_status(a.status, kDevBadSeqlens);
+        if (!(pc.seq_ok && tree.ok) && t == 0) report_status(a.status, kDevBadSeqlens);
         const int row = pc.r0 + (kWide ? 128 * w : 0) + r;
-        const uint64_t see = pc.seq_ok && sm.tree.ok && row < R ? sm.tree.anc[row / G] : 0ull;
+        const uint64_t see = pc.seq_ok && tree.ok && row < R ? tree.anc[row / G] : 0ull;
         const bool busy = __any_sync(0xffffffffu, see != 0);
         float m = -INFINITY, l = 0.f;               // m in score units, before sc
         bool begun = false;
@@ -551,10 +560,16 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                     }
                 };
                 bool stored = false;
-                if (all && begun) {
-                    // A tile that every row sees whole, after the first: the weights are formed from the
-                    // last maximum while the tile's own is still being found, and stored over the
-                    // scores once it is known that the maximum may stand (nearly always).
+                if (all) {
+                    // A tile that every row sees whole: the weights are formed from the last maximum (in
+                    // a piece's first tile, that of 32 tokens) while the tile's own is still being
+                    // found, and stored over the scores once it is known that it may stand (nearly always).
+                    if (!begun) {
+                        float x[32];
+                        tmem_ld32(tS, x);
+                        tmem_wait_ld();
+                        m = max_of(x);
+                    }
                     const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
                     float2 sum = make_float2(0.f, 0.f);
                     float top = -INFINITY;
@@ -641,20 +656,23 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             m = -INFINITY;
             l = 0.f;
         }
+        const bool two = !kWide && tiles > 1;       // stream 1 has a part of the same rows
+        float* st = stats + (kWide ? 0 : 512 * (piece & 1));
         if (!kWide) {
-            stats[256 * w + r] = m;
-            stats[256 * w + 128 + r] = l;
+            st[256 * w + r] = m;
+            st[256 * w + 128 + r] = l;
         }
-        wait(&sm.o_done, piece & 1);
+        for (int k = 0; k < 2; ++k)                 // the streams this thread reads: its own, or both of the piece
+            if (kWide ? k == w : k == 0 || two) wait(&sm.o_done[k], pieces[k]++ & 1);
+        __syncwarp();
         tc_fence_after_sync();
-        bar_sync(1, kSoftmaxThreads);
+        if (!kWide) bar_sync(1, kSoftmaxThreads);
         const uint64_t bad = *const_cast<volatile uint64_t*>(&sm.bad_nodes[piece & 7]) & see;
         // this thread's columns [c0, c1) of the row: stream 1's part is joined when it has one
         const int c0 = kWide ? 0 : w * (D / 2), c1 = kWide ? D : c0 + D / 2;
-        const bool two = !kWide && tiles > 1;
         float f0 = 1.f, f1 = 0.f;
         if (!kWide) {
-            const float m0 = stats[r], m1 = two ? stats[256 + r] : -INFINITY, l0 = stats[128 + r], l1 = two ? stats[384 + r] : 0.f;
+            const float m0 = st[r], m1 = two ? st[256 + r] : -INFINITY, l0 = st[128 + r], l1 = two ? st[384 + r] : 0.f;
             m = fmaxf(m0, m1);
             f0 = m0 == -INFINITY ? 0.f : ex2((m0 - m) * sc);
             f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * sc);
@@ -733,9 +751,10 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_free);
-        bar_sync(1, kSoftmaxThreads);
-        if (t == 0) sm.bad_nodes[piece & 7] = 0;
+        if (lane == 0) {
+            if (kWide || w == 0 || two) mbar_arrive(&sm.o_free[w]);
+            if (!kWide && (w == 1 || two)) mbar_arrive(&sm.o_free[w ^ 1]);
+        }
     }
 }
 
@@ -761,11 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.o_free[i], kWide ? 4 : 8);
         }
         mbar_init(&sm.q_full, kQueryThreads);
         mbar_init(&sm.q_empty, 1);
-        mbar_init(&sm.o_done, 1);
-        mbar_init(&sm.o_free, kSoftmaxThreads / 32);
         for (int i = 0; i < 8; ++i) sm.bad_nodes[i] = 0;
         mbar_fence_init();
     }
