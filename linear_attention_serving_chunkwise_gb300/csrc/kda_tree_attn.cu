@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
 
     while (line.next(a, sh, blockIdx.x, pc)) {
         const int b = pc.b, hk = pc.hk, r0 = pc.r0, n = pc.n, ctx = pc.ctx;
-        rec.see(pc);
+        rec.see(line, pc);
 
         __syncthreads();              // the last unit's reads of shared memory are done
         if (masks_of != b) {

@@ -10,7 +10,7 @@
 // A unit that lies within one CTA's range is finished there.  Of any other, each CTA leaves
 // its part (running maximum, sum and unnormalised output per row, fp32) in the workspace:
 // slot 2 c when the unit began before the CTA's range, slot 2 c + 1 otherwise, so a CTA has
-// at most two, and a record of both.  join_kernel joins a unit's parts in tile order.
+// at most two, and a record for the join.  join_kernel joins a unit's parts in tile order.
 #pragma once
 
 #include "kda_draft_launch.h"
@@ -26,12 +26,10 @@ struct Shape {
     int head;      // places of the line before a unit's tiles: what a unit costs beyond them, in tiles
 };
 
-// What a CTA left for the join.
+// What CTA c left for the join: the unit whose first part is in slot 2 c + 1 and the CTA with
+// its last part (the CTAs between have one each, in their slots 2 x); last = 0: none.
 struct Record {
-    int begins;    // slot 2 c + 1 holds the first part of a unit: this one
-    int b, hk, r0;
-    int goes_on;   // slot 2 c holds a later part of a unit: 1 a middle one, 2 its last; 0 none
-    int pad[3];
+    int last, b, hk, r0;
 };
 
 // rows of a (sequence, head): K nodes x G query heads, row = node * G + head of the group
@@ -79,6 +77,7 @@ struct Piece {
     bool seq_ok;
     bool begins, ends;      // the unit's first, last tile is in this CTA's range
     int slot;               // workspace slot of the part, when it is not the whole unit
+    int rest;               // the unit's tiles past this CTA's range
     __device__ __forceinline__ bool whole() const { return begins && ends; }
 };
 
@@ -86,6 +85,7 @@ struct Piece {
 struct Line {
     int hi, lo, at, b0;
     int b, per_seq, rb;
+    int T, N;               // places, and CTAs that share them: no more than there are places
 
     // a full warp
     __device__ __forceinline__ void begin(const TreeAttnArgs& a, const Shape& sh, int cta, int lane)
@@ -95,9 +95,14 @@ struct Line {
         const int mine = lane < a.batch ? unit_places(a, lane, sh) : 0;    // of the first 32 sequences
         int sum = mine;
         for (int i = lane + 32; i < a.batch; i += 32) sum += unit_places(a, i, sh);
-        const int T = __reduce_add_sync(0xffffffffu, sum) * per_seq;
-        lo = at = line_start(T, cta, sh.ctas);
-        hi = line_start(T, cta + 1, sh.ctas);
+        T = __reduce_add_sync(0xffffffffu, sum) * per_seq;
+        N = min(sh.ctas, T);
+        if (cta >= N) {
+            lo = hi = at = 0;
+            return;
+        }
+        lo = at = line_start(T, cta, N);
+        hi = line_start(T, cta + 1, N);
         // the sequence that holds place lo, and where it begins
         b = a.batch;
         b0 = 0;
@@ -139,6 +144,7 @@ struct Line {
             p.ctx = p.n - a.nodes;
             p.begins = us + sh.head >= lo;
             p.ends = ue <= hi;
+            p.rest = max(ue - hi, 0);
             p.slot = 2 * cta + (p.begins ? 1 : 0);
             at = min(hi, ue);
             if (p.last > p.first) return true;      // (else only places of its head are here)
@@ -150,10 +156,15 @@ struct Line {
 // One thread of each CTA, piece by piece and once at the end.
 struct Recorder {
     Record r = {};
-    __device__ __forceinline__ void see(const Piece& p)
+    __device__ __forceinline__ void see(const Line& line, const Piece& p)
     {
-        if (!p.begins) r.goes_on = p.ends ? 2 : 1;
-        else if (!p.ends) { r.begins = 1; r.b = p.b; r.hk = p.hk; r.r0 = p.r0; }
+        if (!p.begins || p.ends) return;
+        // the CTA that holds the unit's last place
+        const int end = line.hi + p.rest - 1;
+        r.last = (int)((((long long)end + 1) * line.N - 1) / line.T);
+        r.b = p.b;
+        r.hk = p.hk;
+        r.r0 = p.r0;
     }
     __device__ __forceinline__ void leave(const TreeAttnArgs& a, int cta) { static_cast<Record*>(a.workspace)[cta] = r; }
 };
@@ -172,77 +183,84 @@ __device__ __forceinline__ float* slot_of(const TreeAttnArgs& a, const Shape& sh
 }
 __device__ __forceinline__ float4* slot_out(float* slot, int BM) { return reinterpret_cast<float4*>(slot + 2 * BM); }
 
-// Joins the units that cross a boundary of the line: CTA (c, y) takes rows [32 y, 32 y + 32) of
-// the unit whose first part CTA c left, if there is one.  Lane = row; the warps share the
-// channels.  m = max m_i, o = sum e^{m_i - m} o_i / sum e^{m_i - m} l_i, in tile order.
-constexpr int kJoinThreads = 256;
+// Joins the units that cross a boundary of the line: block (c, y, z) takes rows [32 y, 32 y + 32)
+// and channels [32 z, 32 z + 32) of the unit whose first part CTA c left, if there is one.
+// Lane = row.  The warps share the parts first and the channels second, as many to the parts
+// as give each two: a unit in a hundred parts is as quick to join as one in two.
+// m = max m_i, o = sum e^{m_i - m} o_i / sum e^{m_i - m} l_i, in an order set by the parts alone.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 template <typename Tout, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnArgs a, Shape sh)
 {
-    constexpr int W = kJoinThreads / 32, C = D / 4 / W;      // chunks of 4 channels per warp
-    extern __shared__ short s_parts[];                       // slots of the unit's parts, in order
-    __shared__ float4 s_out[32][D / 4 + 1];
-    __shared__ int s_n;
+    constexpr int K = 2;                                     // chunks of 4 channels a warp takes at a time
+    __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
+    __shared__ float4 s_o[kJoinWarps][K][32];
+    __shared__ float4 s_out[32][9];
     const int t = threadIdx.x, lane = t & 31, w = t >> 5, c = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
-    const Record* recs = static_cast<const Record*>(a.workspace);
-    const Record rec = recs[c];
-    if (!rec.begins) return;
+    const int4 raw = *(reinterpret_cast<const int4*>(a.workspace) + c);
+    const Record rec = {raw.x, raw.y, raw.z, raw.w};
     const int G = a.heads / a.kv_heads, rows = min(sh.BM, a.nodes * G - rec.r0), r0 = 32 * blockIdx.y;
-    if (r0 >= rows) return;
-    if (w == 0) {
-        int n = 0;
-        if (lane == 0) s_parts[0] = (short)(2 * c + 1);
-        for (int x0 = c + 1, more = 1; more && x0 < sh.ctas; x0 += 32) {
-            const int x = x0 + lane, g = x < sh.ctas ? recs[x].goes_on : 0;
-            const unsigned last = __ballot_sync(0xffffffffu, g == 2);
-            const unsigned upto = last ? 0xffffffffu >> (32 - __ffs(last)) : 0xffffffffu;
-            const unsigned on = __ballot_sync(0xffffffffu, g != 0) & upto;
-            if (on >> lane & 1) s_parts[1 + n + __popc(on & ((1u << lane) - 1))] = (short)(2 * x);
-            n += __popc(on);
-            more = last == 0;
-        }
-        if (lane == 0) s_n = 1 + n;
-    }
-    __syncthreads();
-    const int parts = s_n, r = min(r0 + lane, sh.BM - 1);
+    if (rec.last == 0 || r0 >= rows) return;
+    const int parts = rec.last - c + 1, r = min(r0 + lane, sh.BM - 1);
+    const auto part = [&](int i) { return slot_of(a, sh, D, i == 0 ? 2 * c + 1 : 2 * (c + i)); };
     float m = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) m = fmaxf(m, slot_of(a, sh, D, s_parts[i])[r]);
+#pragma unroll 4
+    for (int i = w; i < parts; i += kJoinWarps) m = fmaxf(m, part(i)[r]);
+    s_m[w][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, s_m[k][lane]);
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    float4 o[C] = {};
+    for (int i = w; i < parts; i += kJoinWarps) l = fmaf(exp2f(part(i)[r] - base), part(i)[sh.BM + r], l);
+    s_l[w][lane] = l;
+    const int pw = parts <= 4 ? 2 : parts <= 8 ? 4 : 8, cw = kJoinWarps / pw, pl = w % pw, cl = w / pw;
+    for (int k0 = 0; k0 < 8; k0 += cw * K) {
+        float4 o[K] = {};
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        float* p = slot_of(a, sh, D, s_parts[i]);
-        const float f = exp2f(p[r] - base);
-        l = fmaf(f, p[sh.BM + r], l);
+        for (int i = pl; i < parts; i += pw) {
+            float* p = part(i);
+            const float f = exp2f(p[r] - base);
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const float4 x = slot_out(p, sh.BM)[(size_t)(w + W * k) * sh.BM + r];
-            o[k].x = fmaf(f, x.x, o[k].x);
-            o[k].y = fmaf(f, x.y, o[k].y);
-            o[k].z = fmaf(f, x.z, o[k].z);
-            o[k].w = fmaf(f, x.w, o[k].w);
-        }
-    }
-    const float inv = 1.f / l;                               // nothing to attend to: zeros; NaN stays
-#pragma unroll
-    for (int k = 0; k < C; ++k)
-        s_out[lane][w + W * k] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
-    __syncthreads();
-    for (int i = w; i < 32 && r0 + i < rows; i += W) {
-        const int row = rec.r0 + r0 + i;
-        Tout* dst = static_cast<Tout*>(a.out) + (((size_t)rec.b * a.nodes + row / G) * a.heads + rec.hk * G + row % G) * D;
-        for (int k = lane; k < D / 4; k += 32) {
-            const float4 x = s_out[i][k];
-            if constexpr (sizeof(Tout) == 2) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-                *reinterpret_cast<uint2*>(dst + 4 * k) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            } else {
-                *reinterpret_cast<float4*>(dst + 4 * k) = x;
+            for (int k = 0; k < K; ++k) {
+                const float4 x = slot_out(p, sh.BM)[(size_t)(8 * blockIdx.z + k0 + cl * K + k) * sh.BM + r];
+                o[k].x = fmaf(f, x.x, o[k].x);
+                o[k].y = fmaf(f, x.y, o[k].y);
+                o[k].z = fmaf(f, x.z, o[k].z);
+                o[k].w = fmaf(f, x.w, o[k].w);
             }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) s_o[w][k][lane] = o[k];
+        __syncthreads();
+        if (w < cw * K) {                                    // a warp to a chunk
+            const int k = w % K, first = (w / K) * pw;
+            float4 x = s_o[first][k][lane];
+            for (int i = 1; i < pw; ++i) {
+                const float4 y = s_o[first + i][k][lane];
+                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) sum += s_l[i][lane];
+            const float inv = 1.f / sum;                     // nothing to attend to: zeros; NaN stays
+            s_out[lane][k0 + w] = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        }
+        __syncthreads();
+    }
+    // 8 lanes to a row's 32 channels
+    const int i = t >> 3, k = t & 7;
+    if (r0 + i < rows) {
+        const int row = rec.r0 + r0 + i;
+        Tout* dst = static_cast<Tout*>(a.out) + (((size_t)rec.b * a.nodes + row / G) * a.heads + rec.hk * G + row % G) * D + 32 * blockIdx.z + 4 * k;
+        const float4 x = s_out[i][k];
+        if constexpr (sizeof(Tout) == 2) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+            *reinterpret_cast<float4*>(dst) = x;
         }
     }
 }
@@ -253,9 +271,9 @@ template <typename Tout, int D>
 cudaError_t launch_join(const TreeAttnArgs& a, const Shape& sh, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sh.ctas - 1, (sh.BM + 31) / 32);
+    const int rows = a.nodes * (a.heads / a.kv_heads);
+    cfg.gridDim = dim3(sh.ctas - 1, ((rows < sh.BM ? rows : sh.BM) + 31) / 32, D / 32);
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = (sh.ctas + 1) * sizeof(short);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

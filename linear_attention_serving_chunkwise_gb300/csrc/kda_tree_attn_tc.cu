@@ -354,8 +354,8 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
 }
 
 // ------------------------------------------------------------------ the query rows
-// Three warps, as soon as the last piece's scores are done: rows past the last are zero, and
-// scale 0 is a zero Q (every score is then 0).
+// Three warps, as soon as the last piece's scores are done.  Rows past the unit's last are left as
+// they are (no row's result depends on another row); scale 0 is a zero Q (every score is then 0).
 constexpr int kQueryThreads = 96;
 
 template <int D, bool kWide>
@@ -370,13 +370,13 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
     attn::Piece pc;
     attn::Recorder rec;
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
-        rec.see(pc);
+        rec.see(line, pc);
         int r = t / CH, node = (pc.r0 + r) / G, head = pc.r0 + r - node * G;
         const __nv_bfloat16* src = q + ((size_t)pc.b * a.nodes * a.heads + pc.hk * G) * D + 8 * c;
         if (piece) wait(&sm.q_empty, (piece - 1) & 1);
 #pragma unroll 4
-        for (; r < sh.BM; r += STEP) {
-            const bool there = pc.r0 + r < R && a.scale != 0.f;
+        for (const int rows = min(sh.BM, R - pc.r0); r < rows; r += STEP) {
+            const bool there = a.scale != 0.f;
             cp16(smem_u32(base + (r >> 7) * L::kTile + sw128_chunk(r & 127, c, 128)), there ? src + ((size_t)node * a.heads + head) * D : q, there);
             node += step_node;
             head += step_head;
@@ -536,7 +536,8 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
         const int row = pc.r0 + (kWide ? 128 * w : 0) + r;
         const uint64_t see = pc.seq_ok && tree.ok && row < R ? tree.anc[row / G] : 0ull;
         const bool busy = __any_sync(0xffffffffu, see != 0);
-        float m = -INFINITY, l = 0.f;               // m in score units, before sc
+        // m in score units, before sc; a row that may see nothing never asks for another maximum
+        float m = see ? -INFINITY : INFINITY, l = 0.f;
         bool begun = false;
 
         for (int i = kWide ? 0 : w; i < tiles; i += kWide ? 1 : 2) {
@@ -568,7 +569,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                         float x[32];
                         tmem_ld32(tS, x);
                         tmem_wait_ld();
-                        m = max_of(x);
+                        m = see ? max_of(x) : INFINITY;
                     }
                     const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
                     float2 sum = make_float2(0.f, 0.f);
