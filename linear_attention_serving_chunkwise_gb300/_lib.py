@@ -374,14 +374,34 @@ def state_combine(transition, state_in, state_add, out=None, *, stream=None, che
 
 
 # ---- the draft step (include/kda.h) -----------------------------------------------------
-def _expect(name: str, t: torch.Tensor, dtype, shape, device) -> None:
-    """The C calls know pointers only: a wrong type, shape or device is found here."""
+# These calls take a few microseconds on the GPU, so the marshalling is kept lean: pointers go
+# to ctypes as plain integers, the stream comes as its raw handle, small outputs share an allocation.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _stream_on(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
+    """Address of ``t``.  The C calls know pointers only: a wrong type, shape, device or layout is found here."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _fresh(shape, dtype, device, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        _keep_until_done(t, stream)
+    return t
 
 
 def page_tables(context_lens, new_lens, pages_held, block_table, free_pages, *, page_size: int, max_tokens: int,
@@ -392,32 +412,36 @@ def page_tables(context_lens, new_lens, pages_held, block_table, free_pages, *, 
     of new_lens).  Returns (slot_map [max_tokens] int64, cu_seqlens [B+1] int32, pages_held after
     the call [B] int32, pages_taken [1] int32)."""
     dev, (B, cols) = block_table.device, block_table.shape
-    i32 = torch.int32
-    for name, t in (("context_lens", context_lens), ("new_lens", new_lens), ("pages_held", pages_held)):
-        _expect(name, t, i32, (B,), dev)
-    _expect("block_table", block_table, i32, (B, cols), dev)
-    _expect("free_pages", free_pages, i32, (free_pages.numel(),), dev)
-    slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-    cu = torch.empty(B + 1, dtype=i32, device=dev)
-    held = torch.empty(B, dtype=i32, device=dev)
-    taken = torch.empty(1, dtype=i32, device=dev)
-    if stream is not None:
-        for t in (slots, cu, held, taken):
-            _keep_until_done(t, stream)
-    st = load().kda_page_tables(B, cols, free_pages.numel(), int(page_size), int(max_tokens), _ptr(context_lens),
-                                _ptr(new_lens), _ptr(pages_held), _ptr(block_table), _ptr(free_pages), _ptr(slots),
-                                _ptr(cu), _ptr(held), _ptr(taken), _stream_handle(stream))
+    at, F = block_table.get_device(), free_pages.numel()
+    ctx = _expect("context_lens", context_lens, _I32, (B,), at)
+    new = _expect("new_lens", new_lens, _I32, (B,), at)
+    had = _expect("pages_held", pages_held, _I32, (B,), at)
+    table = _expect("block_table", block_table, _I32, (B, cols), at)
+    free = _expect("free_pages", free_pages, _I32, (F,), at)
+    slots = _fresh((max_tokens,), torch.int64, dev, stream)
+    small = _fresh((2 * B + 2,), _I32, dev, stream)
+    cu, held, taken = small.split((B + 1, B, 1))
+    p = small.data_ptr()
+    st = load().kda_page_tables(B, cols, F, page_size, max_tokens, ctx, new, had, table, free, slots.data_ptr(),
+                                p, p + 4 * (B + 1), p + 4 * (2 * B + 1), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_page_tables")
     return slots, cu, held, taken
 
 
-def _cache_stride(name: str, c: torch.Tensor) -> int:
-    """Elements from page to page of a cache [pages, page_size, heads, dim] whose pages are contiguous."""
-    _, ps, h, d = c.shape
-    if c.stride()[1:] != (h * d, d, 1) and c.numel() > 0 and not c[0].is_contiguous():
+def _cache(name: str, c: torch.Tensor, dtype, shape, device: int):
+    """(address, elements from page to page) of a cache [pages, page_size, heads, dim] whose pages are contiguous."""
+    if c.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {c.dtype}")
+    if c.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(c.shape)}")
+    if c.get_device() != device:
+        raise ValueError(f"{name} is on {c.device}, not on the device of the other tensors")
+    P, ps, h, d = shape
+    stride = c.stride()
+    if stride[1:] != (h * d, d, 1) and P > 0 and not c[0].is_contiguous():
         raise ValueError(f"{name}: each page must be contiguous")
-    return c.stride(0) if c.shape[0] > 1 else ps * h * d
+    return c.data_ptr(), stride[0] if P > 1 else ps * h * d
 
 
 def make_tree_attention_desc(batch, nodes, num_heads, num_kv_heads, dim, dtype, num_pages, page_size, table_cols,
@@ -437,32 +461,31 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents, out=
     q [B,K,Hq,D] (fp32 or bf16); k_cache, v_cache [pages, page_size, Hk, D] of q's type, each page
     contiguous (the pages themselves may be strided, as in views of one [pages, 2, ...] tensor);
     block_table [B, cols] int32; context_lens [B] int32; parents [B,K] int32; ``scale`` defaults
-    to 1 / sqrt(D).  Node j's key and value lie at logical position context_lens + j.  Returns
-    out [B,K,Hq,D] of q's type."""
+    to 1 / sqrt(D).  Node j's key and value lie at logical position context_lens + j.  ``workspace``:
+    uint8 scratch of ``tree_attention_workspace_bytes``, allocated if not given.  Returns out
+    [B,K,Hq,D] of q's type."""
     B, K, H, D = q.shape
     P, ps, Hk, _ = k_cache.shape
-    dev = q.device
-    _expect("k_cache", k_cache, q.dtype, (P, ps, Hk, D), dev)
-    _expect("v_cache", v_cache, q.dtype, (P, ps, Hk, D), dev)
-    _expect("block_table", block_table, torch.int32, (B, block_table.shape[-1]), dev)
-    _expect("context_lens", context_lens, torch.int32, (B,), dev)
-    _expect("parents", parents, torch.int32, (B, K), dev)
-    desc = TreeAttentionDesc(B, K, H, Hk, D, _dtype_code(q), P, ps, block_table.shape[1],
-                             D ** -0.5 if scale is None else scale, _cache_stride("k_cache", k_cache),
-                             _cache_stride("v_cache", v_cache))
+    dt, dev, at = q.dtype, q.device, q.get_device()
+    code = _dtype_code(q)
+    qp = _expect("q", q, dt, (B, K, H, D), at)
+    kp, ks = _cache("k_cache", k_cache, dt, (P, ps, Hk, D), at)
+    vp, vs = _cache("v_cache", v_cache, dt, (P, ps, Hk, D), at)
+    cols = block_table.shape[-1]
+    table = _expect("block_table", block_table, _I32, (B, cols), at)
+    ctx = _expect("context_lens", context_lens, _I32, (B,), at)
+    par = _expect("parents", parents, _I32, (B, K), at)
+    desc = ctypes.byref(TreeAttentionDesc(B, K, H, Hk, D, code, P, ps, cols, D ** -0.5 if scale is None else scale, ks, vs))
     if out is None:
-        out = torch.empty((B, K, H, D), dtype=q.dtype, device=dev)
-        _keep_until_done(out, stream)
+        out = _fresh((B, K, H, D), dt, dev, stream)
+        op = out.data_ptr()
     else:
-        _expect("out", out, q.dtype, (B, K, H, D), dev)
+        op = _expect("out", out, dt, (B, K, H, D), at)
     lib = load()
     if workspace is None:
-        workspace = torch.empty(lib.kda_tree_attention_workspace_bytes(ctypes.byref(desc)), dtype=torch.uint8, device=dev)
-        _keep_until_done(workspace, stream)
-    at = lambda c: ctypes.c_void_p(c.data_ptr()) if c.numel() > 0 else None
-    st = lib.kda_tree_attention(ctypes.byref(desc), _ptr(q), at(k_cache), at(v_cache), _ptr(block_table),
-                                _ptr(context_lens), _ptr(parents), _ptr(out), _ptr(workspace),
-                                workspace.numel() * workspace.element_size(), _stream_handle(stream))
+        workspace = _fresh((lib.kda_tree_attention_workspace_bytes(desc),), torch.uint8, dev, stream)
+    st = lib.kda_tree_attention(desc, qp, kp, vp, table, ctx, par, op, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_tree_attention")
     return out
@@ -475,28 +498,19 @@ def tree_decode(q, k, v, g, beta, parents, state, out=None, writes=None, *, stre
     [B,H,dk,dv] fp32 is only read; ``prologue``: KDA_PROLOGUE_* bits; ``gate``: output gate logits
     [B,K,H,dv] fp32.  Returns (out, writes), both [B,K,H,dv] fp32; ``tree_commit`` takes writes."""
     B, K, H, dk = q.shape
-    dv, dev, f32 = v.shape[3], q.device, torch.float32
-    _expect("k", k, q.dtype, (B, K, H, dk), dev)
-    _expect("v", v, q.dtype, (B, K, H, dv), dev)
-    _expect("g", g, f32, (B, K, H, dk), dev)
-    _expect("beta", beta, f32, (B, K, H), dev)
-    _expect("parents", parents, torch.int32, (B, K), dev)
-    _expect("state", state, f32, (B, H, dk, dv), dev)
-    if gate is not None:
-        _expect("gate", gate, f32, (B, K, H, dv), dev)
+    dv, dt, dev, at = v.shape[3], q.dtype, q.device, q.get_device()
+    code = _dtype_code(q)
+    wide = (B, K, H, dv)
+    ins = (_expect("q", q, dt, (B, K, H, dk), at), _expect("k", k, dt, (B, K, H, dk), at), _expect("v", v, dt, wide, at),
+           _expect("g", g, _F32, (B, K, H, dk), at), _expect("beta", beta, _F32, (B, K, H), at),
+           _expect("parents", parents, _I32, (B, K), at), None if gate is None else _expect("gate", gate, _F32, wide, at),
+           _expect("state", state, _F32, (B, H, dk, dv), at))
     if out is None:
-        out = torch.empty((B, K, H, dv), dtype=f32, device=dev)
-        _keep_until_done(out, stream)
-    else:
-        _expect("out", out, f32, (B, K, H, dv), dev)
+        out = _fresh(wide, _F32, dev, stream)
     if writes is None:
-        writes = torch.empty((B, K, H, dv), dtype=f32, device=dev)
-        _keep_until_done(writes, stream)
-    else:
-        _expect("writes", writes, f32, (B, K, H, dv), dev)
-    st = load().kda_tree_decode(B, K, H, dk, dv, _dtype_code(q), int(prologue), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                _ptr(beta), _ptr(parents), _ptr(gate), _ptr(state), _ptr(out), _ptr(writes),
-                                _stream_handle(stream))
+        writes = _fresh(wide, _F32, dev, stream)
+    st = load().kda_tree_decode(B, K, H, dk, dv, code, prologue, *ins, _expect("out", out, _F32, wide, at),
+                                _expect("writes", writes, _F32, wide, at), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_tree_decode")
     return out, writes
@@ -507,14 +521,11 @@ def tree_commit(k, g, writes, path, n_accept, state, *, stream=None, check=True,
     ``kda_tree_commit``: k, g and ``prologue`` as given to ``tree_decode``, ``writes`` as it returned
     them; path [B,K] and n_accept [B] int32 as ``verify_drafts`` returns them.  Returns state."""
     B, K, H, dk = k.shape
-    dv, dev = state.shape[3], k.device
-    _expect("g", g, torch.float32, (B, K, H, dk), dev)
-    _expect("writes", writes, torch.float32, (B, K, H, dv), dev)
-    _expect("path", path, torch.int32, (B, K), dev)
-    _expect("n_accept", n_accept, torch.int32, (B,), dev)
-    _expect("state", state, torch.float32, (B, H, dk, dv), dev)
-    st = load().kda_tree_commit(B, K, H, dk, dv, _dtype_code(k), int(prologue), _ptr(k), _ptr(g), _ptr(writes),
-                                _ptr(path), _ptr(n_accept), _ptr(state), _stream_handle(stream))
+    dv, at = state.shape[3], k.get_device()
+    st = load().kda_tree_commit(B, K, H, dk, dv, _dtype_code(k), prologue, _expect("k", k, k.dtype, (B, K, H, dk), at),
+                                _expect("g", g, _F32, (B, K, H, dk), at), _expect("writes", writes, _F32, (B, K, H, dv), at),
+                                _expect("path", path, _I32, (B, K), at), _expect("n_accept", n_accept, _I32, (B,), at),
+                                _expect("state", state, _F32, (B, H, dk, dv), at), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_tree_commit")
     return state
@@ -528,23 +539,19 @@ def verify_drafts(target_probs, tokens, parents, uniforms, noise, draft_probs=No
     Returns (path [B,K] int32 with -1 after the kept nodes, n_accept [B] int32, next_token [B]
     int32)."""
     B, K1, V = target_probs.shape
-    K, dev, i32, f32 = K1 - 1, target_probs.device, torch.int32, torch.float32
-    _expect("target_probs", target_probs, f32, (B, K1, V), dev)
-    _expect("tokens", tokens, i32, (B, K), dev)
-    _expect("parents", parents, i32, (B, K), dev)
-    _expect("uniforms", uniforms, f32, (B, K), dev)
-    _expect("noise", noise, f32, (B, V), dev)
-    if draft_probs is not None:
-        _expect("draft_probs", draft_probs, f32, (B, K, V), dev)
-    path = torch.empty((B, K), dtype=i32, device=dev)
-    n_accept = torch.empty(B, dtype=i32, device=dev)
-    next_token = torch.empty(B, dtype=i32, device=dev)
-    if stream is not None:
-        for t in (path, n_accept, next_token):
-            _keep_until_done(t, stream)
-    st = load().kda_verify_drafts(B, K, V, _ptr(target_probs), _ptr(draft_probs), _ptr(tokens), _ptr(parents),
-                                  _ptr(uniforms), _ptr(noise), _ptr(path), _ptr(n_accept), _ptr(next_token),
-                                  _stream_handle(stream))
+    K, dev, at = K1 - 1, target_probs.device, target_probs.get_device()
+    target = _expect("target_probs", target_probs, _F32, (B, K1, V), at)
+    tok = _expect("tokens", tokens, _I32, (B, K), at)
+    par = _expect("parents", parents, _I32, (B, K), at)
+    uni = _expect("uniforms", uniforms, _F32, (B, K), at)
+    noi = _expect("noise", noise, _F32, (B, V), at)
+    dra = None if draft_probs is None else _expect("draft_probs", draft_probs, _F32, (B, K, V), at)
+    path = _fresh((B, K), _I32, dev, stream)
+    small = _fresh((2 * B,), _I32, dev, stream)
+    n_accept, next_token = small.split(B) if B else (small, small)
+    p = small.data_ptr()
+    st = load().kda_verify_drafts(B, K, V, target, dra, tok, par, uni, noi, path.data_ptr(), p, p + 4 * B,
+                                  _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_verify_drafts")
     return path, n_accept, next_token

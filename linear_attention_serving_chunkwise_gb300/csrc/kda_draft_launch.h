@@ -61,6 +61,27 @@ struct TreeAttnArgs {
     int* status;
 };
 
+// Sets up a kernel on the current device at its first call there (its dynamic shared memory, and
+// that it starts with `regs` registers a thread when that matters); later calls cost a lookup.
+struct KernelSetup {
+    unsigned long long done = 0;   // a bit per device; a race only repeats the set-up
+    template <typename F>
+    cudaError_t operator()(F* kernel, size_t smem, int regs = 0)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || (dev < 64 && (__atomic_load_n(&done, __ATOMIC_RELAXED) >> dev & 1))) return e;
+        if (regs) {
+            cudaFuncAttributes at;
+            if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess) return e;
+            if (at.numRegs != regs) return cudaErrorLaunchOutOfResources;
+        }
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
+        return cudaSuccess;
+    }
+};
+
 // the device status word of the current device (kda_api.cu)
 int* device_status_ptr();
 

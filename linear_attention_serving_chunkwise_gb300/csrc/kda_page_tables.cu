@@ -142,10 +142,9 @@ cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream)
 {
     const size_t smem = (size_t)(2 * a.batch + 1) * sizeof(int32_t);
     static_assert((2 * kPageTablesMaxBatch + 1) * 4 <= 227 * 1024 - 1024, "the scan fits shared memory");
-    if (smem > 47 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static KernelSetup setup;
+    const cudaError_t e = setup(page_tables_kernel, (2 * kPageTablesMaxBatch + 1) * sizeof(int32_t));
+    if (e != cudaSuccess) return e;
     const int grid = a.max_tokens > kTokensPerCta ? (int)(((long long)a.max_tokens + kTokensPerCta - 1) / kTokensPerCta) : 1;
     page_tables_kernel<<<grid, kThreads, smem, stream>>>(a);
     return cudaGetLastError();

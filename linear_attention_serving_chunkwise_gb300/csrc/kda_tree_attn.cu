@@ -184,7 +184,8 @@ cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
     const attn::Shape sh = {16 * TM, kBN, kSimtCtas, 1};
     if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     constexpr size_t smem = simt_smem<D, TM>();
-    cudaError_t e = cudaFuncSetAttribute(tree_attn_simt_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static KernelSetup setup;
+    cudaError_t e = setup(tree_attn_simt_kernel<D, TM>, smem);
     if (e != cudaSuccess) return e;
     tree_attn_simt_kernel<D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

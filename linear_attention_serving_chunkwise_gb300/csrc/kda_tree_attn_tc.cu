@@ -864,12 +864,9 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
         if (!make_map(&maps.k, a.k_cache, a.k_page_stride, a, maps.box_rows) || !make_map(&maps.v, a.v_cache, a.v_page_stride, a, maps.box_rows))
             return cudaErrorInvalidValue;
     }
-    // the register split needs the block to start with all 128 registers a thread
-    cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, kernel);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs != 128) return cudaErrorLaunchOutOfResources;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    // (the register split needs the block to start with all 128 registers a thread)
+    static KernelSetup setup;
+    cudaError_t e = setup(kernel, L::kBytes, 128);
     if (e != cudaSuccess) return e;
     kernel<<<sh.ctas, kThreads, L::kBytes, stream>>>(a, sh, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

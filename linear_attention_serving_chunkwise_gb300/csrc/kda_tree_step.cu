@@ -255,7 +255,8 @@ template <typename Tin, int D>
 cudaError_t launch_step(const TreeDecodeArgs& a, cudaStream_t stream)
 {
     const size_t smem = StepLayout<D>::floats(a.nodes) * sizeof(float);
-    const cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static KernelSetup setup;
+    const cudaError_t e = setup(tree_decode_kernel<Tin, D>, StepLayout<D>::floats(kTreeMaxNodes) * sizeof(float));
     if (e != cudaSuccess) return e;
     tree_decode_kernel<Tin, D><<<a.batch * a.num_heads, 2 * D, smem, stream>>>(a);
     return cudaGetLastError();
