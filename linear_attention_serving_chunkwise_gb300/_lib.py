@@ -375,7 +375,8 @@ def state_combine(transition, state_in, state_add, out=None, *, stream=None, che
 
 # ---- the draft step (include/kda.h) -----------------------------------------------------
 # These calls take a few microseconds on the GPU, so the marshalling is kept lean: pointers go
-# to ctypes as plain integers, the stream comes as its raw handle, small outputs share an allocation.
+# to ctypes as plain integers and the stream comes as its raw handle (outputs are allocations of
+# their own: a view of a fresh tensor costs three times an allocation).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -419,11 +420,9 @@ def page_tables(context_lens, new_lens, pages_held, block_table, free_pages, *, 
     table = _expect("block_table", block_table, _I32, (B, cols), at)
     free = _expect("free_pages", free_pages, _I32, (F,), at)
     slots = _fresh((max_tokens,), torch.int64, dev, stream)
-    small = _fresh((2 * B + 2,), _I32, dev, stream)
-    cu, held, taken = small.split((B + 1, B, 1))
-    p = small.data_ptr()
+    cu, held, taken = _fresh((B + 1,), _I32, dev, stream), _fresh((B,), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
     st = load().kda_page_tables(B, cols, F, page_size, max_tokens, ctx, new, had, table, free, slots.data_ptr(),
-                                p, p + 4 * (B + 1), p + 4 * (2 * B + 1), _stream_on(stream, at))
+                                cu.data_ptr(), held.data_ptr(), taken.data_ptr(), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_page_tables")
     return slots, cu, held, taken
@@ -547,11 +546,9 @@ def verify_drafts(target_probs, tokens, parents, uniforms, noise, draft_probs=No
     noi = _expect("noise", noise, _F32, (B, V), at)
     dra = None if draft_probs is None else _expect("draft_probs", draft_probs, _F32, (B, K, V), at)
     path = _fresh((B, K), _I32, dev, stream)
-    small = _fresh((2 * B,), _I32, dev, stream)
-    n_accept, next_token = small.split(B) if B else (small, small)
-    p = small.data_ptr()
-    st = load().kda_verify_drafts(B, K, V, target, dra, tok, par, uni, noi, path.data_ptr(), p, p + 4 * B,
-                                  _stream_on(stream, at))
+    n_accept, next_token = _fresh((B,), _I32, dev, stream), _fresh((B,), _I32, dev, stream)
+    st = load().kda_verify_drafts(B, K, V, target, dra, tok, par, uni, noi, path.data_ptr(), n_accept.data_ptr(),
+                                  next_token.data_ptr(), _stream_on(stream, at))
     if check and st != KDA_OK:
         raise KDAError(st, "kda_verify_drafts")
     return path, n_accept, next_token
