@@ -14,7 +14,10 @@
 // result does not depend on how the vocabulary is split.
 //
 // One thread-block cluster per sequence, the vocabulary split over its CTAs; each CTA repeats
-// the walk (K gathered probabilities) and scans its slice of the one row that is sampled.
+// the walk (K gathered probabilities, one warp) and scans its slice of the one row that is
+// sampled.  The quotient is formed only where it can win: rest / noise > best is first tested as
+// rest >= best (1 - 2^-21) noise, which no rounding can turn down wrongly, with the best of the
+// whole warp, so that after the first batch few elements get as far as a division.
 // Bound: HBM, 8 bytes (12 after a turned-down draft) per vocabulary entry.
 #include <cooperative_groups.h>
 
@@ -26,14 +29,12 @@ namespace cg = cooperative_groups;
 namespace kda {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMaxCluster = 8;      // the portable cluster size
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCluster = 8;         // the portable cluster size
+constexpr int kBatch = 4;           // entries a lane has in flight
 
 // larger score first, then the lower index; scores are >= 0, whose bits order like integers
-__device__ __forceinline__ uint64_t key_of(float score, int idx)
-{
-    return ((uint64_t)__float_as_uint(score) << 32) | (uint32_t)(0xffffffffu - (uint32_t)idx);
-}
+__device__ __forceinline__ uint64_t key_of(uint32_t score, int idx) { return ((uint64_t)score << 32) | (uint32_t)(0xffffffffu - (uint32_t)idx); }
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // What is not above zero (a negative zero or NaN too) counts as zero.
@@ -45,125 +46,205 @@ struct Walk {
     int n_kept, n_down, row, first_down, bad;
 };
 
-// Warp 0: the walk.  Lanes gather what every node's test needs, then lane 0 walks.
-__device__ void walk_tree(const VerifyArgs& a, int b, Walk& wk, float* sp, float* sq, int* stok, int* spar, float* su, int lane)
+// One warp: the walk.  A lane holds nodes lane and lane + 32; the children of the current node
+// are a ballot away and each test is a few shuffles.
+__device__ void walk_tree(const VerifyArgs& a, int b, Walk& wk, int lane)
 {
     const int K = a.nodes;
+    int par[2], tok[2];
+    float p[2] = {}, q[2] = {}, u[2] = {};
     bool bad = false;
-    for (int i = lane; i < K; i += 32) {
-        const int p = a.parents[(size_t)b * K + i], x = a.tokens[(size_t)b * K + i];
-        bool ok = p >= kTreePad && p < i;
-        if (p != kTreePad) ok = ok && x >= 0 && x < a.vocab;
-        spar[i] = p;
-        stok[i] = x;
-        su[i] = a.uniforms[(size_t)b * K + i];
-        if (ok && p != kTreePad) {
-            sp[i] = a.target[((size_t)b * (K + 1) + p + 1) * a.vocab + x];
-            if (a.draft) sq[i] = a.draft[((size_t)b * K + i) * a.vocab + x];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int i = lane + 32 * s;
+        par[s] = kTreePad;
+        tok[s] = -1;
+        if (i < K) {
+            par[s] = a.parents[(size_t)b * K + i];
+            tok[s] = a.tokens[(size_t)b * K + i];
+            u[s] = a.uniforms[(size_t)b * K + i];
         }
+        const bool there = par[s] != kTreePad, ok = par[s] >= kTreePad && par[s] < i && (!there || (tok[s] >= 0 && tok[s] < a.vocab));
         bad |= !ok;
-    }
-    __syncwarp();
-    if (!__any_sync(0xffffffffu, bad)) {
-        for (int i = lane; i < K; i += 32) {
-            const int p = spar[i];
-            if (p >= 0 && spar[p] == kTreePad) bad = true;                                  // hangs on an absent node
-            if (a.draft && p != kTreePad)                                                   // a draft row belongs to one child
-                for (int j = 0; j < i; ++j) bad |= spar[j] == p;
+        if (ok && there) {
+            p[s] = a.target[((size_t)b * (K + 1) + par[s] + 1) * a.vocab + tok[s]];
+            if (a.draft) q[s] = a.draft[((size_t)b * K + i) * a.vocab + tok[s]];
         }
+        if (!there) tok[s] = -1;
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) {
-        wk.bad = bad;
-        int cur = -1, n = 0, down = 0, first = -1;
-        float mass = 1.f;
-        if (!bad) {
-            for (int c = 0; c < K; ++c) {       // children come after their parents: one pass in index order
-                if (spar[c] != cur) continue;
-                const float p = sp[c];
+    if (!bad) {
+        // a node may not hang on an absent one; a draft row belongs to one child
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int src = max(par[s], 0), lo = __shfl_sync(0xffffffffu, par[0], src & 31), hi = __shfl_sync(0xffffffffu, par[1], src & 31);
+            bad |= par[s] >= 0 && (src < 32 ? lo : hi) == kTreePad;
+        }
+        if (a.draft) {
+            for (int x = -1; x < K; ++x)
+                bad |= __popc(__ballot_sync(0xffffffffu, par[0] == x)) + __popc(__ballot_sync(0xffffffffu, par[1] == x)) > 1;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+    }
+    int cur = -1, n = 0;
+    uint64_t down = 0;                                       // children of cur turned down
+    if (!bad) {
+        for (bool on = true; on;) {
+            uint64_t left = (uint64_t)__ballot_sync(0xffffffffu, par[0] == cur) | (uint64_t)__ballot_sync(0xffffffffu, par[1] == cur) << 32;
+            float mass = 1.f;
+            down = 0;
+            on = false;
+            for (; left; left &= left - 1) {
+                const int c = __ffsll((long long)left) - 1, src = c & 31;
+                const bool hi = c >= 32;
+                const int x = __shfl_sync(0xffffffffu, hi ? tok[1] : tok[0], src);
+                const float pc = __shfl_sync(0xffffffffu, hi ? p[1] : p[0], src), uc = __shfl_sync(0xffffffffu, hi ? u[1] : u[0], src),
+                            qc = __shfl_sync(0xffffffffu, hi ? q[1] : q[0], src);
                 bool keep;
                 if (a.draft) {
-                    keep = __fmul_rn(su[c], sq[c]) < p;
-                } else {
-                    bool again = false;          // a token turned down here before has no mass left
-                    for (int j = 0; j < down; ++j) again |= wk.tok[j] == stok[c];
-                    if (again) continue;
-                    keep = __fmul_rn(su[c], mass) < p;
+                    keep = __fmul_rn(uc, qc) < pc;
+                } else {                                     // a token turned down here before has no mass left
+                    const uint64_t same = (uint64_t)__ballot_sync(0xffffffffu, tok[0] == x) | (uint64_t)__ballot_sync(0xffffffffu, tok[1] == x) << 32;
+                    if (same & down) {
+                        down |= 1ull << c;
+                        continue;
+                    }
+                    keep = __fmul_rn(uc, mass) < pc;
                 }
                 if (keep) {
-                    wk.kept[n++] = c;
+                    if (lane == 0) wk.kept[n] = c;
+                    ++n;
                     cur = c;
-                    mass = 1.f;
-                    down = 0;
-                    first = -1;
-                } else {
-                    wk.tok[down++] = stok[c];
-                    if (first < 0) first = c;
-                    mass = __fsub_rn(mass, p);
+                    on = true;
+                    break;
                 }
+                down |= 1ull << c;
+                mass = __fsub_rn(mass, pc);
             }
         }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const int i = lane + 32 * s;
+        if (i < 64 && (down >> i & 1)) wk.tok[__popcll(down & ((1ull << i) - 1))] = tok[s];
+    }
+    if (lane == 0) {
+        wk.bad = bad;
         wk.n_kept = n;
-        wk.n_down = down;
-        wk.first_down = first;
+        wk.n_down = __popcll(down);
+        wk.first_down = down ? __ffsll((long long)down) - 1 : -1;
         wk.row = cur + 1;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a)
+// A streaming load that stays where it is written: a batch's go out together.
+__device__ __forceinline__ float load_now(const float* p)
+{
+    float x;
+    asm volatile("ld.global.cs.f32 %0, [%1];" : "=f"(x) : "l"(__cvta_generic_to_global(p)));
+    return x;
+}
+
+// A lane's best so far, and the least score worth a division: the warp's best less 2^-21 of it.
+struct Best {
+    uint32_t score = 0;
+    int idx = 0;
+    float worth = 0.f;
+};
+
+// One entry that may win: r is what is left of it before the turned-down tokens are taken out.
+__device__ __forceinline__ void offer(Best& best, float r, float noise, int v, const Walk& wk, int n_down)
+{
+    const uint32_t s = __float_as_uint(__fdiv_rn(r, noise));
+    if (s <= best.score) return;
+    for (int j = 0; j < n_down; ++j)
+        if (wk.tok[j] == v) return;
+    best.score = s;
+    best.idx = v;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a)
 {
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int b = blockIdx.x / C, t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int V = a.vocab;
     __shared__ Walk wk;
-    __shared__ float sp[kTreeMaxNodes], sq[kTreeMaxNodes], su[kTreeMaxNodes];
-    __shared__ int stok[kTreeMaxNodes], spar[kTreeMaxNodes];
-    __shared__ uint64_t red[kThreads / 32];
-    __shared__ uint64_t best[2][kMaxCluster];   // by pass; rank 0's copy collects, every rank gets the result
+    __shared__ uint64_t red[kWarps];
+    __shared__ uint64_t best[2][kCluster];      // by pass; every rank's copy collects all ranks' bests
 
-    if (w == 0) walk_tree(a, b, wk, sp, sq, stok, spar, su, lane);
-    cl.sync();                                 // every CTA of the cluster runs: its shared memory can be written
+    if (w == 0) walk_tree(a, b, wk, lane);
+    cl.sync();                                  // every CTA of the cluster runs: its shared memory can be written
 
     const float* prow = a.target + ((size_t)b * (a.nodes + 1) + wk.row) * V;
     const float* nrow = a.noise + (size_t)b * V;
-    const int per = (V + C - 1) / C;
-    const int v0 = rank * per, v1 = min(V, v0 + per);
+    const int per = ((V + C - 1) / C + 3) & ~3;
+    const int v0 = min(V, rank * per), v1 = min(V, v0 + per);
     uint64_t win = 0;
     if (!wk.bad) {
         // pass 0 draws from what is left; pass 1 from the row itself, when nothing is left
         for (int pass = 0; pass < 2; ++pass) {
             const float* qrow = pass == 0 && a.draft && wk.first_down >= 0 ? a.draft + ((size_t)b * a.nodes + wk.first_down) * V : nullptr;
             const int n_down = pass == 0 && !a.draft ? wk.n_down : 0;
-            uint64_t mine = 0;
-            for (int v = v0 + t; v < v1; v += kThreads) {
+            Best mine;
+            // whole batches of the CTA first, then the rest of the slice entry by entry
+            constexpr int kStep = kThreads * kBatch;
+            const int steps = (v1 - v0) / kStep, at = v0 + w * 32 * kBatch + lane;
+            for (int i = 0; i < steps; ++i) {
+                const int v = at + i * kStep;
+                float p[kBatch], q[kBatch], e[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) p[k] = load_now(prow + v + 32 * k);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) e[k] = load_now(nrow + v + 32 * k);
+                if (qrow) {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) q[k] = load_now(qrow + v + 32 * k);
+                }
+                bool any = false;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    p[k] = above_zero(p[k]);
+                    if (qrow) p[k] = above_zero(__fsub_rn(p[k], q[k]));
+                    any |= p[k] >= mine.worth * e[k];
+                }
+                if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (p[k] >= mine.worth * e[k]) offer(mine, p[k], e[k], v + 32 * k, wk, n_down);
+                mine.worth = __uint_as_float(__reduce_max_sync(0xffffffffu, mine.score)) * (1.f - 0x1p-21f);
+            }
+#pragma unroll 4
+            for (int v = v0 + steps * kStep + t; v < v1; v += kThreads) {
                 float r = above_zero(prow[v]);
                 if (qrow) r = above_zero(__fsub_rn(r, qrow[v]));
-                for (int j = 0; j < n_down; ++j) r = wk.tok[j] == v ? 0.f : r;
-                mine = max64(mine, key_of(__fdiv_rn(r, nrow[v]), v));
+                const float n = nrow[v];
+                if (r >= mine.worth * n) offer(mine, r, n, v, wk, n_down);
             }
+            uint64_t key = key_of(mine.score, mine.idx);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mine = max64(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-            if (lane == 0) red[w] = mine;
+            for (int o = 16; o > 0; o >>= 1) key = max64(key, __shfl_xor_sync(0xffffffffu, key, o));
+            if (lane == 0) red[w] = key;
             __syncthreads();
-            if (t < C) {                       // thread r hands this CTA's best to rank r
+            if (t < C) {                        // thread r hands this CTA's best to rank r
                 uint64_t m = 0;
-                for (int i = 0; i < kThreads / 32; ++i) m = max64(m, red[i]);
+                for (int i = 0; i < kWarps; ++i) m = max64(m, red[i]);
                 *cl.map_shared_rank(&best[pass][rank], t) = m;
             }
             cl.sync();
             win = 0;
             for (int i = 0; i < C; ++i) win = max64(win, best[pass][i]);
-            if ((win >> 32) != 0) break;       // the same in every CTA of the cluster
+            if ((win >> 32) != 0) break;        // the same in every CTA of the cluster
         }
     }
-    cl.sync();                                 // no CTA leaves while another may still write to it
+    cl.sync();                                  // no CTA leaves while another may still write to it
     if (rank == 0) {
         const int n = wk.bad ? 0 : wk.n_kept;
         for (int i = t; i < a.nodes; i += kThreads) a.path[(size_t)b * a.nodes + i] = i < n ? wk.kept[i] : -1;
         if (t == 0) {
             a.n_accept[b] = n;
-            a.next_token[b] = wk.bad ? -1 : (int)(0xffffffffu - (uint32_t)win);
+            // (a row without any probability: the lowest index, as an argmax over zeros has it)
+            a.next_token[b] = wk.bad ? -1 : (win >> 32) ? (int)(0xffffffffu - (uint32_t)win) : 0;
             if (wk.bad) report_status(a.status, kDevBadSeqlens);
         }
     }
@@ -171,9 +252,14 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a)
 
 }  // namespace
 
+// A CTA spends about 4 us on the walk and on meeting its cluster, whatever its slice; past this
+// many CTAs (some 7 to an SM, 4 at a time) a cluster is made smaller and its slices longer.
+constexpr long long kMostCtas = 1100;
+
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream)
 {
-    int cluster = kMaxCluster;
+    int cluster = kCluster;
+    while (cluster > 1 && (long long)a.batch * cluster > kMostCtas) cluster /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.batch * cluster);
     cfg.blockDim = dim3(kThreads);
