@@ -87,7 +87,9 @@ int* device_status_ptr();
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+// dk = 128 on the tensor cores (kda_tree_step_tc.cu), dk = 64 on the CUDA cores
 cudaError_t launch_tree_decode(const TreeDecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_decode_tc(const TreeDecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t stream);
 // bf16 on the tensor cores (kda_tree_attn_tc.cu), fp32 on the CUDA cores
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream);

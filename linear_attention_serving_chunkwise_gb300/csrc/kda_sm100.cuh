@@ -140,6 +140,15 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, ui
         : "memory");
 }
 
+// Untiled load of `bytes` (a multiple of 16) from and to 16-byte boundaries.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(smem_dst)),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // Start moving a 3-D tile into L2 (no completion to wait for).
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2)
 {

@@ -33,7 +33,7 @@
 
 #include <mutex>
 
-#include "kda_sm100.cuh"
+#include "kda_draft_sm100.cuh"
 #include "kda_tree_attn.cuh"
 
 namespace kda {
@@ -47,7 +47,6 @@ constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads sta
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
 constexpr int kCtas = 152;                          // one to an SM
 constexpr int kHead = 2;                            // a unit's fixed cost (Q, first tile, epilogue), in tiles
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
 
@@ -78,25 +77,6 @@ struct Maps {
     int box_rows;
 };
 
-struct Waiter {
-    int* status;
-    bool alive = true;
-    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity)
-    {
-        if (!alive) return;
-        if (mbar_try_wait(bar, parity)) return;
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait_sleep(bar, parity, 1000)) {
-            if (globaltimer_ns() - t0 > kWaitNs) {
-                alive = false;
-                report_status(status, kDevTimeout);
-                return;
-            }
-        }
-    }
-};
-
-__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there)
 {
     const int n = there ? 16 : 0;                   // 0: the 16 bytes become zero
@@ -105,12 +85,6 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there)
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7f80u) != 0x7f80u; }
 
 // ------------------------------------------------------------------ the cache rows
@@ -281,7 +255,7 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
     // no load is in flight when the block ends, whatever became of its reader
     if (w == 0)
         for (uint32_t i = fill > (uint32_t)L::kSlots ? fill - L::kSlots : 0; i < fill; ++i)
-            mbar_wait_bounded(&sm.kv_full[i % L::kSlots], (i / L::kSlots) & 1, kWaitNs);
+            mbar_wait_bounded(&sm.kv_full[i % L::kSlots], (i / L::kSlots) & 1, kDraftWaitNs);
     if (bad_page && lane == 0) report_status(a.status, kDevBadSeqlens);
 }
 

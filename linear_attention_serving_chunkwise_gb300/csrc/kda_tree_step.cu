@@ -273,7 +273,7 @@ cudaError_t launch_commit(const TreeCommitArgs& a, cudaStream_t stream)
 
 cudaError_t launch_tree_decode(const TreeDecodeArgs& a, cudaStream_t stream)
 {
-    if (a.dk == 128) return a.bf16 ? launch_step<__nv_bfloat16, 128>(a, stream) : launch_step<float, 128>(a, stream);
+    if (a.dk == 128) return launch_tree_decode_tc(a, stream);
     return a.bf16 ? launch_step<__nv_bfloat16, 64>(a, stream) : launch_step<float, 64>(a, stream);
 }
 
