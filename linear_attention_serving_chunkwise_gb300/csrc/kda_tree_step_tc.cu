@@ -29,7 +29,10 @@ namespace {
 using namespace sm100;
 
 constexpr int D = 128, NB = 16;                     // channels; nodes of a block
-constexpr int kPrepThreads = 256, kThreads = 18 * 32, kCtas = 152;
+constexpr int kPrepThreads = 256, kThreads = 640, kCtas = 152;
+// registers a thread: at launch, and after the split (substitution, state, preparation, the rest)
+constexpr int kStartRegs = 96, kSolveRegs = 96, kSplitRegs = 104, kPrepRegs = 112, kRestRegs = 40;
+static_assert(128 * (kSolveRegs + kSplitRegs + kRestRegs) + kPrepThreads * kPrepRegs <= kThreads * kStartRegs, "register split");
 constexpr int kHalf = 64 * D * 4;                   // bytes of half a state
 constexpr int kETile = 4 * NB * D * 4;              // k hi, q hi, k lo, q lo rows of a block
 constexpr float kLog2e = 1.4426950408889634f;
@@ -42,8 +45,8 @@ struct Plan {
 
 struct Shared {
     uint64_t s_full[4], s_empty[4], t_full, t_empty, e_full[2], e_empty[2], d_full[2], d_empty[2], a_full[2], a_empty[2];
+    alignas(16) signed char parent[kTreeMaxNodes];   // -1: none
     TreeSmem tree[2];       // of the preparation, of the substitution
-    signed char parent[kTreeMaxNodes];
     uint32_t tmem;
 };
 
@@ -57,28 +60,31 @@ __host__ __device__ constexpr Plan plan_of(int K, int states, int tiles)
     p.g = at; at += K * D * 4;
     p.q = at; at += NB * D * 4;
     p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
-    p.w = at; at += K > NB ? K * D * 4 : 0;
+    p.w = at; at += K * D * 4;
+    at = (at + 15) & ~15;
     p.shared = at;
     p.bytes = at + (int)sizeof(Shared);
     return p;
 }
 
-__device__ __forceinline__ float to_tf32(float x)
-{
-    uint32_t y;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
-    return __uint_as_float(y);
-}
+// x rounded to tf32 (half away from zero), in two integer operations: the conversion
+// instruction runs at a quarter of their rate and would be the state split's bound.
+__device__ __forceinline__ float to_tf32(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
+// the same for an operand of the tensor core, which drops the low bits itself
+__device__ __forceinline__ float as_tf32(float x) { return __uint_as_float(__float_as_uint(x) + 0x1000u); }
 
 struct Units {              // this CTA's, one after the other (a sequence's heads stay together)
     int first, last;
 };
 
 // ------------------------------------------------------------------ preparation
+// (Loops are unrolled no more than their registers ask for: the five roles run side by side, and
+// straight-line code for each would be fetched anew for every block.)
 template <typename Tin>
 __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
 {
-    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, c = t & 127, odd = t >> 7;
+    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, c = t & 127;
+    const bool decays = t < D;                      // one half of the threads has the decays, the other k and q
     float* sk = reinterpret_cast<float*>(base + pl.k);
     float* sg = reinterpret_cast<float*>(base + pl.g);
     float* sq = reinterpret_cast<float*>(base + pl.q);
@@ -86,18 +92,23 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
     Waiter wait{a.status};
     uint32_t block = 0;
     int tree_of = -1;
-    // a block's k, q and g: node 2 r + odd, channel c; the next block's are loaded a block ahead
-    float rk[NB / 2], rq[NB / 2], rg[NB / 2];
+    // channel c of a block's nodes, loaded a block ahead and kept as it lies in memory (a conversion
+    // would wait for the load); past the last node the last one again
+    float rg[NB];
+    Tin rk[NB], rq[NB];
     auto load = [&](int u, int i0) {
+        u = min(u, un.last - 1);
         const int b = u / H, h = u - b * H;
+        const size_t at = ((size_t)b * K * H + h) * D + c;
 #pragma unroll
-        for (int r = 0; r < NB / 2; ++r) {
-            const int i = i0 + 2 * r + odd;
-            if (u >= un.last || i >= K) continue;
-            const size_t at = (((size_t)b * K + i) * H + h) * D + c;
-            rk[r] = to_f32(__ldg(static_cast<const Tin*>(a.k) + at));
-            rq[r] = to_f32(__ldg(static_cast<const Tin*>(a.q) + at));
-            rg[r] = __ldg(a.g + at);
+        for (int i = 0; i < NB; ++i) {
+            const size_t o = at + (size_t)(min(i0 + i, K - 1) * H) * D;
+            if (decays) {
+                rg[i] = a.g[o];
+            } else {
+                rk[i] = static_cast<const Tin*>(a.k)[o];
+                rq[i] = static_cast<const Tin*>(a.q)[o];
+            }
         }
     };
     load(un.first, 0);
@@ -107,20 +118,34 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             bar_sync(1, kPrepThreads);              // the last tree has been read
             if (w == 0) {
                 tree_masks(tree, a.parents + (size_t)b * K, K, lane);
-                for (int i = lane; i < K; i += 32) sm.parent[i] = (signed char)max(a.parents[(size_t)b * K + i], -1);
+                for (int i = lane; i < K; i += 32) {
+                    const uint64_t above = tree.anc[i] & ~(1ull << i);
+                    sm.parent[i] = tree.ok && above ? (signed char)(63 - __clzll((long long)above)) : (signed char)-1;
+                }
             }
             tree_of = b;
         }
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
             const int n = min(NB, K - i0), eb = block % pl.tiles, ab = block & 1;
             bar_sync(1, kPrepThreads);              // the last block's k, q and G have been read; the tree is there
+            if (decays) {
+                // G in powers of two: a node's is its parent's and its own g; parents come first
+                const uint4 up = *reinterpret_cast<const uint4*>(sm.parent + i0);
+                const uint32_t ups[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
-            for (int r = 0; r < NB / 2; ++r) {
-                const int i = 2 * r + odd;
-                if (i >= n) continue;
-                sk[(i0 + i) * D + c] = rk[r];
-                sq[i * D + c] = rq[r];
-                sg[(i0 + i) * D + c] = g_of(rg[r], a.prologue) * kLog2e;
+                for (int i = 0; i < NB; ++i) {
+                    if (i >= n) break;
+                    const int p = (int)(signed char)(ups[i / 4] >> 8 * (i % 4));
+                    const float own = g_of(rg[i], a.prologue) * kLog2e;
+                    sg[(i0 + i) * D + c] = p >= 0 ? own + sg[p * D + c] : own;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (i >= n) break;
+                    sk[(i0 + i) * D + c] = to_f32(rk[i]);
+                    sq[i * D + c] = to_f32(rq[i]);
+                }
             }
             if (i0 + NB < K) load(u, i0 + NB);
             else load(u + 1, 0);
@@ -135,35 +160,28 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     const float inv = l2_inv(ss);
                     *x = make_float4(l2_scale(v.x, inv, Tin{}), l2_scale(v.y, inv, Tin{}), l2_scale(v.z, inv, Tin{}), l2_scale(v.w, inv, Tin{}));
                 }
+                bar_sync(1, kPrepThreads);
             }
-            // G (in powers of two): a thread per channel adds the parent's, parents come first
-            if (t < D && tree.ok) {
-                for (int i = 0; i < n; ++i) {
-                    const int p = sm.parent[i0 + i];
-                    if (p >= 0) sg[(i0 + i) * D + c] += sg[p * D + c];
-                }
-            }
-            bar_sync(1, kPrepThreads);
             // the B operand
             if (block >= (uint32_t)pl.tiles) wait(&sm.e_empty[eb], (block / pl.tiles - 1) & 1);
             uint8_t* et = base + pl.states * kHalf + eb * kETile;
-#pragma unroll
-            for (int r = 0; r < NB / 2; ++r) {
-                const int i = 2 * r + odd;
-                if (i >= n) continue;               // (rows of the block beyond its nodes: columns of D that nobody reads)
+#pragma unroll 2
+            for (int i = t >> 7; i < n; i += 2) {   // (rows of the block beyond its nodes: columns of D that nobody reads)
                 const float e = ex2(sg[(i0 + i) * D + c]);
                 const float kx = sk[(i0 + i) * D + c] * e, qx = sq[i * D + c] * e, kh = to_tf32(kx), qh = to_tf32(qx);
                 *reinterpret_cast<float*>(et + sw128_off_f32(i, c, 4 * NB)) = kh;
                 *reinterpret_cast<float*>(et + sw128_off_f32(NB + i, c, 4 * NB)) = qh;
-                *reinterpret_cast<float*>(et + sw128_off_f32(2 * NB + i, c, 4 * NB)) = to_tf32(kx - kh);
-                *reinterpret_cast<float*>(et + sw128_off_f32(3 * NB + i, c, 4 * NB)) = to_tf32(qx - qh);
+                *reinterpret_cast<float*>(et + sw128_off_f32(2 * NB + i, c, 4 * NB)) = as_tf32(kx - kh);
+                *reinterpret_cast<float*>(et + sw128_off_f32(3 * NB + i, c, 4 * NB)) = as_tf32(qx - qh);
             }
             fence_proxy_async_smem();
             mbar_arrive(&sm.e_full[eb]);
-            // the ancestor pairs: a warp to a node, a lane to four channels
+            // the ancestor pairs: a warp to a node, a lane to four channels; entry e of the node's list is its
+            // e-th ancestor from the context on, the last is the node itself
             if (block >= 2) wait(&sm.a_empty[ab], (block / 2 - 1) & 1);
             float2* ap = reinterpret_cast<float2*>(base + pl.ap) + ab * NB * KP;
-            for (int i = w; i < n && tree.ok; i += kPrepThreads / 32) {
+#pragma unroll 1
+            for (int i = w; i < n; i += kPrepThreads / 32) {
                 const float4 ki = reinterpret_cast<const float4*>(sk + (i0 + i) * D)[lane], qi = reinterpret_cast<const float4*>(sq + i * D)[lane],
                              gi = reinterpret_cast<const float4*>(sg + (i0 + i) * D)[lane];
                 auto dots = [&](int j, float& da, float& dp) {
@@ -172,11 +190,14 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     da = fmaf(x, ki.x, fmaf(y, ki.y, fmaf(z, ki.z, v * ki.w)));
                     dp = fmaf(x, qi.x, fmaf(y, qi.y, fmaf(z, qi.z, v * qi.w)));
                 };
-                for (uint64_t m = tree.anc[i0 + i]; m;) {
+                int e = 0;
+#pragma unroll 1
+                for (uint64_t m = tree.ok ? tree.anc[i0 + i] : 0ull; m; e += 2) {
                     // two pairs at a time; their four sums end in lanes 0, 8, 16 and 24
                     const int j0 = __ffsll((long long)m) - 1;
                     m &= m - 1;
-                    const int j1 = m ? __ffsll((long long)m) - 1 : j0;
+                    const bool two = m != 0;
+                    const int j1 = two ? __ffsll((long long)m) - 1 : j0;
                     m &= m - 1;
                     float a0, p0, a1, p1;
                     dots(j0, a0, p0);
@@ -189,7 +210,7 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     z += __shfl_xor_sync(0xffffffffu, mid ? x : y, 8);
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                    if ((lane & 7) == 0) reinterpret_cast<float*>(ap + i * KP + (up ? j1 : j0))[mid ? 1 : 0] = z;
+                    if ((lane & 7) == 0 && (two || !up)) reinterpret_cast<float*>(ap + i * KP + e + (up ? 1 : 0))[mid ? 1 : 0] = z;
                 }
             }
             __syncwarp();
@@ -222,7 +243,7 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
                 for (int i = 0; i < 32; ++i) {
                     const float x = src[(c0 + i) * D];
                     hi[i] = to_tf32(x);
-                    lo[i] = to_tf32(x - hi[i]);
+                    lo[i] = as_tf32(x - hi[i]);
                 }
                 tmem_st32(tmem_addr(sm.tmem, quad, kColHi + 64 * k + c0), hi);
                 tmem_st32(tmem_addr(sm.tmem, quad, kColLo + 64 * k + c0), lo);
@@ -277,20 +298,22 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
 {
     const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31;
     const uint32_t quad = 32 * (t >> 5);
-    float* sw = reinterpret_cast<float*>(base + pl.w) + t;      // this channel's writes, when a later block needs them
+    float* sw = reinterpret_cast<float*>(base + pl.w) + t;      // this channel's writes
     TreeSmem& tree = sm.tree[1];
     Waiter wait{a.status};
     uint32_t block = 0;
     int tree_of = -1;
-    float rv[NB], rb[NB];                                       // a block's v and beta, loaded a block ahead
-    auto load = [&](int u, int i0) {
+    constexpr int Q = 4;                                        // nodes at a time
+    Tin rv[Q];                                                  // their v and beta, loaded four nodes ahead
+    float rb[Q];
+    auto load = [&](int u, int i) {                             // (past the last node the last one again)
+        u = min(u, un.last - 1);
         const int b = u / H, h = u - b * H;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            if (u >= un.last || i0 + i >= K) continue;
-            const size_t tok = ((size_t)b * K + i0 + i) * H + h;
-            rv[i] = to_f32(__ldg(static_cast<const Tin*>(a.v) + tok * D + t));
-            rb[i] = __ldg(a.beta + tok);
+        for (int k = 0; k < Q; ++k) {
+            const size_t tok = ((size_t)b * K + min(i + k, K - 1)) * H + h;
+            rv[k] = static_cast<const Tin*>(a.v)[tok * D + t];
+            rb[k] = a.beta[tok];
         }
     };
     load(un.first, 0);
@@ -308,59 +331,88 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
             const uint32_t db = block & 1;
             wait(&sm.d_full[db], (block / 2) & 1);
-            __syncwarp();
-            tc_fence_after_sync();
-            float x[32], x2[32];                                // X of 16 nodes, then Y; hi and lo parts of E
-            tmem_ld32(tmem_addr(sm.tmem, quad, kColD + 64 * db), x);
-            tmem_ld32(tmem_addr(sm.tmem, quad, kColD + 64 * db + 32), x2);
-            tmem_wait_ld();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.d_empty[db]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += x2[i];
-            float v[NB], beta[NB], wr[NB];
-#pragma unroll
-            for (int i = 0; i < NB; ++i) { v[i] = rv[i]; beta[i] = rb[i]; }
-            if (i0 + NB < K) load(u, i0 + NB);
-            else load(u + 1, 0);
             wait(&sm.a_full[db], (block / 2) & 1);
             __syncwarp();
+            tc_fence_after_sync();
+            const uint32_t td = tmem_addr(sm.tmem, quad, kColD + 64 * db);
             const float2* ap = reinterpret_cast<const float2*>(base + pl.ap) + db * NB * KP;
+#pragma unroll 1
+            for (int g0 = 0; g0 < min(NB, K - i0); g0 += Q) {
+                float x[Q], y[Q], x2[Q], y2[Q];                 // X and Y, and their parts from the low half of E
+                tmem_ld4(td + g0, x);
+                tmem_ld4(td + NB + g0, y);
+                tmem_ld4(td + 2 * NB + g0, x2);
+                tmem_ld4(td + 3 * NB + g0, y2);
+                float v[Q], beta[Q];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                if (i0 + i >= K || !tree.ok) break;
-                const size_t at = (((size_t)b * K + i0 + i) * H + h) * D + t;
-                const uint64_t m = tree.anc[i0 + i];
-                const uint32_t in = (uint32_t)(m >> i0) & 0xffffu;
-                float xi = x[i], yi = x[NB + i];
-                for (uint64_t out = m & ((1ull << i0) - 1); out; out &= out - 1) {   // ancestors in earlier blocks
-                    const int j = __ffsll((long long)out) - 1;
-                    const float2 c = ap[i * KP + j];
-                    const float wj = sw[j * D];
-                    xi = fmaf(c.x, wj, xi);
-                    yi = fmaf(c.y, wj, yi);
-                }
+                for (int k = 0; k < Q; ++k) { v[k] = to_f32(rv[k]); beta[k] = beta_of(rb[k], a.prologue); }
+                if (i0 + g0 + Q < K) load(u, i0 + g0 + Q);
+                else load(u + 1, 0);
+                tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < i; ++j) {                   // and in this one
-                    const float2 c = ap[i * KP + i0 + j];
-                    if (in >> j & 1) {
-                        xi = fmaf(c.x, wr[j], xi);
-                        yi = fmaf(c.y, wr[j], yi);
+                for (int k = 0; k < Q; ++k) {
+                    const int i = i0 + g0 + k;
+                    if (i >= K || !tree.ok) break;
+                    const size_t at = (((size_t)b * K + i) * H + h) * D + t;
+                    const float2* row = ap + (g0 + k) * KP;
+                    uint64_t m = tree.anc[i];
+                    const bool there = m != 0;
+                    m &= ~(1ull << i);
+                    float xi = x[k] + x2[k], yi = y[k] + y2[k];
+                    int e = 0;
+#pragma unroll 1
+                    while (m) {                                 // ancestors, two at a time
+                        const float4 c = *reinterpret_cast<const float4*>(row + e);
+                        const int j0 = __ffsll((long long)m) - 1;
+                        m &= m - 1;
+                        const float w0 = sw[j0 * D];
+                        xi = fmaf(c.x, w0, xi);
+                        yi = fmaf(c.y, w0, yi);
+                        ++e;
+                        if (m) {
+                            const float w1 = sw[(__ffsll((long long)m) - 1) * D];
+                            m &= m - 1;
+                            xi = fmaf(c.z, w1, xi);
+                            yi = fmaf(c.w, w1, yi);
+                            ++e;
+                        }
                     }
+                    float wi = beta[k] * (v[k] - xi);
+                    yi = fmaf(row[e].y, wi, yi);
+                    if (!there) wi = yi = 0.f;                  // an absent node
+                    if (a.gate) yi = gate1(yi, __ldg(a.gate + at));
+                    sw[i * D] = wi;
+                    a.writes[at] = wi;
+                    a.out[at] = yi;
                 }
-                wr[i] = beta_of(beta[i], a.prologue) * (v[i] - xi);
-                yi = fmaf(ap[i * KP + i0 + i].y, wr[i], yi);
-                if (!(in >> i & 1)) wr[i] = yi = 0.f;           // an absent node
-                if (a.gate) yi = gate1(yi, __ldg(a.gate + at));
-                a.writes[at] = wr[i];
-                a.out[at] = yi;
-                if (K > NB) sw[(i0 + i) * D] = wr[i];
             }
+            tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.a_empty[db]);
+            if (lane == 0) {
+                mbar_arrive(&sm.d_empty[db]);
+                mbar_arrive(&sm.a_empty[db]);
+            }
         }
     }
+}
+
+// ------------------------------------------------------------------ the states, by one thread
+__device__ __forceinline__ void copy_states(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base)
+{
+    Waiter wait{a.status};
+    const char* src = reinterpret_cast<const char*>(a.state) + (size_t)un.first * 2 * kHalf;
+    const uint32_t halves = 2 * (un.last - un.first);
+    uint32_t i = 0;
+    for (; i < halves; ++i) {
+        const uint32_t s = i % pl.states;
+        if (i >= (uint32_t)pl.states) wait(&sm.s_empty[s], (i / pl.states - 1) & 1);
+        if (!wait.alive) break;
+        mbar_arrive_expect_tx(&sm.s_full[s], kHalf);
+        bulk_load(base + s * kHalf, src + (size_t)i * kHalf, kHalf, &sm.s_full[s]);
+    }
+    // no load is in flight when the block ends, whatever became of its reader
+    for (uint32_t j = i > (uint32_t)pl.states ? i - pl.states : 0; j < i; ++j)
+        mbar_wait_bounded(&sm.s_full[j % pl.states], (j / pl.states) & 1, kDraftWaitNs);
 }
 
 template <typename Tin>
@@ -394,25 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     if (warp < 4) {
         solve<Tin>(a, pl, un, sm, base, t);
     } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSplitRegs));
         split(a, pl, un, sm, base, t - 128);
     } else if (warp < 16) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrepRegs));
         prepare<Tin>(a, pl, un, sm, base, t - 256);
-    } else if (warp == 17) {
-        multiply(a, pl, un, sm, base);
-    } else if (elect_one()) {
-        Waiter wait{a.status};
-        const char* src = reinterpret_cast<const char*>(a.state) + (size_t)un.first * 2 * kHalf;
-        const uint32_t halves = 2 * (un.last - un.first);
-        uint32_t i = 0;
-        for (; i < halves; ++i) {
-            const uint32_t s = i % pl.states;
-            if (i >= (uint32_t)pl.states) wait(&sm.s_empty[s], (i / pl.states - 1) & 1);
-            if (!wait.alive) break;
-            mbar_arrive_expect_tx(&sm.s_full[s], kHalf);
-            bulk_load(base + s * kHalf, src + (size_t)i * kHalf, kHalf, &sm.s_full[s]);
-        }
-        // no load is in flight when the block ends, whatever became of its reader
-        for (uint32_t j = i > (uint32_t)pl.states ? i - pl.states : 0; j < i; ++j) mbar_wait_bounded(&sm.s_full[j % pl.states], (j / pl.states) & 1, kDraftWaitNs);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+        if (warp == 17) multiply(a, pl, un, sm, base);
+        if (warp == 16 && elect_one()) copy_states(a, pl, un, sm, base);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -439,7 +481,7 @@ cudaError_t launch(const TreeDecodeArgs& a, cudaStream_t stream)
 {
     const Plan p = choose_plan(a.nodes);
     static KernelSetup setup;
-    const cudaError_t e = setup(tree_decode_tc_kernel<Tin>, 232448);
+    const cudaError_t e = setup(tree_decode_tc_kernel<Tin>, 232448, kStartRegs);   // (the split needs its start)
     if (e != cudaSuccess) return e;
     const int total = a.batch * a.num_heads;
     tree_decode_tc_kernel<Tin><<<total < kCtas ? total : kCtas, kThreads, p.bytes, stream>>>(a, p);
