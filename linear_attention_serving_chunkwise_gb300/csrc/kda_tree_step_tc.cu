@@ -10,14 +10,15 @@
 // forward substitution over the nodes runs there in registers, one thread per channel.
 //
 // Warp roles of a persistent CTA, each ahead of the next by its buffers:
-//     16        copies states (32 KB halves, 2 to 4 in flight: HBM's latency is covered by these)
+//     16        copies states in quarters of 16 KB (what keeps HBM busy), 18 the nodes' k, q, g and v,
+//               rows of 256 or 512 bytes: no other warp loads them, so none waits for memory
 //     4 - 7     split a state into tensor memory
 //     8 - 15    prepare a block: G along the paths, e^G k and e^G q split into the B operand, and
 //               A_ij = <e^{G_i - G_j} k_i, k_j>, P_ij = <e^{G_i - G_j} q_i, k_j> on the ancestor pairs
 //               alone, each exponential of a difference <= 0 (a factored e^{-G_j} would overflow)
 //     17        issues the products
 //     0 - 3     substitution and outputs
-// Bound: HBM (one read of the state) up to about 16 nodes, then the pairs of the preparation.
+// Bound: the warps' issue slots (about 11 K instructions a block) beside HBM's one read of the state.
 // Every wait is bounded (Waiter).
 #include "kda_draft_launch.h"
 #include "kda_draft_sm100.cuh"
@@ -33,37 +34,45 @@ constexpr int kPrepThreads = 256, kThreads = 640, kCtas = 152;
 // registers a thread: at launch, and after the split (substitution, state, preparation, the rest)
 constexpr int kStartRegs = 96, kSolveRegs = 96, kSplitRegs = 104, kPrepRegs = 112, kRestRegs = 40;
 static_assert(128 * (kSolveRegs + kSplitRegs + kRestRegs) + kPrepThreads * kPrepRegs <= kThreads * kStartRegs, "register split");
-constexpr int kHalf = 64 * D * 4;                   // bytes of half a state
+constexpr int kQuarter = 32 * D * 4;                // bytes of a quarter of a state
 constexpr int kETile = 4 * NB * D * 4;              // k hi, q hi, k lo, q lo rows of a block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kColHi = 0, kColLo = 128, kColD = 256;   // D: two buffers of 64 columns
+constexpr int kMostStates = 8;
 
+// Buffers and where they lie (bytes from the start of shared memory).
 struct Plan {
-    int states, tiles;      // halves of the state ring, B tiles
-    int k, g, q, ap, w, shared, bytes;   // offsets
+    int tiles, raws, keys, states;   // B tiles; blocks of q, g and v; units of k; state quarters
+    int raw, k, g, ap, w, state, shared, bytes;
 };
 
 struct Shared {
-    uint64_t s_full[4], s_empty[4], t_full, t_empty, e_full[2], e_empty[2], d_full[2], d_empty[2], a_full[2], a_empty[2];
+    uint64_t s_full[kMostStates], s_empty[kMostStates], r_full[2], r_empty[2], k_empty[2], t_full, t_empty, e_full[2], e_empty[2],
+        d_full[2], d_empty[2], a_full[2], a_empty[2];
     alignas(16) signed char parent[kTreeMaxNodes];   // -1: none
+    alignas(16) unsigned char above[kTreeMaxNodes][kTreeMaxNodes];   // a node's ancestors from the context on, without itself
     TreeSmem tree[2];       // of the preparation, of the substitution
+    float kn[kTreeMaxNodes], qn[NB];   // reciprocal norms (input prologue)
     uint32_t tmem;
 };
 
-__host__ __device__ constexpr Plan plan_of(int K, int states, int tiles)
+__host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, int keys)
 {
     Plan p = {};
-    p.states = states;
     p.tiles = tiles;
-    int at = states * kHalf + tiles * kETile;
-    p.k = at; at += K * D * 4;
+    p.raws = raws;
+    p.keys = keys;
+    int at = tiles * kETile;
+    p.raw = at; at += raws * NB * D * (2 * esz + 4);   // of each block g, then q, then v
+    p.k = at; at += keys * K * D * esz;
     p.g = at; at += K * D * 4;
-    p.q = at; at += NB * D * 4;
-    p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
     p.w = at; at += K * D * 4;
-    at = (at + 15) & ~15;
-    p.shared = at;
-    p.bytes = at + (int)sizeof(Shared);
+    p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
+    p.shared = (at + 15) & ~15;
+    p.state = (p.shared + (int)sizeof(Shared) + 127) & ~127;
+    const int fit = (232448 - p.state) / kQuarter;
+    p.states = fit > kMostStates ? kMostStates : fit;
+    p.bytes = p.state + p.states * kQuarter;
     return p;
 }
 
@@ -78,41 +87,27 @@ struct Units {              // this CTA's, one after the other (a sequence's hea
 };
 
 // ------------------------------------------------------------------ preparation
-// (Loops are unrolled no more than their registers ask for: the five roles run side by side, and
-// straight-line code for each would be fetched anew for every block.)
+// four channels as they lie in shared memory
+__device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 four(const __nv_bfloat16* p)
+{
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// (Loops are unrolled little: the roles run side by side, and straight-line code for each would
+// be fetched anew for every block.)
 template <typename Tin>
 __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
 {
-    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, c = t & 127;
-    const bool decays = t < D;                      // one half of the threads has the decays, the other k and q
-    float* sk = reinterpret_cast<float*>(base + pl.k);
+    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, W = kPrepThreads / 32;
+    const bool norm = a.prologue & kProQK;
     float* sg = reinterpret_cast<float*>(base + pl.g);
-    float* sq = reinterpret_cast<float*>(base + pl.q);
     TreeSmem& tree = sm.tree[0];
     Waiter wait{a.status};
-    uint32_t block = 0;
+    uint32_t block = 0, unit = 0;
     int tree_of = -1;
-    // channel c of a block's nodes, loaded a block ahead and kept as it lies in memory (a conversion
-    // would wait for the load); past the last node the last one again
-    float rg[NB];
-    Tin rk[NB], rq[NB];
-    auto load = [&](int u, int i0) {
-        u = min(u, un.last - 1);
-        const int b = u / H, h = u - b * H;
-        const size_t at = ((size_t)b * K * H + h) * D + c;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const size_t o = at + (size_t)(min(i0 + i, K - 1) * H) * D;
-            if (decays) {
-                rg[i] = a.g[o];
-            } else {
-                rk[i] = static_cast<const Tin*>(a.k)[o];
-                rq[i] = static_cast<const Tin*>(a.q)[o];
-            }
-        }
-    };
-    load(un.first, 0);
-    for (int u = un.first; u < un.last; ++u) {
+    for (int u = un.first; u < un.last; ++u, ++unit) {
         const int b = u / H;
         if (b != tree_of) {
             bar_sync(1, kPrepThreads);              // the last tree has been read
@@ -125,67 +120,78 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             }
             tree_of = b;
         }
+        const Tin* sk = reinterpret_cast<const Tin*>(base + pl.k) + (unit % pl.keys) * K * D;
+        // a row's four channels of this lane, normalised where the prologue says so
+        auto row4 = [&](const Tin* p, float inv) {
+            float4 x = four(p + 4 * lane);
+            if (norm) x = make_float4(l2_scale(x.x, inv, Tin{}), l2_scale(x.y, inv, Tin{}), l2_scale(x.z, inv, Tin{}), l2_scale(x.w, inv, Tin{}));
+            return x;
+        };
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
-            const int n = min(NB, K - i0), eb = block % pl.tiles, ab = block & 1;
-            bar_sync(1, kPrepThreads);              // the last block's k, q and G have been read; the tree is there
-            if (decays) {
-                // G in powers of two: a node's is its parent's and its own g; parents come first
-                const uint4 up = *reinterpret_cast<const uint4*>(sm.parent + i0);
-                const uint32_t ups[4] = {up.x, up.y, up.z, up.w};
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    if (i >= n) break;
-                    const int p = (int)(signed char)(ups[i / 4] >> 8 * (i % 4));
-                    const float own = g_of(rg[i], a.prologue) * kLog2e;
-                    sg[(i0 + i) * D + c] = p >= 0 ? own + sg[p * D + c] : own;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    if (i >= n) break;
-                    sk[(i0 + i) * D + c] = to_f32(rk[i]);
-                    sq[i * D + c] = to_f32(rq[i]);
-                }
-            }
-            if (i0 + NB < K) load(u, i0 + NB);
-            else load(u + 1, 0);
-            bar_sync(1, kPrepThreads);
-            if (a.prologue & kProQK) {
-                for (int i = w; i < 2 * n; i += kPrepThreads / 32) {
-                    float4* x = reinterpret_cast<float4*>(i & 1 ? sq + (i >> 1) * D : sk + (i0 + (i >> 1)) * D) + lane;
-                    float4 v = *x;
+            const int n = min(NB, K - i0), eb = block % pl.tiles, ab = block & 1, rb = block % pl.raws;
+            const float* graw = reinterpret_cast<const float*>(base + pl.raw + rb * NB * D * (2 * (int)sizeof(Tin) + 4));
+            const Tin* sq = reinterpret_cast<const Tin*>(graw + NB * D);
+            wait(&sm.r_full[rb], (block / pl.raws) & 1);
+            bar_sync(1, kPrepThreads);              // the last block's G has been read; the tree is there
+            if (norm) {
+                for (int i = w; i < 2 * n; i += W) {
+                    const float4 v = four((i & 1 ? sq + (i >> 1) * D : sk + (i0 + (i >> 1)) * D) + 4 * lane);
                     float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float inv = l2_inv(ss);
-                    *x = make_float4(l2_scale(v.x, inv, Tin{}), l2_scale(v.y, inv, Tin{}), l2_scale(v.z, inv, Tin{}), l2_scale(v.w, inv, Tin{}));
+                    if (lane == 0) (i & 1 ? sm.qn[i >> 1] : sm.kn[i0 + (i >> 1)]) = l2_inv(ss);
                 }
-                bar_sync(1, kPrepThreads);
             }
-            // the B operand
+            // G in powers of two: a node's is its parent's and its own g; parents come first
+            if (w == 0) {
+                float4* g4 = reinterpret_cast<float4*>(sg) + lane;
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) {
+                    const int p = sm.parent[i0 + i];
+                    const float4 own = reinterpret_cast<const float4*>(graw)[i * (D / 4) + lane];
+                    const float4 up = p >= 0 ? g4[p * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    g4[(i0 + i) * (D / 4)] = make_float4(fmaf(g_of(own.x, a.prologue), kLog2e, up.x), fmaf(g_of(own.y, a.prologue), kLog2e, up.y),
+                                                         fmaf(g_of(own.z, a.prologue), kLog2e, up.z), fmaf(g_of(own.w, a.prologue), kLog2e, up.w));
+                }
+            }
+            bar_sync(1, kPrepThreads);
+            // the B operand: a warp to a node's row, a lane to four channels (16 bytes of each of its four rows,
+            // 16 rows apart: the swizzle, which goes by the row's last three bits, is theirs in common)
             if (block >= (uint32_t)pl.tiles) wait(&sm.e_empty[eb], (block / pl.tiles - 1) & 1);
-            uint8_t* et = base + pl.states * kHalf + eb * kETile;
-#pragma unroll 2
-            for (int i = t >> 7; i < n; i += 2) {   // (rows of the block beyond its nodes: columns of D that nobody reads)
-                const float e = ex2(sg[(i0 + i) * D + c]);
-                const float kx = sk[(i0 + i) * D + c] * e, qx = sq[i * D + c] * e, kh = to_tf32(kx), qh = to_tf32(qx);
-                *reinterpret_cast<float*>(et + sw128_off_f32(i, c, 4 * NB)) = kh;
-                *reinterpret_cast<float*>(et + sw128_off_f32(NB + i, c, 4 * NB)) = qh;
-                *reinterpret_cast<float*>(et + sw128_off_f32(2 * NB + i, c, 4 * NB)) = as_tf32(kx - kh);
-                *reinterpret_cast<float*>(et + sw128_off_f32(3 * NB + i, c, 4 * NB)) = as_tf32(qx - qh);
+            uint8_t* et = base + eb * kETile + (lane >> 3) * (4 * NB * 128);
+#pragma unroll 1
+            for (int i = w; i < n; i += W) {        // (rows of the block beyond its nodes: columns of D that nobody reads)
+                const float4 g = four(sg + (i0 + i) * D + 4 * lane), k = row4(sk + (i0 + i) * D, norm ? sm.kn[i0 + i] : 1.f),
+                             q = row4(sq + i * D, norm ? sm.qn[i] : 1.f);
+                const float e[4] = {ex2(g.x), ex2(g.y), ex2(g.z), ex2(g.w)}, kk[4] = {k.x, k.y, k.z, k.w}, qq[4] = {q.x, q.y, q.z, q.w};
+                float kh[4], kl[4], qh[4], ql[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const float kx = kk[s] * e[s], qx = qq[s] * e[s];
+                    kh[s] = to_tf32(kx);
+                    kl[s] = as_tf32(kx - kh[s]);
+                    qh[s] = to_tf32(qx);
+                    ql[s] = as_tf32(qx - qh[s]);
+                }
+                float4* at = reinterpret_cast<float4*>(et + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+                at[0] = make_float4(kh[0], kh[1], kh[2], kh[3]);
+                at[NB * 8] = make_float4(qh[0], qh[1], qh[2], qh[3]);
+                at[2 * NB * 8] = make_float4(kl[0], kl[1], kl[2], kl[3]);
+                at[3 * NB * 8] = make_float4(ql[0], ql[1], ql[2], ql[3]);
             }
             fence_proxy_async_smem();
             mbar_arrive(&sm.e_full[eb]);
             // the ancestor pairs: a warp to a node, a lane to four channels; entry e of the node's list is its
             // e-th ancestor from the context on, the last is the node itself
             if (block >= 2) wait(&sm.a_empty[ab], (block / 2 - 1) & 1);
+            __syncwarp();
             float2* ap = reinterpret_cast<float2*>(base + pl.ap) + ab * NB * KP;
 #pragma unroll 1
-            for (int i = w; i < n; i += kPrepThreads / 32) {
-                const float4 ki = reinterpret_cast<const float4*>(sk + (i0 + i) * D)[lane], qi = reinterpret_cast<const float4*>(sq + i * D)[lane],
-                             gi = reinterpret_cast<const float4*>(sg + (i0 + i) * D)[lane];
+            for (int i = W - 1 - w; i < n; i += W) {
+                const float4 ki = row4(sk + (i0 + i) * D, norm ? sm.kn[i0 + i] : 1.f), qi = row4(sq + i * D, norm ? sm.qn[i] : 1.f),
+                             gi = four(sg + (i0 + i) * D + 4 * lane);
                 auto dots = [&](int j, float& da, float& dp) {
-                    const float4 kj = reinterpret_cast<const float4*>(sk + j * D)[lane], gj = reinterpret_cast<const float4*>(sg + j * D)[lane];
+                    const float4 kj = row4(sk + j * D, norm ? sm.kn[j] : 1.f), gj = four(sg + j * D + 4 * lane);
                     const float x = ex2(gi.x - gj.x) * kj.x, y = ex2(gi.y - gj.y) * kj.y, z = ex2(gi.z - gj.z) * kj.z, v = ex2(gi.w - gj.w) * kj.w;
                     da = fmaf(x, ki.x, fmaf(y, ki.y, fmaf(z, ki.z, v * ki.w)));
                     dp = fmaf(x, qi.x, fmaf(y, qi.y, fmaf(z, qi.z, v * qi.w)));
@@ -214,7 +220,11 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.a_full[ab]);
+            if (lane == 0) {
+                mbar_arrive(&sm.a_full[ab]);
+                mbar_arrive(&sm.r_empty[rb]);
+                if (i0 + NB >= K) mbar_arrive(&sm.k_empty[unit % pl.keys]);
+            }
         }
     }
 }
@@ -225,31 +235,29 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
     const int lane = t & 31, dv = t;                // lane of tensor memory = value channel
     const uint32_t quad = 32 * (t >> 5);
     Waiter wait{a.status};
-    uint32_t half = 0, unit = 0;
+    uint32_t s = 0, phase = 0, unit = 0;
     for (int u = un.first; u < un.last; ++u, ++unit) {
-        for (int k = 0; k < 2; ++k, ++half) {
-            const uint32_t s = half % pl.states;
-            wait(&sm.s_full[s], (half / pl.states) & 1);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            wait(&sm.s_full[s], phase);
             if (k == 0 && unit) {
                 wait(&sm.t_empty, (unit - 1) & 1);
                 tc_fence_after_sync();
             }
             __syncwarp();
-            const float* src = reinterpret_cast<const float*>(base + s * kHalf) + dv;
-#pragma unroll 1
-            for (int c0 = 0; c0 < 64; c0 += 32) {
-                float hi[32], lo[32];
+            const float* src = reinterpret_cast<const float*>(base + pl.state + s * kQuarter) + dv;
+            float hi[32], lo[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float x = src[(c0 + i) * D];
-                    hi[i] = to_tf32(x);
-                    lo[i] = as_tf32(x - hi[i]);
-                }
-                tmem_st32(tmem_addr(sm.tmem, quad, kColHi + 64 * k + c0), hi);
-                tmem_st32(tmem_addr(sm.tmem, quad, kColLo + 64 * k + c0), lo);
+            for (int i = 0; i < 32; ++i) {
+                const float x = src[i * D];
+                hi[i] = to_tf32(x);
+                lo[i] = as_tf32(x - hi[i]);
             }
+            tmem_st32(tmem_addr(sm.tmem, quad, kColHi + 32 * k), hi);
+            tmem_st32(tmem_addr(sm.tmem, quad, kColLo + 32 * k), lo);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_empty[s]);
+            if (++s == (uint32_t)pl.states) { s = 0; phase ^= 1; }
         }
         tmem_wait_st();
         tc_fence_before_sync();
@@ -262,7 +270,7 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
 __device__ __forceinline__ void multiply(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base)
 {
     Waiter wait{a.status};
-    const uint32_t tm = sm.tmem, tiles = smem_u32(base) + pl.states * kHalf;
+    const uint32_t tm = sm.tmem, tiles = smem_u32(base);
     uint32_t block = 0, unit = 0;
     for (int u = un.first; u < un.last; ++u, ++unit) {
         wait(&sm.t_full, unit & 1);
@@ -304,19 +312,14 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
     uint32_t block = 0;
     int tree_of = -1;
     constexpr int Q = 4;                                        // nodes at a time
-    Tin rv[Q];                                                  // their v and beta, loaded four nodes ahead
-    float rb[Q];
-    auto load = [&](int u, int i) {                             // (past the last node the last one again)
+    const size_t step = (size_t)H * D;                          // from node to node of out, writes and the gate
+    // beta of node (lane % 16) of a block, loaded a block ahead (past the last node the last one again)
+    auto beta_at = [&](int u, int i0) {
         u = min(u, un.last - 1);
         const int b = u / H, h = u - b * H;
-#pragma unroll
-        for (int k = 0; k < Q; ++k) {
-            const size_t tok = ((size_t)b * K + min(i + k, K - 1)) * H + h;
-            rv[k] = static_cast<const Tin*>(a.v)[tok * D + t];
-            rb[k] = a.beta[tok];
-        }
+        return a.beta[((size_t)b * K + min(i0 + (lane & 15), K - 1)) * H + h];
     };
-    load(un.first, 0);
+    float next_beta = beta_at(un.first, 0);
     for (int u = un.first; u < un.last; ++u) {
         const int b = u / H, h = u - b * H;
         if (b != tree_of) {
@@ -327,17 +330,28 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
             }
             tree_of = b;
             bar_sync(2, 128);
+            if (t < K) {
+                int e = 0;
+                for (uint64_t m = tree.anc[t] & ~(1ull << t); m; m &= m - 1) sm.above[t][e++] = (unsigned char)(__ffsll((long long)m) - 1);
+            }
+            bar_sync(2, 128);
         }
+        size_t at = ((size_t)b * K * H + h) * D + t;
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
-            const uint32_t db = block & 1;
+            const uint32_t db = block & 1, rb = block % pl.raws;
+            const float beta16 = beta_of(next_beta, a.prologue);
+            next_beta = i0 + NB < K ? beta_at(u, i0 + NB) : beta_at(u + 1, 0);
+            const Tin* sv = reinterpret_cast<const Tin*>(base + pl.raw + rb * NB * D * (2 * (int)sizeof(Tin) + 4) + NB * D * (4 + (int)sizeof(Tin))) + t;
+            wait(&sm.r_full[rb], (block / pl.raws) & 1);
             wait(&sm.d_full[db], (block / 2) & 1);
             wait(&sm.a_full[db], (block / 2) & 1);
             __syncwarp();
             tc_fence_after_sync();
             const uint32_t td = tmem_addr(sm.tmem, quad, kColD + 64 * db);
-            const float2* ap = reinterpret_cast<const float2*>(base + pl.ap) + db * NB * KP;
+            const float2* row = reinterpret_cast<const float2*>(base + pl.ap) + db * NB * KP;
+            const int n = min(NB, K - i0);
 #pragma unroll 1
-            for (int g0 = 0; g0 < min(NB, K - i0); g0 += Q) {
+            for (int g0 = 0; g0 < n; g0 += Q) {
                 float x[Q], y[Q], x2[Q], y2[Q];                 // X and Y, and their parts from the low half of E
                 tmem_ld4(td + g0, x);
                 tmem_ld4(td + NB + g0, y);
@@ -345,45 +359,56 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
                 tmem_ld4(td + 3 * NB + g0, y2);
                 float v[Q], beta[Q];
 #pragma unroll
-                for (int k = 0; k < Q; ++k) { v[k] = to_f32(rv[k]); beta[k] = beta_of(rb[k], a.prologue); }
-                if (i0 + g0 + Q < K) load(u, i0 + g0 + Q);
-                else load(u + 1, 0);
+                for (int k = 0; k < Q; ++k) {
+                    v[k] = to_f32(sv[min(g0 + k, n - 1) * D]);
+                    beta[k] = __shfl_sync(0xffffffffu, beta16, g0 + k);
+                }
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < Q; ++k) {
                     const int i = i0 + g0 + k;
                     if (i >= K || !tree.ok) break;
-                    const size_t at = (((size_t)b * K + i) * H + h) * D + t;
-                    const float2* row = ap + (g0 + k) * KP;
-                    uint64_t m = tree.anc[i];
-                    const bool there = m != 0;
-                    m &= ~(1ull << i);
+                    const uint64_t m = tree.anc[i];
+                    const int cnt = __popcll(m) - 1;            // ancestors; -1 for an absent node
                     float xi = x[k] + x2[k], yi = y[k] + y2[k];
-                    int e = 0;
+                    // four ancestors at a time; what lies in the lists past the last is not used
 #pragma unroll 1
-                    while (m) {                                 // ancestors, two at a time
-                        const float4 c = *reinterpret_cast<const float4*>(row + e);
-                        const int j0 = __ffsll((long long)m) - 1;
-                        m &= m - 1;
-                        const float w0 = sw[j0 * D];
-                        xi = fmaf(c.x, w0, xi);
-                        yi = fmaf(c.y, w0, yi);
-                        ++e;
-                        if (m) {
-                            const float w1 = sw[(__ffsll((long long)m) - 1) * D];
-                            m &= m - 1;
-                            xi = fmaf(c.z, w1, xi);
-                            yi = fmaf(c.w, w1, yi);
-                            ++e;
+                    for (int e = 0; e < cnt; e += 4) {
+                        const uint32_t j = *reinterpret_cast<const uint32_t*>(&sm.above[i][e]);
+                        const float4 c0 = *reinterpret_cast<const float4*>(row + e);
+                        const float w0 = sw[(j & 63) * D];
+                        xi = fmaf(c0.x, w0, xi);
+                        yi = fmaf(c0.y, w0, yi);
+                        if (e + 1 < cnt) {
+                            const float w1 = sw[(j >> 8 & 63) * D];
+                            xi = fmaf(c0.z, w1, xi);
+                            yi = fmaf(c0.w, w1, yi);
+                        }
+                        if (e + 2 < cnt) {
+                            const float4 c1 = *reinterpret_cast<const float4*>(row + e + 2);
+                            const float w2 = sw[(j >> 16 & 63) * D];
+                            xi = fmaf(c1.x, w2, xi);
+                            yi = fmaf(c1.y, w2, yi);
+                            if (e + 3 < cnt) {
+                                const float w3 = sw[(j >> 24 & 63) * D];
+                                xi = fmaf(c1.z, w3, xi);
+                                yi = fmaf(c1.w, w3, yi);
+                            }
                         }
                     }
-                    float wi = beta[k] * (v[k] - xi);
-                    yi = fmaf(row[e].y, wi, yi);
-                    if (!there) wi = yi = 0.f;                  // an absent node
+                    float wi = 0.f;
+                    if (cnt >= 0) {
+                        wi = beta[k] * (v[k] - xi);
+                        yi = fmaf(row[cnt].y, wi, yi);
+                    } else {
+                        yi = 0.f;
+                    }
                     if (a.gate) yi = gate1(yi, __ldg(a.gate + at));
                     sw[i * D] = wi;
                     a.writes[at] = wi;
                     a.out[at] = yi;
+                    at += step;
+                    row += KP;
                 }
             }
             tc_fence_before_sync();
@@ -391,28 +416,68 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
             if (lane == 0) {
                 mbar_arrive(&sm.d_empty[db]);
                 mbar_arrive(&sm.a_empty[db]);
+                mbar_arrive(&sm.r_empty[rb]);
             }
         }
     }
 }
 
-// ------------------------------------------------------------------ the states, by one thread
+// ------------------------------------------------------------------ copies
+// the states, by one thread
 __device__ __forceinline__ void copy_states(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base)
 {
     Waiter wait{a.status};
-    const char* src = reinterpret_cast<const char*>(a.state) + (size_t)un.first * 2 * kHalf;
-    const uint32_t halves = 2 * (un.last - un.first);
+    const char* src = reinterpret_cast<const char*>(a.state) + (size_t)un.first * 4 * kQuarter;
+    const uint32_t total = 4 * (un.last - un.first);
     uint32_t i = 0;
-    for (; i < halves; ++i) {
+    for (; i < total; ++i) {
         const uint32_t s = i % pl.states;
         if (i >= (uint32_t)pl.states) wait(&sm.s_empty[s], (i / pl.states - 1) & 1);
         if (!wait.alive) break;
-        mbar_arrive_expect_tx(&sm.s_full[s], kHalf);
-        bulk_load(base + s * kHalf, src + (size_t)i * kHalf, kHalf, &sm.s_full[s]);
+        mbar_arrive_expect_tx(&sm.s_full[s], kQuarter);
+        bulk_load(base + pl.state + s * kQuarter, src + (size_t)i * kQuarter, kQuarter, &sm.s_full[s]);
     }
     // no load is in flight when the block ends, whatever became of its reader
     for (uint32_t j = i > (uint32_t)pl.states ? i - pl.states : 0; j < i; ++j)
         mbar_wait_bounded(&sm.s_full[j % pl.states], (j / pl.states) & 1, kDraftWaitNs);
+}
+
+// a block's rows of k (into its unit's buffer), g, q and v, by one warp, a lane to a row
+template <typename Tin>
+__device__ __forceinline__ void copy_nodes(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int lane)
+{
+    constexpr int E = (int)sizeof(Tin), kRow = D * E;
+    const int K = a.nodes, H = a.num_heads;
+    Waiter wait{a.status};
+    uint32_t block = 0, unit = 0;
+    bool go = true;
+    for (int u = un.first; u < un.last && go; ++u, ++unit) {
+        const int b = u / H, h = u - b * H;
+        const uint32_t kb = unit % pl.keys;
+        if (unit >= (uint32_t)pl.keys) wait(&sm.k_empty[kb], (unit / pl.keys - 1) & 1);
+        for (int i0 = 0; i0 < K && go; i0 += NB) {
+            const int n = min(NB, K - i0);
+            const uint32_t rb = block % pl.raws;
+            if (block >= (uint32_t)pl.raws) wait(&sm.r_empty[rb], (block / pl.raws - 1) & 1);
+            go = __all_sync(0xffffffffu, wait.alive);
+            if (!go) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.r_full[rb], n * (3 * kRow + D * 4));
+            __syncwarp();
+            uint8_t* raw = base + pl.raw + rb * NB * D * (2 * E + 4);
+            for (int x = lane; x < 64; x += 32) {
+                const int i = x & 15, what = x >> 4;
+                if (i >= n) continue;
+                const size_t at = (((size_t)b * K + i0 + i) * H + h) * D;
+                if (what == 0) bulk_load(raw + i * D * 4, a.g + at, D * 4, &sm.r_full[rb]);
+                else if (what == 1) bulk_load(raw + NB * D * 4 + i * kRow, static_cast<const Tin*>(a.q) + at, kRow, &sm.r_full[rb]);
+                else if (what == 2) bulk_load(raw + NB * D * 4 + (NB + i) * kRow, static_cast<const Tin*>(a.v) + at, kRow, &sm.r_full[rb]);
+                else bulk_load(base + pl.k + (kb * K + i0 + i) * kRow, static_cast<const Tin*>(a.k) + at, kRow, &sm.r_full[rb]);
+            }
+            ++block;
+        }
+    }
+    for (uint32_t j = block > (uint32_t)pl.raws ? block - pl.raws : 0; j < block; ++j)
+        mbar_wait_bounded(&sm.r_full[j % pl.raws], (j / pl.raws) & 1, kDraftWaitNs);
 }
 
 template <typename Tin>
@@ -426,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
         tmem_relinquish();
     }
     if (t == 0) {
-        for (int i = 0; i < 4; ++i) { mbar_init(&sm.s_full[i], 1); mbar_init(&sm.s_empty[i], 4); }
+        for (int i = 0; i < kMostStates; ++i) { mbar_init(&sm.s_full[i], 1); mbar_init(&sm.s_empty[i], 4); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.e_full[i], kPrepThreads);
             mbar_init(&sm.e_empty[i], 1);
@@ -434,6 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
             mbar_init(&sm.d_empty[i], 4);
             mbar_init(&sm.a_full[i], kPrepThreads / 32);
             mbar_init(&sm.a_empty[i], 4);
+            mbar_init(&sm.r_full[i], 1);
+            mbar_init(&sm.r_empty[i], kPrepThreads / 32 + 4);
+            mbar_init(&sm.k_empty[i], kPrepThreads / 32);
         }
         mbar_init(&sm.t_full, 4);
         mbar_init(&sm.t_empty, 1);
@@ -455,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
         if (warp == 17) multiply(a, pl, un, sm, base);
         if (warp == 16 && elect_one()) copy_states(a, pl, un, sm, base);
+        if (warp == 18) copy_nodes<Tin>(a, pl, un, sm, base, t & 31);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -463,23 +532,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     if (warp == 17) tmem_dealloc(sm.tmem, 512);
 }
 
-// As many state halves and B tiles as fit: two tiles let the preparation run a block ahead of the
-// products, and the states are what keeps HBM busy (three halves cover its latency at its full rate).
-Plan choose_plan(int K)
+// Buffers for K nodes: everything double while that leaves the states six quarters (96 KB in
+// flight cover HBM's latency at its full rate), else as much of it as leaves them three.
+constexpr Plan choose_plan(int K, int esz)
 {
-    constexpr int options[][2] = {{4, 2}, {3, 2}, {2, 2}, {3, 1}, {2, 1}};
+    constexpr int options[5][4] = {{2, 2, 2, 6}, {2, 2, 1, 4}, {1, 2, 2, 4}, {1, 2, 1, 3}, {1, 1, 1, 3}};
     for (const auto& o : options) {
-        const Plan p = plan_of(K, o[0], o[1]);
-        if (p.bytes <= 232448) return p;
+        const Plan p = plan_of(K, esz, o[0], o[1], o[2]);
+        if (p.states >= o[3]) return p;
     }
     return {};
 }
-static_assert(plan_of(kTreeMaxNodes, 2, 1).bytes <= 232448, "the largest tree fits");
+constexpr bool all_fit()
+{
+    for (int K = 1; K <= kTreeMaxNodes; ++K)
+        if (choose_plan(K, 2).bytes == 0 || choose_plan(K, 4).bytes == 0) return false;
+    return true;
+}
+static_assert(all_fit(), "every tree has a plan");
 
 template <typename Tin>
 cudaError_t launch(const TreeDecodeArgs& a, cudaStream_t stream)
 {
-    const Plan p = choose_plan(a.nodes);
+    const Plan p = choose_plan(a.nodes, (int)sizeof(Tin));
     static KernelSetup setup;
     const cudaError_t e = setup(tree_decode_tc_kernel<Tin>, 232448, kStartRegs);   // (the split needs its start)
     if (e != cudaSuccess) return e;
