@@ -17,7 +17,8 @@
 //               A_ij = <e^{G_i - G_j} k_i, k_j>, P_ij = <e^{G_i - G_j} q_i, k_j> on the ancestor pairs
 //               alone, each exponential of a difference <= 0 (a factored e^{-G_j} would overflow)
 //     17        issues the products
-//     0 - 3     substitution and outputs
+//     0 - 3, 20 - 23   substitution and outputs: a unit of one block each in turn (the substitution
+//               is a chain of short steps, the longest of the roles); larger trees the first alone
 // Bound: the warps' issue slots (about 11 K instructions a block) beside HBM's one read of the state.
 // Every wait is bounded (Waiter).
 #include "kda_draft_launch.h"
@@ -30,10 +31,10 @@ namespace {
 using namespace sm100;
 
 constexpr int D = 128, NB = 16;                     // channels; nodes of a block
-constexpr int kPrepThreads = 256, kThreads = 640, kCtas = 152;
+constexpr int kPrepThreads = 256, kThreads = 768, kCtas = 152;
 // registers a thread: at launch, and after the split (substitution, state, preparation, the rest)
-constexpr int kStartRegs = 96, kSolveRegs = 96, kSplitRegs = 104, kPrepRegs = 112, kRestRegs = 40;
-static_assert(128 * (kSolveRegs + kSplitRegs + kRestRegs) + kPrepThreads * kPrepRegs <= kThreads * kStartRegs, "register split");
+constexpr int kStartRegs = 80, kSolveRegs = 88, kSplitRegs = 88, kPrepRegs = 88, kRestRegs = 40;
+static_assert(128 * (2 * kSolveRegs + kSplitRegs + kRestRegs) + kPrepThreads * kPrepRegs <= kThreads * kStartRegs, "register split");
 constexpr int kQuarter = 32 * D * 4;                // bytes of a quarter of a state
 constexpr int kETile = 4 * NB * D * 4;              // k hi, q hi, k lo, q lo rows of a block
 constexpr float kLog2e = 1.4426950408889634f;
@@ -42,31 +43,33 @@ constexpr int kMostStates = 8;
 
 // Buffers and where they lie (bytes from the start of shared memory).
 struct Plan {
-    int tiles, raws, keys, states;   // B tiles; blocks of q, g and v; units of k; state quarters
-    int raw, k, g, ap, w, state, shared, bytes;
+    int tiles, raws, vals, keys, states;   // B tiles; blocks of g and q, and of v; units of k; state quarters
+    int raw, v, k, g, ap, w, state, shared, bytes;
 };
 
 struct Shared {
-    uint64_t s_full[kMostStates], s_empty[kMostStates], r_full[2], r_empty[2], k_empty[2], t_full, t_empty, e_full[2], e_empty[2],
+    uint64_t s_full[kMostStates], s_empty[kMostStates], r_full[2], r_empty[2], v_full[4], v_empty[4], k_empty[2], t_full[4], t_empty[4], e_full[2], e_empty[2],
         d_full[2], d_empty[2], a_full[2], a_empty[2];
-    alignas(16) signed char parent[kTreeMaxNodes];   // -1: none
     alignas(16) unsigned char above[kTreeMaxNodes][kTreeMaxNodes];   // a node's ancestors from the context on, without itself
-    TreeSmem tree[2];       // of the preparation, of the substitution
+    signed char count[kTreeMaxNodes];                // how many those are; -1 for an absent node
+    TreeSmem tree[3];       // of the preparation, of the two substitutions
     float kn[kTreeMaxNodes], qn[NB];   // reciprocal norms (input prologue)
     uint32_t tmem;
 };
 
-__host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, int keys)
+__host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, int vals, int keys)
 {
     Plan p = {};
     p.tiles = tiles;
     p.raws = raws;
+    p.vals = vals;
     p.keys = keys;
     int at = tiles * kETile;
-    p.raw = at; at += raws * NB * D * (2 * esz + 4);   // of each block g, then q, then v
+    p.raw = at; at += raws * NB * D * (esz + 4);    // of each block g, then q
+    p.v = at; at += vals * NB * D * esz;
     p.k = at; at += keys * K * D * esz;
     p.g = at; at += K * D * 4;
-    p.w = at; at += K * D * 4;
+    p.w = at; at += (K <= NB ? 2 : 1) * K * D * 4;
     p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
     p.shared = (at + 15) & ~15;
     p.state = (p.shared + (int)sizeof(Shared) + 127) & ~127;
@@ -82,8 +85,24 @@ __device__ __forceinline__ float to_tf32(float x) { return __uint_as_float((__fl
 // the same for an operand of the tensor core, which drops the low bits itself
 __device__ __forceinline__ float as_tf32(float x) { return __uint_as_float(__float_as_uint(x) + 0x1000u); }
 
-struct Units {              // this CTA's, one after the other (a sequence's heads stay together)
-    int first, last;
+// A CTA's units: runs of `run` consecutive ones (heads of a sequence, which share its tree), dealt to
+// the CTAs in turn, since trees differ in depth and so in work (a contiguous share each: the last CTA
+// ended 30 % after the middle one).
+struct Units {
+    int total, run, count;
+    __device__ Units(int units, int run_) : total(units), run(run_), count(0)
+    {
+        const int runs = (total + run - 1) / run, mine = (runs - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+        if (mine > 0) {
+            const int last = ((int)blockIdx.x + (mine - 1) * (int)gridDim.x) * run;   // the only run that can be short
+            count = (mine - 1) * run + min(run, total - last);
+        }
+    }
+    __device__ __forceinline__ int operator[](int i) const
+    {
+        const int k = i / run;
+        return ((int)blockIdx.x + k * (int)gridDim.x) * run + i - k * run;
+    }
 };
 
 // ------------------------------------------------------------------ preparation
@@ -107,17 +126,11 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
     Waiter wait{a.status};
     uint32_t block = 0, unit = 0;
     int tree_of = -1;
-    for (int u = un.first; u < un.last; ++u, ++unit) {
-        const int b = u / H;
+    for (; unit < (uint32_t)un.count; ++unit) {
+        const int b = un[unit] / H;
         if (b != tree_of) {
             bar_sync(1, kPrepThreads);              // the last tree has been read
-            if (w == 0) {
-                tree_masks(tree, a.parents + (size_t)b * K, K, lane);
-                for (int i = lane; i < K; i += 32) {
-                    const uint64_t above = tree.anc[i] & ~(1ull << i);
-                    sm.parent[i] = tree.ok && above ? (signed char)(63 - __clzll((long long)above)) : (signed char)-1;
-                }
-            }
+            if (w == 0) tree_masks(tree, a.parents + (size_t)b * K, K, lane);
             tree_of = b;
         }
         const Tin* sk = reinterpret_cast<const Tin*>(base + pl.k) + (unit % pl.keys) * K * D;
@@ -129,7 +142,7 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
         };
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
             const int n = min(NB, K - i0), eb = block % pl.tiles, ab = block & 1, rb = block % pl.raws;
-            const float* graw = reinterpret_cast<const float*>(base + pl.raw + rb * NB * D * (2 * (int)sizeof(Tin) + 4));
+            const float* graw = reinterpret_cast<const float*>(base + pl.raw + rb * NB * D * ((int)sizeof(Tin) + 4));
             const Tin* sq = reinterpret_cast<const Tin*>(graw + NB * D);
             wait(&sm.r_full[rb], (block / pl.raws) & 1);
             bar_sync(1, kPrepThreads);              // the last block's G has been read; the tree is there
@@ -142,16 +155,21 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     if (lane == 0) (i & 1 ? sm.qn[i >> 1] : sm.kn[i0 + (i >> 1)]) = l2_inv(ss);
                 }
             }
-            // G in powers of two: a node's is its parent's and its own g; parents come first
-            if (w == 0) {
-                float4* g4 = reinterpret_cast<float4*>(sg) + lane;
-#pragma unroll 4
-                for (int i = 0; i < n; ++i) {
-                    const int p = sm.parent[i0 + i];
-                    const float4 own = reinterpret_cast<const float4*>(graw)[i * (D / 4) + lane];
-                    const float4 up = p >= 0 ? g4[p * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    g4[(i0 + i) * (D / 4)] = make_float4(fmaf(g_of(own.x, a.prologue), kLog2e, up.x), fmaf(g_of(own.y, a.prologue), kLog2e, up.y),
-                                                         fmaf(g_of(own.z, a.prologue), kLog2e, up.z), fmaf(g_of(own.w, a.prologue), kLog2e, up.w));
+            // G in powers of two: the g of the path's nodes in this block and the G of the node before
+            // them; 16 threads to a node, all nodes at once
+            if (const int i = t >> 4; i < n) {
+                const uint64_t path = tree.anc[i0 + i], before = path & ((1ull << i0) - 1);
+                const float4* g4 = reinterpret_cast<const float4*>(graw) + (t & 15);
+                float4* out = reinterpret_cast<float4*>(sg) + (t & 15);
+#pragma unroll
+                for (int c = 0; c < D / 4; c += 16) {
+                    float4 x = before ? out[(63 - __clzll((long long)before)) * (D / 4) + c] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (uint32_t in = (uint32_t)(path >> i0) & 0xffffu; in; in &= in - 1) {
+                        const float4 y = g4[(__ffs(in) - 1) * (D / 4) + c];
+                        x = make_float4(fmaf(g_of(y.x, a.prologue), kLog2e, x.x), fmaf(g_of(y.y, a.prologue), kLog2e, x.y),
+                                        fmaf(g_of(y.z, a.prologue), kLog2e, x.z), fmaf(g_of(y.w, a.prologue), kLog2e, x.w));
+                    }
+                    out[(i0 + i) * (D / 4) + c] = x;
                 }
             }
             bar_sync(1, kPrepThreads);
@@ -235,13 +253,13 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
     const int lane = t & 31, dv = t;                // lane of tensor memory = value channel
     const uint32_t quad = 32 * (t >> 5);
     Waiter wait{a.status};
-    uint32_t s = 0, phase = 0, unit = 0;
-    for (int u = un.first; u < un.last; ++u, ++unit) {
+    uint32_t s = 0, phase = 0;
+    for (uint32_t unit = 0; unit < (uint32_t)un.count; ++unit) {
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             wait(&sm.s_full[s], phase);
-            if (k == 0 && unit) {
-                wait(&sm.t_empty, (unit - 1) & 1);
+            if (unit) {
+                wait(&sm.t_empty[k], (unit - 1) & 1);
                 tc_fence_after_sync();
             }
             __syncwarp();
@@ -255,14 +273,15 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
             }
             tmem_st32(tmem_addr(sm.tmem, quad, kColHi + 32 * k), hi);
             tmem_st32(tmem_addr(sm.tmem, quad, kColLo + 32 * k), lo);
+            tmem_wait_st();
+            tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_empty[s]);
+            if (lane == 0) {
+                mbar_arrive(&sm.s_empty[s]);
+                mbar_arrive(&sm.t_full[k]);
+            }
             if (++s == (uint32_t)pl.states) { s = 0; phase ^= 1; }
         }
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.t_full);
     }
 }
 
@@ -271,78 +290,89 @@ __device__ __forceinline__ void multiply(const TreeDecodeArgs& a, const Plan& pl
 {
     Waiter wait{a.status};
     const uint32_t tm = sm.tmem, tiles = smem_u32(base);
-    uint32_t block = 0, unit = 0;
-    for (int u = un.first; u < un.last; ++u, ++unit) {
-        wait(&sm.t_full, unit & 1);
+    uint32_t block = 0;
+    for (uint32_t unit = 0; unit < (uint32_t)un.count; ++unit) {
         for (int i0 = 0; i0 < a.nodes; i0 += NB, ++block) {
             const uint32_t eb = block % pl.tiles, db = block & 1;
+            const bool last = i0 + NB >= a.nodes;
             wait(&sm.e_full[eb], (block / pl.tiles) & 1);
             if (block >= 2) wait(&sm.d_empty[db], (block / 2 - 1) & 1);
-            tc_fence_after_sync();
-            if (elect_one()) {
-                if (wait.alive) {
-                    const uint64_t ed = kmajor_base(tiles + eb * kETile);
-                    const uint32_t d = tm + kColD + 64 * db;
+            const uint64_t ed = kmajor_base(tiles + eb * kETile);
+            const uint32_t d = tm + kColD + 64 * db;
+            // quarter by quarter of the key channels, so that the next state's split follows close behind
 #pragma unroll
-                    for (int ks = 0; ks < D / 8; ++ks)
-                        umma_tf32_tmem_a(d, tm + kColHi + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 4 * NB), ks > 0);
+            for (int k = 0; k < 4; ++k) {
+                if (i0 == 0) wait(&sm.t_full[k], unit & 1);
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    if (wait.alive) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 8; ++ks)
-                        umma_tf32_tmem_a(d, tm + kColLo + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 2 * NB), 1);
+                        for (int ks = 4 * k; ks < 4 * k + 4; ++ks)
+                            umma_tf32_tmem_a(d, tm + kColHi + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 4 * NB), ks > 0);
+#pragma unroll
+                        for (int ks = 4 * k; ks < 4 * k + 4; ++ks)
+                            umma_tf32_tmem_a(d, tm + kColLo + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 2 * NB), 1);
+                    }
+                    if (last) umma_commit(&sm.t_empty[k]);
+                    if (k == 3) {
+                        umma_commit(&sm.e_empty[eb]);
+                        umma_commit(&sm.d_full[db]);
+                    }
                 }
-                umma_commit(&sm.e_empty[eb]);
-                umma_commit(&sm.d_full[db]);
-                if (i0 + NB >= a.nodes) umma_commit(&sm.t_empty);
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
-    if (unit) wait(&sm.t_empty, (unit - 1) & 1);    // no product or commit is in flight after this
+    if (block) wait(&sm.d_full[(block - 1) & 1], ((block - 1) / 2) & 1);    // no product or commit is in flight after this
 }
 
 // ------------------------------------------------------------------ substitution and outputs
 template <typename Tin>
-__device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
+__device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t, int group)
 {
     const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31;
+    const int groups = K <= NB ? 2 : 1, blocks = (K + NB - 1) / NB;
+    if (group >= groups) return;
     const uint32_t quad = 32 * (t >> 5);
-    float* sw = reinterpret_cast<float*>(base + pl.w) + t;      // this channel's writes
-    TreeSmem& tree = sm.tree[1];
+    float* sw = reinterpret_cast<float*>(base + pl.w) + group * K * D + t;   // this channel's writes
+    TreeSmem& tree = sm.tree[1 + group];
+    unsigned char (*above)[kTreeMaxNodes] = sm.above + group * (kTreeMaxNodes / 2);
+    signed char* count = sm.count + group * (kTreeMaxNodes / 2);
     Waiter wait{a.status};
-    uint32_t block = 0;
+    uint32_t block = group * blocks;
     int tree_of = -1;
     constexpr int Q = 4;                                        // nodes at a time
     const size_t step = (size_t)H * D;                          // from node to node of out, writes and the gate
     // beta of node (lane % 16) of a block, loaded a block ahead (past the last node the last one again)
-    auto beta_at = [&](int u, int i0) {
-        u = min(u, un.last - 1);
-        const int b = u / H, h = u - b * H;
+    auto beta_at = [&](int unit, int i0) {
+        const int u = un[min(unit, un.count - 1)], b = u / H, h = u - b * H;
         return a.beta[((size_t)b * K + min(i0 + (lane & 15), K - 1)) * H + h];
     };
-    float next_beta = beta_at(un.first, 0);
-    for (int u = un.first; u < un.last; ++u) {
-        const int b = u / H, h = u - b * H;
+    float next_beta = beta_at(group, 0);
+    for (int unit = group; unit < un.count; unit += groups, block += (groups - 1) * blocks) {
+        const int u = un[unit], b = u / H, h = u - b * H;
         if (b != tree_of) {
-            bar_sync(2, 128);
+            bar_sync(2 + group, 128);
             if (t < 32) {
                 tree_masks(tree, a.parents + (size_t)b * K, K, lane);
                 if (lane == 0 && !tree.ok) report_status(a.status, kDevBadSeqlens);
             }
             tree_of = b;
-            bar_sync(2, 128);
+            bar_sync(2 + group, 128);
             if (t < K) {
                 int e = 0;
-                for (uint64_t m = tree.anc[t] & ~(1ull << t); m; m &= m - 1) sm.above[t][e++] = (unsigned char)(__ffsll((long long)m) - 1);
+                for (uint64_t m = tree.anc[t] & ~(1ull << t); m; m &= m - 1) above[t][e++] = (unsigned char)(__ffsll((long long)m) - 1);
+                count[t] = tree.anc[t] ? (signed char)e : (signed char)-1;
             }
-            bar_sync(2, 128);
+            bar_sync(2 + group, 128);
         }
         size_t at = ((size_t)b * K * H + h) * D + t;
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
-            const uint32_t db = block & 1, rb = block % pl.raws;
+            const uint32_t db = block & 1, vb = block % pl.vals;
             const float beta16 = beta_of(next_beta, a.prologue);
-            next_beta = i0 + NB < K ? beta_at(u, i0 + NB) : beta_at(u + 1, 0);
-            const Tin* sv = reinterpret_cast<const Tin*>(base + pl.raw + rb * NB * D * (2 * (int)sizeof(Tin) + 4) + NB * D * (4 + (int)sizeof(Tin))) + t;
-            wait(&sm.r_full[rb], (block / pl.raws) & 1);
+            next_beta = i0 + NB < K ? beta_at(unit, i0 + NB) : beta_at(unit + groups, 0);
+            const Tin* sv = reinterpret_cast<const Tin*>(base + pl.v) + vb * NB * D + t;
+            wait(&sm.v_full[vb], (block / pl.vals) & 1);
             wait(&sm.d_full[db], (block / 2) & 1);
             wait(&sm.a_full[db], (block / 2) & 1);
             __syncwarp();
@@ -357,58 +387,71 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
                 tmem_ld4(td + NB + g0, y);
                 tmem_ld4(td + 2 * NB + g0, x2);
                 tmem_ld4(td + 3 * NB + g0, y2);
-                float v[Q], beta[Q];
+                // what the four nodes need besides one another's writes, before the first of them: v, beta,
+                // the number of ancestors (-1: an absent node), the first four with their pairs, the own pair
+                float v[Q], beta[Q], own[Q];
+                int cnt[Q];
+                uint32_t js[Q];
+                float4 c0[Q], c1[Q];
 #pragma unroll
                 for (int k = 0; k < Q; ++k) {
-                    v[k] = to_f32(sv[min(g0 + k, n - 1) * D]);
+                    const int i = min(g0 + k, n - 1);
+                    const float2* r = row + i * KP;
+                    v[k] = to_f32(sv[i * D]);
                     beta[k] = __shfl_sync(0xffffffffu, beta16, g0 + k);
+                    cnt[k] = count[i0 + i];
+                    js[k] = *reinterpret_cast<const uint32_t*>(above[i0 + i]) & 0x3f3f3f3fu;
+                    c0[k] = *reinterpret_cast<const float4*>(r);
+                    c1[k] = *reinterpret_cast<const float4*>(r + 2);
+                    own[k] = r[max(cnt[k], 0)].y;
                 }
                 tmem_wait_ld();
+                if (!tree.ok) continue;
 #pragma unroll
                 for (int k = 0; k < Q; ++k) {
-                    const int i = i0 + g0 + k;
-                    if (i >= K || !tree.ok) break;
-                    const uint64_t m = tree.anc[i];
-                    const int cnt = __popcll(m) - 1;            // ancestors; -1 for an absent node
+                    const int i = g0 + k;
+                    if (i >= n) break;
                     float xi = x[k] + x2[k], yi = y[k] + y2[k];
-                    // four ancestors at a time; what lies in the lists past the last is not used
+                    if (cnt[k] > 0) {
+                        const float w0 = sw[(js[k] & 63) * D];
+                        xi = fmaf(c0[k].x, w0, xi);
+                        yi = fmaf(c0[k].y, w0, yi);
+                    }
+                    if (cnt[k] > 1) {
+                        const float w1 = sw[(js[k] >> 8 & 63) * D];
+                        xi = fmaf(c0[k].z, w1, xi);
+                        yi = fmaf(c0[k].w, w1, yi);
+                    }
+                    if (cnt[k] > 2) {
+                        const float w2 = sw[(js[k] >> 16 & 63) * D];
+                        xi = fmaf(c1[k].x, w2, xi);
+                        yi = fmaf(c1[k].y, w2, yi);
+                    }
+                    if (cnt[k] > 3) {
+                        const float w3 = sw[(js[k] >> 24) * D];
+                        xi = fmaf(c1[k].z, w3, xi);
+                        yi = fmaf(c1[k].w, w3, yi);
+                    }
 #pragma unroll 1
-                    for (int e = 0; e < cnt; e += 4) {
-                        const uint32_t j = *reinterpret_cast<const uint32_t*>(&sm.above[i][e]);
-                        const float4 c0 = *reinterpret_cast<const float4*>(row + e);
-                        const float w0 = sw[(j & 63) * D];
-                        xi = fmaf(c0.x, w0, xi);
-                        yi = fmaf(c0.y, w0, yi);
-                        if (e + 1 < cnt) {
-                            const float w1 = sw[(j >> 8 & 63) * D];
-                            xi = fmaf(c0.z, w1, xi);
-                            yi = fmaf(c0.w, w1, yi);
-                        }
-                        if (e + 2 < cnt) {
-                            const float4 c1 = *reinterpret_cast<const float4*>(row + e + 2);
-                            const float w2 = sw[(j >> 16 & 63) * D];
-                            xi = fmaf(c1.x, w2, xi);
-                            yi = fmaf(c1.y, w2, yi);
-                            if (e + 3 < cnt) {
-                                const float w3 = sw[(j >> 24 & 63) * D];
-                                xi = fmaf(c1.z, w3, xi);
-                                yi = fmaf(c1.w, w3, yi);
-                            }
+                    for (int e = 4; e < cnt[k]; e += 2) {       // deeper nodes
+                        const uint32_t j = *reinterpret_cast<const uint16_t*>(&above[i0 + i][e]);
+                        const float4 c = *reinterpret_cast<const float4*>(row + i * KP + e);
+                        const float w0 = sw[(j & 63) * D], w1 = e + 1 < cnt[k] ? sw[(j >> 8 & 63) * D] : 0.f;
+                        xi = fmaf(c.x, w0, xi);
+                        yi = fmaf(c.y, w0, yi);
+                        if (e + 1 < cnt[k]) {
+                            xi = fmaf(c.z, w1, xi);
+                            yi = fmaf(c.w, w1, yi);
                         }
                     }
-                    float wi = 0.f;
-                    if (cnt >= 0) {
-                        wi = beta[k] * (v[k] - xi);
-                        yi = fmaf(row[cnt].y, wi, yi);
-                    } else {
-                        yi = 0.f;
-                    }
+                    float wi = beta[k] * (v[k] - xi);
+                    yi = fmaf(own[k], wi, yi);
+                    if (cnt[k] < 0) wi = yi = 0.f;
                     if (a.gate) yi = gate1(yi, __ldg(a.gate + at));
-                    sw[i * D] = wi;
+                    sw[(i0 + i) * D] = wi;
                     a.writes[at] = wi;
                     a.out[at] = yi;
                     at += step;
-                    row += KP;
                 }
             }
             tc_fence_before_sync();
@@ -416,7 +459,7 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
             if (lane == 0) {
                 mbar_arrive(&sm.d_empty[db]);
                 mbar_arrive(&sm.a_empty[db]);
-                mbar_arrive(&sm.r_empty[rb]);
+                mbar_arrive(&sm.v_empty[vb]);
             }
         }
     }
@@ -427,15 +470,15 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
 __device__ __forceinline__ void copy_states(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base)
 {
     Waiter wait{a.status};
-    const char* src = reinterpret_cast<const char*>(a.state) + (size_t)un.first * 4 * kQuarter;
-    const uint32_t total = 4 * (un.last - un.first);
+    const char* src = reinterpret_cast<const char*>(a.state);
+    const uint32_t total = 4 * un.count;
     uint32_t i = 0;
     for (; i < total; ++i) {
         const uint32_t s = i % pl.states;
         if (i >= (uint32_t)pl.states) wait(&sm.s_empty[s], (i / pl.states - 1) & 1);
         if (!wait.alive) break;
         mbar_arrive_expect_tx(&sm.s_full[s], kQuarter);
-        bulk_load(base + pl.state + s * kQuarter, src + (size_t)i * kQuarter, kQuarter, &sm.s_full[s]);
+        bulk_load(base + pl.state + s * kQuarter, src + ((size_t)un[i / 4] * 4 + i % 4) * kQuarter, kQuarter, &sm.s_full[s]);
     }
     // no load is in flight when the block ends, whatever became of its reader
     for (uint32_t j = i > (uint32_t)pl.states ? i - pl.states : 0; j < i; ++j)
@@ -451,33 +494,39 @@ __device__ __forceinline__ void copy_nodes(const TreeDecodeArgs& a, const Plan& 
     Waiter wait{a.status};
     uint32_t block = 0, unit = 0;
     bool go = true;
-    for (int u = un.first; u < un.last && go; ++u, ++unit) {
-        const int b = u / H, h = u - b * H;
+    for (; unit < (uint32_t)un.count && go; ++unit) {
+        const int u = un[unit], b = u / H, h = u - b * H;
         const uint32_t kb = unit % pl.keys;
         if (unit >= (uint32_t)pl.keys) wait(&sm.k_empty[kb], (unit / pl.keys - 1) & 1);
         for (int i0 = 0; i0 < K && go; i0 += NB) {
             const int n = min(NB, K - i0);
-            const uint32_t rb = block % pl.raws;
+            const uint32_t rb = block % pl.raws, vb = block % pl.vals;
             if (block >= (uint32_t)pl.raws) wait(&sm.r_empty[rb], (block / pl.raws - 1) & 1);
+            if (block >= (uint32_t)pl.vals) wait(&sm.v_empty[vb], (block / pl.vals - 1) & 1);
             go = __all_sync(0xffffffffu, wait.alive);
             if (!go) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.r_full[rb], n * (3 * kRow + D * 4));
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.r_full[rb], n * (2 * kRow + D * 4));
+                mbar_arrive_expect_tx(&sm.v_full[vb], n * kRow);
+            }
             __syncwarp();
-            uint8_t* raw = base + pl.raw + rb * NB * D * (2 * E + 4);
+            uint8_t* raw = base + pl.raw + rb * NB * D * (E + 4);
             for (int x = lane; x < 64; x += 32) {
                 const int i = x & 15, what = x >> 4;
                 if (i >= n) continue;
                 const size_t at = (((size_t)b * K + i0 + i) * H + h) * D;
                 if (what == 0) bulk_load(raw + i * D * 4, a.g + at, D * 4, &sm.r_full[rb]);
                 else if (what == 1) bulk_load(raw + NB * D * 4 + i * kRow, static_cast<const Tin*>(a.q) + at, kRow, &sm.r_full[rb]);
-                else if (what == 2) bulk_load(raw + NB * D * 4 + (NB + i) * kRow, static_cast<const Tin*>(a.v) + at, kRow, &sm.r_full[rb]);
-                else bulk_load(base + pl.k + (kb * K + i0 + i) * kRow, static_cast<const Tin*>(a.k) + at, kRow, &sm.r_full[rb]);
+                else if (what == 2) bulk_load(base + pl.k + (kb * K + i0 + i) * kRow, static_cast<const Tin*>(a.k) + at, kRow, &sm.r_full[rb]);
+                else bulk_load(base + pl.v + (vb * NB + i) * kRow, static_cast<const Tin*>(a.v) + at, kRow, &sm.v_full[vb]);
             }
             ++block;
         }
     }
     for (uint32_t j = block > (uint32_t)pl.raws ? block - pl.raws : 0; j < block; ++j)
         mbar_wait_bounded(&sm.r_full[j % pl.raws], (j / pl.raws) & 1, kDraftWaitNs);
+    for (uint32_t j = block > (uint32_t)pl.vals ? block - pl.vals : 0; j < block; ++j)
+        mbar_wait_bounded(&sm.v_full[j % pl.vals], (j / pl.vals) & 1, kDraftWaitNs);
 }
 
 template <typename Tin>
@@ -500,25 +549,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
             mbar_init(&sm.a_full[i], kPrepThreads / 32);
             mbar_init(&sm.a_empty[i], 4);
             mbar_init(&sm.r_full[i], 1);
-            mbar_init(&sm.r_empty[i], kPrepThreads / 32 + 4);
+            mbar_init(&sm.r_empty[i], kPrepThreads / 32);
             mbar_init(&sm.k_empty[i], kPrepThreads / 32);
         }
-        mbar_init(&sm.t_full, 4);
-        mbar_init(&sm.t_empty, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.t_full[i], 4);
+            mbar_init(&sm.t_empty[i], 1);
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 4);
+        }
         mbar_fence_init();
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const Units un = {(int)((long long)total * blockIdx.x / gridDim.x), (int)((long long)total * (blockIdx.x + 1) / gridDim.x)};
+    const Units un(total, total >= 16 * (int)gridDim.x ? 4 : total >= 4 * (int)gridDim.x ? 2 : 1);
     if (warp < 4) {
-        solve<Tin>(a, pl, un, sm, base, t);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
+        solve<Tin>(a, pl, un, sm, base, t, 0);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSplitRegs));
         split(a, pl, un, sm, base, t - 128);
     } else if (warp < 16) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrepRegs));
         prepare<Tin>(a, pl, un, sm, base, t - 256);
+    } else if (warp >= 20) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
+        solve<Tin>(a, pl, un, sm, base, t - 640, 1);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
         if (warp == 17) multiply(a, pl, un, sm, base);
@@ -532,14 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     if (warp == 17) tmem_dealloc(sm.tmem, 512);
 }
 
-// Buffers for K nodes: everything double while that leaves the states six quarters (96 KB in
-// flight cover HBM's latency at its full rate), else as much of it as leaves them three.
+// Buffers for K nodes: as much in double (v, which waits for the last of the roles, in fourfold) as
+// leaves the states three quarters or more (48 KB in flight cover HBM's latency).
 constexpr Plan choose_plan(int K, int esz)
 {
-    constexpr int options[5][4] = {{2, 2, 2, 6}, {2, 2, 1, 4}, {1, 2, 2, 4}, {1, 2, 1, 3}, {1, 1, 1, 3}};
+    constexpr int options[6][5] = {{2, 2, 4, 2, 4}, {2, 2, 4, 2, 3}, {2, 2, 2, 1, 3}, {1, 2, 2, 2, 3}, {1, 2, 2, 1, 3}, {1, 1, 1, 1, 3}};
     for (const auto& o : options) {
-        const Plan p = plan_of(K, esz, o[0], o[1], o[2]);
-        if (p.states >= o[3]) return p;
+        const Plan p = plan_of(K, esz, o[0], o[1], o[2], o[3]);
+        if (p.states >= o[4]) return p;
     }
     return {};
 }
