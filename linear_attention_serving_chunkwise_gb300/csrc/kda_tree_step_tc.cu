@@ -13,7 +13,7 @@
 //     16        copies states in quarters of 16 KB (what keeps HBM busy), 18 the nodes' k, q, g and v,
 //               rows of 256 or 512 bytes: no other warp loads them, so none waits for memory
 //     4 - 7     split a state into tensor memory
-//     8 - 15    prepare a block: G along the paths, e^G k and e^G q split into the B operand, and
+//     8 - 15    prepare a block (eight warps, or four each in turn where a unit is one block): G along the paths, e^G k and e^G q split into the B operand, and
 //               A_ij = <e^{G_i - G_j} k_i, k_j>, P_ij = <e^{G_i - G_j} q_i, k_j> on the ancestor pairs
 //               alone, each exponential of a difference <= 0 (a factored e^{-G_j} would overflow)
 //     17        issues the products
@@ -52,8 +52,8 @@ struct Shared {
         d_full[2], d_empty[2], a_full[2], a_empty[2];
     alignas(16) unsigned char above[kTreeMaxNodes][kTreeMaxNodes];   // a node's ancestors from the context on, without itself
     signed char count[kTreeMaxNodes];                // how many those are; -1 for an absent node
-    TreeSmem tree[3];       // of the preparation, of the two substitutions
-    float kn[kTreeMaxNodes], qn[NB];   // reciprocal norms (input prologue)
+    TreeSmem tree[4];       // of the two preparations, of the two substitutions
+    float kn[2 * kTreeMaxNodes], qn[2 * NB];   // reciprocal norms (input prologue)
     uint32_t tmem;
 };
 
@@ -68,7 +68,7 @@ __host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, 
     p.raw = at; at += raws * NB * D * (esz + 4);    // of each block g, then q
     p.v = at; at += vals * NB * D * esz;
     p.k = at; at += keys * K * D * esz;
-    p.g = at; at += K * D * 4;
+    p.g = at; at += (K <= NB ? 2 : 1) * K * D * 4;
     p.w = at; at += (K <= NB ? 2 : 1) * K * D * 4;
     p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
     p.shared = (at + 15) & ~15;
@@ -116,20 +116,27 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p)
 
 // (Loops are unrolled little: the roles run side by side, and straight-line code for each would
 // be fetched anew for every block.)
+// units handled side by side by the preparation and by the substitution
+__host__ __device__ constexpr int groups_of(int K) { return K <= NB ? 2 : 1; }
+
 template <typename Tin>
 __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
 {
-    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, W = kPrepThreads / 32;
+    const int groups = groups_of(a.nodes), group = t / (kPrepThreads / groups);
+    t -= group * (kPrepThreads / groups);
+    const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, W = kPrepThreads / 32 / groups;
+    const int bar = 4 + group, threads = 32 * W;
     const bool norm = a.prologue & kProQK;
-    float* sg = reinterpret_cast<float*>(base + pl.g);
-    TreeSmem& tree = sm.tree[0];
+    float* sg = reinterpret_cast<float*>(base + pl.g) + group * K * D;
+    float *kn = sm.kn + group * kTreeMaxNodes, *qn = sm.qn + group * NB;
+    TreeSmem& tree = sm.tree[group];
     Waiter wait{a.status};
-    uint32_t block = 0, unit = 0;
+    uint32_t block = group;                         // (with two groups a unit is one block)
     int tree_of = -1;
-    for (; unit < (uint32_t)un.count; ++unit) {
+    for (uint32_t unit = group; unit < (uint32_t)un.count; unit += groups, block += groups - 1) {
         const int b = un[unit] / H;
         if (b != tree_of) {
-            bar_sync(1, kPrepThreads);              // the last tree has been read
+            bar_sync(bar, threads);              // the last tree has been read
             if (w == 0) tree_masks(tree, a.parents + (size_t)b * K, K, lane);
             tree_of = b;
         }
@@ -145,19 +152,19 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             const float* graw = reinterpret_cast<const float*>(base + pl.raw + rb * NB * D * ((int)sizeof(Tin) + 4));
             const Tin* sq = reinterpret_cast<const Tin*>(graw + NB * D);
             wait(&sm.r_full[rb], (block / pl.raws) & 1);
-            bar_sync(1, kPrepThreads);              // the last block's G has been read; the tree is there
+            bar_sync(bar, threads);              // the last block's G has been read; the tree is there
             if (norm) {
                 for (int i = w; i < 2 * n; i += W) {
                     const float4 v = four((i & 1 ? sq + (i >> 1) * D : sk + (i0 + (i >> 1)) * D) + 4 * lane);
                     float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    if (lane == 0) (i & 1 ? sm.qn[i >> 1] : sm.kn[i0 + (i >> 1)]) = l2_inv(ss);
+                    if (lane == 0) (i & 1 ? qn[i >> 1] : kn[i0 + (i >> 1)]) = l2_inv(ss);
                 }
             }
             // G in powers of two: the g of the path's nodes in this block and the G of the node before
             // them; 16 threads to a node, all nodes at once
-            if (const int i = t >> 4; i < n) {
+            for (int i = t >> 4; i < n; i += threads / 16) {
                 const uint64_t path = tree.anc[i0 + i], before = path & ((1ull << i0) - 1);
                 const float4* g4 = reinterpret_cast<const float4*>(graw) + (t & 15);
                 float4* out = reinterpret_cast<float4*>(sg) + (t & 15);
@@ -172,15 +179,15 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     out[(i0 + i) * (D / 4) + c] = x;
                 }
             }
-            bar_sync(1, kPrepThreads);
+            bar_sync(bar, threads);
             // the B operand: a warp to a node's row, a lane to four channels (16 bytes of each of its four rows,
             // 16 rows apart: the swizzle, which goes by the row's last three bits, is theirs in common)
             if (block >= (uint32_t)pl.tiles) wait(&sm.e_empty[eb], (block / pl.tiles - 1) & 1);
             uint8_t* et = base + eb * kETile + (lane >> 3) * (4 * NB * 128);
 #pragma unroll 1
             for (int i = w; i < n; i += W) {        // (rows of the block beyond its nodes: columns of D that nobody reads)
-                const float4 g = four(sg + (i0 + i) * D + 4 * lane), k = row4(sk + (i0 + i) * D, norm ? sm.kn[i0 + i] : 1.f),
-                             q = row4(sq + i * D, norm ? sm.qn[i] : 1.f);
+                const float4 g = four(sg + (i0 + i) * D + 4 * lane), k = row4(sk + (i0 + i) * D, norm ? kn[i0 + i] : 1.f),
+                             q = row4(sq + i * D, norm ? qn[i] : 1.f);
                 const float e[4] = {ex2(g.x), ex2(g.y), ex2(g.z), ex2(g.w)}, kk[4] = {k.x, k.y, k.z, k.w}, qq[4] = {q.x, q.y, q.z, q.w};
                 float kh[4], kl[4], qh[4], ql[4];
 #pragma unroll
@@ -206,10 +213,10 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             float2* ap = reinterpret_cast<float2*>(base + pl.ap) + ab * NB * KP;
 #pragma unroll 1
             for (int i = W - 1 - w; i < n; i += W) {
-                const float4 ki = row4(sk + (i0 + i) * D, norm ? sm.kn[i0 + i] : 1.f), qi = row4(sq + i * D, norm ? sm.qn[i] : 1.f),
+                const float4 ki = row4(sk + (i0 + i) * D, norm ? kn[i0 + i] : 1.f), qi = row4(sq + i * D, norm ? qn[i] : 1.f),
                              gi = four(sg + (i0 + i) * D + 4 * lane);
                 auto dots = [&](int j, float& da, float& dp) {
-                    const float4 kj = row4(sk + j * D, norm ? sm.kn[j] : 1.f), gj = four(sg + j * D + 4 * lane);
+                    const float4 kj = row4(sk + j * D, norm ? kn[j] : 1.f), gj = four(sg + j * D + 4 * lane);
                     const float x = ex2(gi.x - gj.x) * kj.x, y = ex2(gi.y - gj.y) * kj.y, z = ex2(gi.z - gj.z) * kj.z, v = ex2(gi.w - gj.w) * kj.w;
                     da = fmaf(x, ki.x, fmaf(y, ki.y, fmaf(z, ki.z, v * ki.w)));
                     dp = fmaf(x, qi.x, fmaf(y, qi.y, fmaf(z, qi.z, v * qi.w)));
@@ -300,18 +307,20 @@ __device__ __forceinline__ void multiply(const TreeDecodeArgs& a, const Plan& pl
             const uint64_t ed = kmajor_base(tiles + eb * kETile);
             const uint32_t d = tm + kColD + 64 * db;
             // quarter by quarter of the key channels, so that the next state's split follows close behind
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 if (i0 == 0) wait(&sm.t_full[k], unit & 1);
                 tc_fence_after_sync();
                 if (elect_one()) {
                     if (wait.alive) {
+                        const uint64_t e = desc_off(ed, k * kmajor_off(4 * NB, 4));
+                        const uint32_t hi = tm + kColHi + 32 * k;
 #pragma unroll
-                        for (int ks = 4 * k; ks < 4 * k + 4; ++ks)
-                            umma_tf32_tmem_a(d, tm + kColHi + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 4 * NB), ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_tf32_tmem_a(d, hi + 8 * ks, desc_off(e, 32 * ks), idesc_tf32_f32(128, 4 * NB), k > 0 || ks > 0);
 #pragma unroll
-                        for (int ks = 4 * k; ks < 4 * k + 4; ++ks)
-                            umma_tf32_tmem_a(d, tm + kColLo + 8 * ks, desc_off(ed, kmajor_off(4 * NB, ks)), idesc_tf32_f32(128, 2 * NB), 1);
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_tf32_tmem_a(d, hi + (kColLo - kColHi) + 8 * ks, desc_off(e, 32 * ks), idesc_tf32_f32(128, 2 * NB), 1);
                     }
                     if (last) umma_commit(&sm.t_empty[k]);
                     if (k == 3) {
@@ -331,11 +340,11 @@ template <typename Tin>
 __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t, int group)
 {
     const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31;
-    const int groups = K <= NB ? 2 : 1, blocks = (K + NB - 1) / NB;
+    const int groups = groups_of(K), blocks = (K + NB - 1) / NB;
     if (group >= groups) return;
     const uint32_t quad = 32 * (t >> 5);
     float* sw = reinterpret_cast<float*>(base + pl.w) + group * K * D + t;   // this channel's writes
-    TreeSmem& tree = sm.tree[1 + group];
+    TreeSmem& tree = sm.tree[2 + group];
     unsigned char (*above)[kTreeMaxNodes] = sm.above + group * (kTreeMaxNodes / 2);
     signed char* count = sm.count + group * (kTreeMaxNodes / 2);
     Waiter wait{a.status};
@@ -542,15 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     if (t == 0) {
         for (int i = 0; i < kMostStates; ++i) { mbar_init(&sm.s_full[i], 1); mbar_init(&sm.s_empty[i], 4); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.e_full[i], kPrepThreads);
+            mbar_init(&sm.e_full[i], kPrepThreads / groups_of(a.nodes));
             mbar_init(&sm.e_empty[i], 1);
             mbar_init(&sm.d_full[i], 1);
             mbar_init(&sm.d_empty[i], 4);
-            mbar_init(&sm.a_full[i], kPrepThreads / 32);
+            mbar_init(&sm.a_full[i], kPrepThreads / 32 / groups_of(a.nodes));
             mbar_init(&sm.a_empty[i], 4);
             mbar_init(&sm.r_full[i], 1);
-            mbar_init(&sm.r_empty[i], kPrepThreads / 32);
-            mbar_init(&sm.k_empty[i], kPrepThreads / 32);
+            mbar_init(&sm.r_empty[i], kPrepThreads / 32 / groups_of(a.nodes));
+            mbar_init(&sm.k_empty[i], kPrepThreads / 32 / groups_of(a.nodes));
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm.t_full[i], 4);
