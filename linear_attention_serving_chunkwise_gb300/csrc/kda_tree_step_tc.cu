@@ -119,14 +119,16 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p)
 // units handled side by side by the preparation and by the substitution
 __host__ __device__ constexpr int groups_of(int K) { return K <= NB ? 2 : 1; }
 
-template <typename Tin>
+// kPro (all of them): the input prologue is compiled in (own instances; the common ones stay small)
+template <typename Tin, bool kPro>
 __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
 {
     const int groups = groups_of(a.nodes), group = t / (kPrepThreads / groups);
     t -= group * (kPrepThreads / groups);
     const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31, w = t >> 5, W = kPrepThreads / 32 / groups;
     const int bar = 4 + group, threads = 32 * W;
-    const bool norm = a.prologue & kProQK;
+    const int pro = kPro ? a.prologue : 0;
+    const bool norm = pro & kProQK;
     float* sg = reinterpret_cast<float*>(base + pl.g) + group * K * D;
     float *kn = sm.kn + group * kTreeMaxNodes, *qn = sm.qn + group * NB;
     TreeSmem& tree = sm.tree[group];
@@ -173,8 +175,8 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     float4 x = before ? out[(63 - __clzll((long long)before)) * (D / 4) + c] : make_float4(0.f, 0.f, 0.f, 0.f);
                     for (uint32_t in = (uint32_t)(path >> i0) & 0xffffu; in; in &= in - 1) {
                         const float4 y = g4[(__ffs(in) - 1) * (D / 4) + c];
-                        x = make_float4(fmaf(g_of(y.x, a.prologue), kLog2e, x.x), fmaf(g_of(y.y, a.prologue), kLog2e, x.y),
-                                        fmaf(g_of(y.z, a.prologue), kLog2e, x.z), fmaf(g_of(y.w, a.prologue), kLog2e, x.w));
+                        x = make_float4(fmaf(g_of(y.x, pro), kLog2e, x.x), fmaf(g_of(y.y, pro), kLog2e, x.y),
+                                        fmaf(g_of(y.z, pro), kLog2e, x.z), fmaf(g_of(y.w, pro), kLog2e, x.w));
                     }
                     out[(i0 + i) * (D / 4) + c] = x;
                 }
@@ -206,42 +208,47 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             }
             fence_proxy_async_smem();
             mbar_arrive(&sm.e_full[eb]);
-            // the ancestor pairs: a warp to a node, a lane to four channels; entry e of the node's list is its
-            // e-th ancestor from the context on, the last is the node itself
+            // the ancestor pairs: a warp to a node, eight lanes to an ancestor, four ancestors at a time (lane
+            // l of the eight has channels 4 l + 32 s); entry e of the node's list is its e-th ancestor from the
+            // context on, the last is the node itself
             if (block >= 2) wait(&sm.a_empty[ab], (block / 2 - 1) & 1);
             __syncwarp();
             float2* ap = reinterpret_cast<float2*>(base + pl.ap) + ab * NB * KP;
+            const int c0 = 4 * (lane & 7), which = lane >> 3;
+            auto at4 = [&](const Tin* p, float inv) {
+                float4 x = four(p);
+                if (norm) x = make_float4(l2_scale(x.x, inv, Tin{}), l2_scale(x.y, inv, Tin{}), l2_scale(x.z, inv, Tin{}), l2_scale(x.w, inv, Tin{}));
+                return x;
+            };
 #pragma unroll 1
-            for (int i = W - 1 - w; i < n; i += W) {
-                const float4 ki = row4(sk + (i0 + i) * D, norm ? kn[i0 + i] : 1.f), qi = row4(sq + i * D, norm ? qn[i] : 1.f),
-                             gi = four(sg + (i0 + i) * D + 4 * lane);
-                auto dots = [&](int j, float& da, float& dp) {
-                    const float4 kj = row4(sk + j * D, norm ? kn[j] : 1.f), gj = four(sg + j * D + 4 * lane);
-                    const float x = ex2(gi.x - gj.x) * kj.x, y = ex2(gi.y - gj.y) * kj.y, z = ex2(gi.z - gj.z) * kj.z, v = ex2(gi.w - gj.w) * kj.w;
-                    da = fmaf(x, ki.x, fmaf(y, ki.y, fmaf(z, ki.z, v * ki.w)));
-                    dp = fmaf(x, qi.x, fmaf(y, qi.y, fmaf(z, qi.z, v * qi.w)));
-                };
-                int e = 0;
+            for (int i = w; i < n; i += W) {
+                const uint64_t all = tree.ok ? tree.anc[i0 + i] : 0ull;
+                const int cnt = __popcll(all);
+                uint64_t m = all;                   // from this lane's next ancestor on
+                for (int k = 0; k < which; ++k) m &= m - 1;
 #pragma unroll 1
-                for (uint64_t m = tree.ok ? tree.anc[i0 + i] : 0ull; m; e += 2) {
-                    // two pairs at a time; their four sums end in lanes 0, 8, 16 and 24
-                    const int j0 = __ffsll((long long)m) - 1;
-                    m &= m - 1;
-                    const bool two = m != 0;
-                    const int j1 = two ? __ffsll((long long)m) - 1 : j0;
-                    m &= m - 1;
-                    float a0, p0, a1, p1;
-                    dots(j0, a0, p0);
-                    dots(j1, a1, p1);
-                    const bool up = lane & 16, mid = lane & 8;
-                    float x = up ? a1 : a0, y = up ? p1 : p0;
-                    x += __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 16);
-                    y += __shfl_xor_sync(0xffffffffu, up ? p0 : p1, 16);
-                    float z = mid ? y : x;
-                    z += __shfl_xor_sync(0xffffffffu, mid ? x : y, 8);
+                for (int e = which; e - which < cnt; e += 4) {
+                    const int j = m ? __ffsll((long long)m) - 1 : i0 + i;
+                    float da = 0.f, dp = 0.f;
 #pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                    if ((lane & 7) == 0 && (two || !up)) reinterpret_cast<float*>(ap + i * KP + e + (up ? 1 : 0))[mid ? 1 : 0] = z;
+                    for (int s = 0; s < 4; ++s) {
+                        const int c = c0 + 32 * s;
+                        const float4 gi = four(sg + (i0 + i) * D + c), gj = four(sg + j * D + c), kj = at4(sk + j * D + c, norm ? kn[j] : 1.f),
+                                     ki = at4(sk + (i0 + i) * D + c, norm ? kn[i0 + i] : 1.f), qi = at4(sq + i * D + c, norm ? qn[i] : 1.f);
+                        const float x = ex2(gi.x - gj.x) * kj.x, y = ex2(gi.y - gj.y) * kj.y, z = ex2(gi.z - gj.z) * kj.z, v = ex2(gi.w - gj.w) * kj.w;
+                        da = fmaf(x, ki.x, fmaf(y, ki.y, fmaf(z, ki.z, fmaf(v, ki.w, da))));
+                        dp = fmaf(x, qi.x, fmaf(y, qi.y, fmaf(z, qi.z, fmaf(v, qi.w, dp))));
+                    }
+                    const bool up = lane & 4;       // both sums over the eight lanes: A in the first four, P in the others
+                    float z = up ? dp : da;
+                    z += __shfl_xor_sync(0xffffffffu, up ? da : dp, 4);
+                    z += __shfl_xor_sync(0xffffffffu, z, 2);
+                    z += __shfl_xor_sync(0xffffffffu, z, 1);
+                    if ((lane & 3) == 0 && e < cnt) reinterpret_cast<float*>(ap + i * KP + e)[up ? 1 : 0] = z;
+                    m &= m - 1;
+                    m &= m - 1;
+                    m &= m - 1;
+                    m &= m - 1;
                 }
             }
             __syncwarp();
@@ -271,15 +278,18 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
             }
             __syncwarp();
             const float* src = reinterpret_cast<const float*>(base + pl.state + s * kQuarter) + dv;
-            float hi[32], lo[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float x = src[i * D];
-                hi[i] = to_tf32(x);
-                lo[i] = as_tf32(x - hi[i]);
+            for (int c = 0; c < 32; c += 16) {      // (16 at a time: the second's loads go out under the first's arithmetic)
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = src[(c + i) * D], h = to_tf32(x);
+                    hi[i] = __float_as_uint(h);
+                    lo[i] = __float_as_uint(as_tf32(x - h));
+                }
+                tmem_st16u(tmem_addr(sm.tmem, quad, kColHi + 32 * k + c), hi);
+                tmem_st16u(tmem_addr(sm.tmem, quad, kColLo + 32 * k + c), lo);
             }
-            tmem_st32(tmem_addr(sm.tmem, quad, kColHi + 32 * k), hi);
-            tmem_st32(tmem_addr(sm.tmem, quad, kColLo + 32 * k), lo);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -336,7 +346,7 @@ __device__ __forceinline__ void multiply(const TreeDecodeArgs& a, const Plan& pl
 }
 
 // ------------------------------------------------------------------ substitution and outputs
-template <typename Tin>
+template <typename Tin, bool kPro>
 __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t, int group)
 {
     const int K = a.nodes, H = a.num_heads, KP = (K + 1) & ~1, lane = t & 31;
@@ -378,7 +388,7 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
         size_t at = ((size_t)b * K * H + h) * D + t;
         for (int i0 = 0; i0 < K; i0 += NB, ++block) {
             const uint32_t db = block & 1, vb = block % pl.vals;
-            const float beta16 = beta_of(next_beta, a.prologue);
+            const float beta16 = beta_of(next_beta, kPro ? a.prologue : 0);
             next_beta = i0 + NB < K ? beta_at(unit, i0 + NB) : beta_at(unit + groups, 0);
             const Tin* sv = reinterpret_cast<const Tin*>(base + pl.v) + vb * NB * D + t;
             wait(&sm.v_full[vb], (block / pl.vals) & 1);
@@ -538,7 +548,7 @@ __device__ __forceinline__ void copy_nodes(const TreeDecodeArgs& a, const Plan& 
         mbar_wait_bounded(&sm.v_full[j % pl.vals], (j / pl.vals) & 1, kDraftWaitNs);
 }
 
-template <typename Tin>
+template <typename Tin, bool kPro>
 __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeArgs a, Plan pl)
 {
     extern __shared__ __align__(1024) uint8_t base[];
@@ -575,16 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     const Units un(total, total >= 16 * (int)gridDim.x ? 4 : total >= 4 * (int)gridDim.x ? 2 : 1);
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
-        solve<Tin>(a, pl, un, sm, base, t, 0);
+        solve<Tin, kPro>(a, pl, un, sm, base, t, 0);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSplitRegs));
         split(a, pl, un, sm, base, t - 128);
     } else if (warp < 16) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrepRegs));
-        prepare<Tin>(a, pl, un, sm, base, t - 256);
+        prepare<Tin, kPro>(a, pl, un, sm, base, t - 256);
     } else if (warp >= 20) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
-        solve<Tin>(a, pl, un, sm, base, t - 640, 1);
+        solve<Tin, kPro>(a, pl, un, sm, base, t - 640, 1);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
         if (warp == 17) multiply(a, pl, un, sm, base);
@@ -617,15 +627,15 @@ constexpr bool all_fit()
 }
 static_assert(all_fit(), "every tree has a plan");
 
-template <typename Tin>
+template <typename Tin, bool kPro>
 cudaError_t launch(const TreeDecodeArgs& a, cudaStream_t stream)
 {
     const Plan p = choose_plan(a.nodes, (int)sizeof(Tin));
     static KernelSetup setup;
-    const cudaError_t e = setup(tree_decode_tc_kernel<Tin>, 232448, kStartRegs);   // (the split needs its start)
+    const cudaError_t e = setup(tree_decode_tc_kernel<Tin, kPro>, 232448, kStartRegs);   // (the split needs its start)
     if (e != cudaSuccess) return e;
     const int total = a.batch * a.num_heads;
-    tree_decode_tc_kernel<Tin><<<total < kCtas ? total : kCtas, kThreads, p.bytes, stream>>>(a, p);
+    tree_decode_tc_kernel<Tin, kPro><<<total < kCtas ? total : kCtas, kThreads, p.bytes, stream>>>(a, p);
     return cudaGetLastError();
 }
 
@@ -633,7 +643,8 @@ cudaError_t launch(const TreeDecodeArgs& a, cudaStream_t stream)
 
 cudaError_t launch_tree_decode_tc(const TreeDecodeArgs& a, cudaStream_t stream)
 {
-    return a.bf16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+    if (a.prologue) return a.bf16 ? launch<__nv_bfloat16, true>(a, stream) : launch<float, true>(a, stream);
+    return a.bf16 ? launch<__nv_bfloat16, false>(a, stream) : launch<float, false>(a, stream);
 }
 
 }  // namespace kda
