@@ -257,6 +257,7 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
         for (uint32_t i = fill > (uint32_t)L::kSlots ? fill - L::kSlots : 0; i < fill; ++i)
             mbar_wait_bounded(&sm.kv_full[i % L::kSlots], (i / L::kSlots) & 1, kDraftWaitNs);
     if (bad_page && lane == 0) report_status(a.status, kDevBadSeqlens);
+    wait.finish();
 }
 
 // By 16-byte asynchronous copies, all four warps.
@@ -325,6 +326,7 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
     cp_wait<0>();
     while (sent != fill) hand_over();
     if (bad_page && lane == 0) report_status(a.status, kDevBadSeqlens);
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ the query rows
@@ -362,6 +364,7 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
         mbar_arrive(&sm.q_full);
     }
     if (t == 0) rec.leave(a, blockIdx.x);
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ the products
@@ -438,6 +441,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
     }
     for (int w = 0; w < 2; ++w)                     // no product or commit is in flight after this
         if (pieces[w]) wait(&sm.o_done[w], (pieces[w] - 1) & 1);
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
@@ -731,6 +735,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             if (!kWide && (w == 1 || two)) mbar_arrive(&sm.o_free[w ^ 1]);
         }
     }
+    wait.finish();
 }
 
 template <int D, bool kWide, bool kBoxes>

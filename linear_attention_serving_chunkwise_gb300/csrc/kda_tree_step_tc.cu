@@ -259,6 +259,7 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
             }
         }
     }
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ the state into tensor memory
@@ -300,6 +301,7 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
             if (++s == (uint32_t)pl.states) { s = 0; phase ^= 1; }
         }
     }
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ the products
@@ -343,6 +345,7 @@ __device__ __forceinline__ void multiply(const TreeDecodeArgs& a, const Plan& pl
         }
     }
     if (block) wait(&sm.d_full[(block - 1) & 1], ((block - 1) / 2) & 1);    // no product or commit is in flight after this
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ substitution and outputs
@@ -482,6 +485,7 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
             }
         }
     }
+    wait.finish();
 }
 
 // ------------------------------------------------------------------ copies
@@ -502,6 +506,7 @@ __device__ __forceinline__ void copy_states(const TreeDecodeArgs& a, const Plan&
     // no load is in flight when the block ends, whatever became of its reader
     for (uint32_t j = i > (uint32_t)pl.states ? i - pl.states : 0; j < i; ++j)
         mbar_wait_bounded(&sm.s_full[j % pl.states], (j / pl.states) & 1, kDraftWaitNs);
+    wait.finish();
 }
 
 // a block's rows of k (into its unit's buffer), g, q and v, by one warp, a lane to a row
@@ -546,6 +551,7 @@ __device__ __forceinline__ void copy_nodes(const TreeDecodeArgs& a, const Plan& 
         mbar_wait_bounded(&sm.r_full[j % pl.raws], (j / pl.raws) & 1, kDraftWaitNs);
     for (uint32_t j = block > (uint32_t)pl.vals ? block - pl.vals : 0; j < block; ++j)
         mbar_wait_bounded(&sm.v_full[j % pl.vals], (j / pl.vals) & 1, kDraftWaitNs);
+    wait.finish();
 }
 
 template <typename Tin, bool kPro>
