@@ -472,7 +472,9 @@ size_t kda_tree_attention_workspace_bytes(const kda_tree_attention_desc* desc);
  * nodes of other paths) does not change its output, NaN included.  A sequence whose
  * context_lens is negative, or exceeds its table row with the K nodes added, or whose tree is
  * bad, gets zeros; a token whose page id is outside [0, num_pages) is left out; both make
- * kda_last_device_status() return KDA_ERR_INVALID_ARG.  bf16: the softmax's weights are
+ * kda_last_device_status() return KDA_ERR_INVALID_ARG.  Tables with room for more than 2^31
+ * tiles of work (64 tokens of one block of rows; terabytes of cache) return
+ * KDA_ERR_UNSUPPORTED.  bf16: the softmax's weights are
  * rounded to bf16 before they meet the values (their sum is kept in fp32), fp32: fp32 throughout.
  */
 kda_status kda_tree_attention(const kda_tree_attention_desc* desc,

@@ -54,7 +54,10 @@ kda_status validate_attn(const kda_tree_attention_desc* d)
         if (s < page || s % per16) return KDA_ERR_INVALID_ARG;
         if (d->num_pages > 0 && s > (INT64_MAX >> 4) / d->num_pages) return KDA_ERR_INVALID_ARG;
     }
-    return KDA_OK;
+    kda::TreeAttnArgs a = {};
+    a.batch = d->batch; a.nodes = d->nodes; a.heads = d->num_heads; a.kv_heads = d->num_kv_heads;
+    a.page_size = d->page_size; a.table_cols = d->table_cols; a.bf16 = d->dtype == KDA_BF16;
+    return kda::tree_attn_fits(a) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
 }  // namespace

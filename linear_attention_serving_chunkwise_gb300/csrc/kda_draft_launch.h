@@ -93,6 +93,9 @@ cudaError_t launch_tree_decode_tc(const TreeDecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t stream);
 // bf16 on the tensor cores (kda_tree_attn_tc.cu), fp32 on the CUDA cores
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream);
+// whether the tables could hold no more than the kernels count
+bool tree_attn_fits(const TreeAttnArgs& a);
+bool tree_attn_tc_fits(const TreeAttnArgs& a);
 cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream);
 size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim);
 size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16);

@@ -182,7 +182,6 @@ template <int D, int TM>
 cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 {
     const attn::Shape sh = {16 * TM, kBN, kSimtCtas, 1};
-    if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     constexpr size_t smem = simt_smem<D, TM>();
     static KernelSetup setup;
     cudaError_t e = setup(tree_attn_simt_kernel<D, TM>, smem);
@@ -204,6 +203,12 @@ cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
 }
 
 }  // namespace
+
+bool tree_attn_fits(const TreeAttnArgs& a)
+{
+    const int BM = small_rows(a.nodes, a.heads / a.kv_heads) ? 16 : 64;
+    return a.bf16 ? tree_attn_tc_fits(a) : attn::line_fits(a, {BM, kBN, kSimtCtas, 1});
+}
 
 size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16)
 {

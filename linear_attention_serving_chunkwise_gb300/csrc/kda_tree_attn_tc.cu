@@ -836,7 +836,6 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
     using L = Layout<D, kWide>;
     const auto kernel = tree_attn_tc_kernel<D, kWide, kBoxes>;
     const attn::Shape sh = shape_of(kWide);
-    if (!attn::line_fits(a, sh)) return cudaErrorInvalidValue;
     Maps maps = {};
     if (kBoxes) {
         maps.box_rows = min(a.page_size & -a.page_size, kBN);
@@ -866,6 +865,8 @@ size_t tree_attn_tc_workspace_bytes(int nodes, int group, int dim)
 {
     return attn::workspace_bytes(shape_of(wide_rows(nodes, group)), dim);
 }
+
+bool tree_attn_tc_fits(const TreeAttnArgs& a) { return attn::line_fits(a, shape_of(wide_rows(a.nodes, a.heads / a.kv_heads))); }
 
 cudaError_t launch_tree_attn_tc(const TreeAttnArgs& a, cudaStream_t stream)
 {

@@ -75,6 +75,16 @@ def test_tree_attention_refusals(lib):
     assert kda.tree_attention_workspace_bytes(_desc(batch=0)) == 0
 
 
+@pytest.mark.parametrize("dtype", [kda.KDA_BF16, kda.KDA_F32])
+def test_tree_attention_refuses_more_tiles_than_it_counts(lib, dtype):
+    """2^21 pages of 64 tokens: 16 sequences x 2 heads fit 32-bit tile numbers, 4096 do not."""
+    wide = dict(dtype=dtype, page_size=64, table_cols=1 << 21, k_page_stride=64 * 2 * 128, v_page_stride=64 * 2 * 128)
+    assert kda.tree_attention_workspace_bytes(_desc(batch=16, **wide)) > 0
+    d = _desc(batch=4096, **wide)
+    assert kda.tree_attention_workspace_bytes(d) == 0
+    assert lib.kda_tree_attention(ctypes.byref(d), *[_p(0x10000000 * (i + 1)) for i in range(8)], 1 << 40, None) == UNSUP
+
+
 def test_tree_decode_and_commit_refusals(lib):
     names = ("q", "k", "v", "g", "beta", "par", "gate", "state", "out", "w")
     base = {n: 0x1000000 * (i + 1) for i, n in enumerate(names)}
