@@ -48,6 +48,7 @@ static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kO
 constexpr int kCtas = 152;                          // one to an SM
 constexpr int kHead = 2;                            // a unit's fixed cost (Q, first tile, epilogue), in tiles
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTame = 4096.f;                    // largest m sc of the form with one operation
 constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
 
 struct Shared {
@@ -393,7 +394,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             if (first) wait(&sm.kv_full[s], kp);
             if (last) advance(ks_, kp);
             tc_fence_after_sync();
-            if (elect_one()) {
+            {
                 if (wait.alive) {
                     const uint64_t qd = kmajor_base(q0 + (kWide ? w * L::kTile : 0)), kd = kmajor_base(ring + s * L::kTile);
 #pragma unroll
@@ -404,7 +405,6 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
                 if (last) umma_commit(&sm.kv_empty[s]);
                 if (i == items - 1) umma_commit(&sm.q_empty);
             }
-            __syncwarp();
         };
         auto values = [&](int i, int w) {
             const bool first = !kWide || w == 0, last = !kWide || w == 1;
@@ -418,7 +418,7 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
             tc_fence_after_sync();
-            if (elect_one()) {
+            {
                 if (wait.alive) {
                     const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
 #pragma unroll
@@ -428,7 +428,6 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
                 if (last) umma_commit(&sm.kv_empty[s]);
                 if (i + 2 >= items) umma_commit(&sm.o_done[w]);
             }
-            __syncwarp();
         };
         scores(0, 0);
         if (items > 1) scores(1, 1);
@@ -539,17 +538,28 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                     }
                 };
                 bool stored = false;
-                if (all) {
-                    // A tile that every row sees whole: the weights are formed from the last maximum (in
-                    // a piece's first tile, that of 32 tokens) while the tile's own is still being
-                    // found, and stored over the scores once it is known that it may stand (nearly always).
-                    if (!begun) {
-                        float x[32];
-                        tmem_ld32(tS, x);
-                        tmem_wait_ld();
-                        m = see ? max_of(x) : INFINITY;
-                    }
-                    const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+                if (all && !begun) {
+                    float x[32];
+                    tmem_ld32(tS, x);
+                    tmem_wait_ld();
+                    m = see ? max_of(x) : INFINITY;
+                }
+                // A tile that every row sees whole: the weights are formed from the last maximum (in
+                // a piece's first tile, that of 32 tokens) while the tile's own is still being
+                // found, and stored over the scores once it is known that it may stand (nearly always).
+                // x sc - m sc in one operation: m sc's rounding is a factor that a row's weights share, and
+                // below 2^kTame it is 2^(kTame - 24) of a power of two where the maximum changes.
+                if (all && !__any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame))) {
+                    const float2 off = make_float2(-m * sc, -m * sc);
+                    auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), sc2, off);
+                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                            sum = __fadd2_rn(sum, e);
+                            p[k] = pack_bf16x2(e.x, e.y);
+                        }
+                    };
                     float2 sum = make_float2(0.f, 0.f);
                     float top = -INFINITY;
                     uint32_t p[4][16];
@@ -781,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
             if constexpr (kBoxes) produce_boxes<D, kWide>(a, sh, maps, line, sm, base, t - kSoftmaxThreads);
             else produce_gather<D, kWide>(a, sh, line, sm, base, t - kSoftmaxThreads);
         } else if (warp == 12) {
-            multiply<D, kWide>(a, sh, line, sm, base);
+            if (elect_one()) multiply<D, kWide>(a, sh, line, sm, base);
         } else {
             query<D, kWide>(a, sh, line, sm, base, t - 13 * 32);
         }
