@@ -185,76 +185,114 @@ __device__ __forceinline__ float4* slot_out(float* slot, int BM) { return reinte
 
 // Joins the units that cross a boundary of the line: block (c, y, z) takes rows [32 y, 32 y + 32)
 // and channels [32 z, 32 z + 32) of the unit whose first part CTA c left, if there is one.
-// Lane = row.  The warps share the parts first and the channels second, as many to the parts
-// as give each two: a unit in a hundred parts is as quick to join as one in two.
-// m = max m_i, o = sum e^{m_i - m} o_i / sum e^{m_i - m} l_i, in an order set by the parts alone.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+// Lane = row.  m = max m_i, o = sum e^{m_i - m} o_i / sum e^{m_i - m} l_i, in an order set by the
+// parts alone.
+// Bound: latency, of a chain of dependent reads (the record, then the parts).  A unit in two parts
+// (most, when there are more units than CTAs) has all its reads under way at once, a warp to four
+// channels: 32 trees of 16 nodes took 253 us in all with the general form below, 247 with
+// this one.  More parts are shared by the warps first and the channels second, as many to the parts as
+// give each two, so that a unit in a hundred parts is as quick to join as one in two (this form
+// for up to four parts: 30.4 -> 33.9 us for a small fp32 call).  Blocks of 64 channels, half as many,
+// lost 5 us of 208 where the units are few and their parts many (2 x 131072 tokens).
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinChannels = 32, kFew = 2;
 
 template <typename Tout, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnArgs a, Shape sh)
 {
     constexpr int K = 2;                                     // chunks of 4 channels a warp takes at a time
+    constexpr int C4 = kJoinChannels / 4;                    // chunks of a block
+    static_assert(C4 == kJoinWarps, "a warp to a chunk");
     __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
     __shared__ float4 s_o[kJoinWarps][K][32];
-    __shared__ float4 s_out[32][9];
+    __shared__ float4 s_out[32][C4 + 1];
     const int t = threadIdx.x, lane = t & 31, w = t >> 5, c = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
     const int4 raw = *(reinterpret_cast<const int4*>(a.workspace) + c);
     const Record rec = {raw.x, raw.y, raw.z, raw.w};
     const int G = a.heads / a.kv_heads, rows = min(sh.BM, a.nodes * G - rec.r0), r0 = 32 * blockIdx.y;
     if (rec.last == 0 || r0 >= rows) return;
-    const int parts = rec.last - c + 1, r = min(r0 + lane, sh.BM - 1);
+    const int parts = rec.last - c + 1, r = min(r0 + lane, sh.BM - 1), first4 = C4 * blockIdx.z;
     const auto part = [&](int i) { return slot_of(a, sh, D, i == 0 ? 2 * c + 1 : 2 * (c + i)); };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int i = w; i < parts; i += kJoinWarps) m = fmaxf(m, part(i)[r]);
-    s_m[w][lane] = m;
-    __syncthreads();
+    // nothing to attend to: zeros; NaN stays
+    const auto over = [](float4 x, float sum) {
+        const float inv = 1.f / sum;
+        return sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    };
+    if (parts <= kFew) {
+        float pm[kFew], pl[kFew];
+        float4 po[kFew];
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, s_m[k][lane]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int i = w; i < parts; i += kJoinWarps) l = fmaf(exp2f(part(i)[r] - base), part(i)[sh.BM + r], l);
-    s_l[w][lane] = l;
-    const int pw = parts <= 4 ? 2 : parts <= 8 ? 4 : 8, cw = kJoinWarps / pw, pl = w % pw, cl = w / pw;
-    for (int k0 = 0; k0 < 8; k0 += cw * K) {
-        float4 o[K] = {};
-#pragma unroll 4
-        for (int i = pl; i < parts; i += pw) {
-            float* p = part(i);
-            const float f = exp2f(p[r] - base);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float4 x = slot_out(p, sh.BM)[(size_t)(8 * blockIdx.z + k0 + cl * K + k) * sh.BM + r];
-                o[k].x = fmaf(f, x.x, o[k].x);
-                o[k].y = fmaf(f, x.y, o[k].y);
-                o[k].z = fmaf(f, x.z, o[k].z);
-                o[k].w = fmaf(f, x.w, o[k].w);
-            }
+        for (int i = 0; i < kFew; ++i) {
+            float* p = part(min(i, parts - 1));              // (past the last the last again, which is not added twice)
+            pm[i] = p[r];
+            pl[i] = p[sh.BM + r];
+            po[i] = slot_out(p, sh.BM)[(size_t)(first4 + w) * sh.BM + r];
         }
+        float m = pm[0], l = 0.f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) s_o[w][k][lane] = o[k];
-        __syncthreads();
-        if (w < cw * K) {                                    // a warp to a chunk
-            const int k = w % K, first = (w / K) * pw;
-            float4 x = s_o[first][k][lane];
-            for (int i = 1; i < pw; ++i) {
-                const float4 y = s_o[first + i][k][lane];
-                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-            }
-            float sum = 0.f;
+        for (int i = 1; i < kFew; ++i) m = fmaxf(m, pm[i]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float4 o = {};
 #pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) sum += s_l[i][lane];
-            const float inv = 1.f / sum;                     // nothing to attend to: zeros; NaN stays
-            s_out[lane][k0 + w] = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        for (int i = 0; i < kFew; ++i) {
+            if (i >= parts) break;
+            const float f = exp2f(pm[i] - base);
+            l = fmaf(f, pl[i], l);
+            o = make_float4(fmaf(f, po[i].x, o.x), fmaf(f, po[i].y, o.y), fmaf(f, po[i].z, o.z), fmaf(f, po[i].w, o.w));
         }
+        s_out[lane][w] = over(o, l);
         __syncthreads();
+    } else {
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int i = w; i < parts; i += kJoinWarps) m = fmaxf(m, part(i)[r]);
+        s_m[w][lane] = m;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) m = fmaxf(m, s_m[k][lane]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        for (int i = w; i < parts; i += kJoinWarps) l = fmaf(exp2f(part(i)[r] - base), part(i)[sh.BM + r], l);
+        s_l[w][lane] = l;
+        const int pw = parts <= 4 ? 2 : parts <= 8 ? 4 : 8, cw = kJoinWarps / pw, pl = w % pw, cl = w / pw;
+        for (int k0 = 0; k0 < C4; k0 += cw * K) {
+            float4 o[K] = {};
+#pragma unroll 4
+            for (int i = pl; i < parts; i += pw) {
+                float* p = part(i);
+                const float f = exp2f(p[r] - base);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float4 x = slot_out(p, sh.BM)[(size_t)(first4 + k0 + cl * K + k) * sh.BM + r];
+                    o[k].x = fmaf(f, x.x, o[k].x);
+                    o[k].y = fmaf(f, x.y, o[k].y);
+                    o[k].z = fmaf(f, x.z, o[k].z);
+                    o[k].w = fmaf(f, x.w, o[k].w);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) s_o[w][k][lane] = o[k];
+            __syncthreads();
+            if (w < cw * K) {                                // a warp to a chunk
+                const int k = w % K, first = (w / K) * pw;
+                float4 x = s_o[first][k][lane];
+                for (int i = 1; i < pw; ++i) {
+                    const float4 y = s_o[first + i][k][lane];
+                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                }
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < kJoinWarps; ++i) sum += s_l[i][lane];
+                s_out[lane][k0 + w] = over(x, sum);
+            }
+            __syncthreads();
+        }
     }
     // 8 lanes to a row's 32 channels
     const int i = t >> 3, k = t & 7;
     if (r0 + i < rows) {
         const int row = rec.r0 + r0 + i;
-        Tout* dst = static_cast<Tout*>(a.out) + (((size_t)rec.b * a.nodes + row / G) * a.heads + rec.hk * G + row % G) * D + 32 * blockIdx.z + 4 * k;
+        Tout* dst = static_cast<Tout*>(a.out) + (((size_t)rec.b * a.nodes + row / G) * a.heads + rec.hk * G + row % G) * D + 4 * (first4 + k);
         const float4 x = s_out[i][k];
         if constexpr (sizeof(Tout) == 2) {
             const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
@@ -272,7 +310,7 @@ cudaError_t launch_join(const TreeAttnArgs& a, const Shape& sh, cudaStream_t str
 {
     cudaLaunchConfig_t cfg = {};
     const int rows = a.nodes * (a.heads / a.kv_heads);
-    cfg.gridDim = dim3(sh.ctas - 1, ((rows < sh.BM ? rows : sh.BM) + 31) / 32, D / 32);
+    cfg.gridDim = dim3(sh.ctas - 1, ((rows < sh.BM ? rows : sh.BM) + 31) / 32, D / kJoinChannels);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
