@@ -194,7 +194,7 @@ __device__ __forceinline__ float4* slot_out(float* slot, int BM) { return reinte
 // give each two, so that a unit in a hundred parts is as quick to join as one in two (this form
 // for up to four parts: 30.4 -> 33.9 us for a small fp32 call).  Blocks of 64 channels, half as many,
 // lost 5 us of 208 where the units are few and their parts many (2 x 131072 tokens).
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinChannels = 32, kFew = 2;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinChannels = 32;
 
 template <typename Tout, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnArgs a, Shape sh)
@@ -218,29 +218,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(TreeAttnArgs a, Shap
         const float inv = 1.f / sum;
         return sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     };
-    if (parts <= kFew) {
-        float pm[kFew], pl[kFew];
-        float4 po[kFew];
+    if (parts == 2) {
+        float pm[2], pl[2];
+        float4 po[2];
 #pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-            float* p = part(min(i, parts - 1));              // (past the last the last again, which is not added twice)
+        for (int i = 0; i < 2; ++i) {
+            float* p = part(i);
             pm[i] = p[r];
             pl[i] = p[sh.BM + r];
             po[i] = slot_out(p, sh.BM)[(size_t)(first4 + w) * sh.BM + r];
         }
-        float m = pm[0], l = 0.f;
-#pragma unroll
-        for (int i = 1; i < kFew; ++i) m = fmaxf(m, pm[i]);
-        const float base = m == -INFINITY ? 0.f : m;
-        float4 o = {};
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-            if (i >= parts) break;
-            const float f = exp2f(pm[i] - base);
-            l = fmaf(f, pl[i], l);
-            o = make_float4(fmaf(f, po[i].x, o.x), fmaf(f, po[i].y, o.y), fmaf(f, po[i].z, o.z), fmaf(f, po[i].w, o.w));
-        }
-        s_out[lane][w] = over(o, l);
+        const float m = fmaxf(pm[0], pm[1]), base = m == -INFINITY ? 0.f : m;
+        const float f0 = exp2f(pm[0] - base), f1 = exp2f(pm[1] - base);
+        s_out[lane][w] = over(make_float4(fmaf(f1, po[1].x, f0 * po[0].x), fmaf(f1, po[1].y, f0 * po[0].y),
+                                          fmaf(f1, po[1].z, f0 * po[0].z), fmaf(f1, po[1].w, f0 * po[0].w)),
+                              fmaf(f1, pl[1], f0 * pl[0]));
         __syncthreads();
     } else {
         float m = -INFINITY;

@@ -116,8 +116,10 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p)
 
 // (Loops are unrolled little: the roles run side by side, and straight-line code for each would
 // be fetched anew for every block.)
-// units handled side by side by the preparation and by the substitution
-__host__ __device__ constexpr int groups_of(int K) { return K <= NB ? 2 : 1; }
+// Units handled side by side by the preparation and by the substitution (trees of one block only).  One
+// group's code is fetched by more warps at the same time, two shorten the chain of steps that a
+// block is: 64 x 96 heads x 12 nodes take 189 us with one and 209 with two, x 16 nodes 240 and 229.
+__host__ __device__ constexpr int groups_of(int K) { return K > 12 && K <= NB ? 2 : 1; }
 
 // kPro (all of them): the input prologue is compiled in (own instances; the common ones stay small)
 template <typename Tin, bool kPro>
@@ -588,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const Units un(total, total >= 16 * (int)gridDim.x ? 4 : total >= 4 * (int)gridDim.x ? 2 : 1);
+    // (64 x 96 heads x 16 nodes: 235 us in runs of one unit, 229 of four; 16 x 96: 66 and 72)
+    const Units un(total, total >= 32 * (int)gridDim.x ? 4 : 1);
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
         solve<Tin, kPro>(a, pl, un, sm, base, t, 0);

@@ -252,9 +252,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a)
 
 }  // namespace
 
-// A CTA spends about 4 us on the walk and on meeting its cluster, whatever its slice; past this
-// many CTAs (some 7 to an SM, 4 at a time) a cluster is made smaller and its slices longer.
-constexpr long long kMostCtas = 1100;
+// A CTA spends about 4 us on the walk and on meeting its cluster, whatever its slice.  So all CTAs
+// should run at once (4 to an SM): a cluster is made smaller and its slices longer until they do.  256
+// rows of 100003: 62 us with clusters of 2, 64 of 4, 75 of 8; of 32000: 26, 35; 100 trees
+// over 131072: 28 us with 4, 37 with 8, 35 with 2.
+constexpr long long kMostCtas = 4 * 152;
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream)
 {
