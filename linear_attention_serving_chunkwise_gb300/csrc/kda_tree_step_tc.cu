@@ -57,6 +57,11 @@ struct Shared {
     uint32_t tmem;
 };
 
+// Units handled side by side by the preparation and by the substitution (trees of one block only).  One
+// group's code is fetched by more warps at the same time, two shorten the chain of steps that a
+// block is: 64 x 96 heads x 12 nodes take 189 us with one and 209 with two, x 16 nodes 240 and 229.
+__host__ __device__ constexpr int groups_of(int K) { return K > 12 && K <= NB ? 2 : 1; }
+
 __host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, int vals, int keys)
 {
     Plan p = {};
@@ -68,8 +73,8 @@ __host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, 
     p.raw = at; at += raws * NB * D * (esz + 4);    // of each block g, then q
     p.v = at; at += vals * NB * D * esz;
     p.k = at; at += keys * K * D * esz;
-    p.g = at; at += (K <= NB ? 2 : 1) * K * D * 4;
-    p.w = at; at += (K <= NB ? 2 : 1) * K * D * 4;
+    p.g = at; at += groups_of(K) * K * D * 4;
+    p.w = at; at += groups_of(K) * K * D * 4;
     p.ap = at; at += 2 * NB * ((K + 1) & ~1) * 8;   // two blocks' rows of (A, P), rows of 16-byte multiples
     p.shared = (at + 15) & ~15;
     p.state = (p.shared + (int)sizeof(Shared) + 127) & ~127;
@@ -116,11 +121,6 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* p)
 
 // (Loops are unrolled little: the roles run side by side, and straight-line code for each would
 // be fetched anew for every block.)
-// Units handled side by side by the preparation and by the substitution (trees of one block only).  One
-// group's code is fetched by more warps at the same time, two shorten the chain of steps that a
-// block is: 64 x 96 heads x 12 nodes take 189 us with one and 209 with two, x 16 nodes 240 and 229.
-__host__ __device__ constexpr int groups_of(int K) { return K > 12 && K <= NB ? 2 : 1; }
-
 // kPro (all of them): the input prologue is compiled in (own instances; the common ones stay small)
 template <typename Tin, bool kPro>
 __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl, Units un, Shared& sm, uint8_t* base, int t)
@@ -617,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     if (warp == 17) tmem_dealloc(sm.tmem, 512);
 }
 
-// Buffers for K nodes: as much in double (v, which waits for the last of the roles, in fourfold) as
-// leaves the states three quarters or more (48 KB in flight cover HBM's latency).
+// Buffers for K nodes: as much in double (v, which waits for the last of the roles, in fourfold: 154 us
+// for 64 x 96 heads x 8 nodes, 208 with two of v and one unit's k) as leaves the states three
+// quarters or more (48 KB in flight cover HBM's latency).
 constexpr Plan choose_plan(int K, int esz)
 {
     constexpr int options[6][5] = {{2, 2, 4, 2, 4}, {2, 2, 4, 2, 3}, {2, 2, 2, 1, 3}, {1, 2, 2, 2, 3}, {1, 2, 2, 1, 3}, {1, 1, 1, 1, 3}};
@@ -628,10 +629,18 @@ constexpr Plan choose_plan(int K, int esz)
     }
     return {};
 }
+// Two groups take their units in turn, and a wait by parity can be one phase ahead at most: each
+// group needs slots of its own in the rings it waits on (k comes with g and q).
+constexpr bool plan_ok(int K, int esz)
+{
+    const Plan p = choose_plan(K, esz);
+    const int g = groups_of(K);
+    return p.bytes > 0 && p.tiles % g == 0 && p.raws % g == 0 && p.vals % g == 0;
+}
 constexpr bool all_fit()
 {
     for (int K = 1; K <= kTreeMaxNodes; ++K)
-        if (choose_plan(K, 2).bytes == 0 || choose_plan(K, 4).bytes == 0) return false;
+        if (!plan_ok(K, 2) || !plan_ok(K, 4)) return false;
     return true;
 }
 static_assert(all_fit(), "every tree has a plan");
