@@ -5,7 +5,8 @@
 // head, then row block; before a unit's tiles a few places stand for its fixed cost), and CTA
 // c of N takes the places [start(c), start(c + 1)) with start(c) = floor(T c / N): every CTA
 // gets the same share (a place more or less) whatever the mix of lengths, a long sequence
-// is split over many CTAs and a short one is not.  The context lengths live on the device, so each CTA works its cut out for itself.
+// is split over many CTAs and a short one is not.  The context lengths live on the device, so each
+// CTA works its cut out for itself (one warp's scan over the lengths, about 1 us for 64).
 //
 // A unit that lies within one CTA's range is finished there.  Of any other, each CTA leaves
 // its part (running maximum, sum and unnormalised output per row, fp32) in the workspace:

@@ -14,13 +14,21 @@
 // (until then the weights are at most 2^8, which bf16 and the fp32 sums hold as well).
 //
 // Warps 0-3 and 4-7: softmax and epilogue of stream 0 and 1, a row to a thread.  Warps 8-11:
-// the cache rows, into a ring of K and V tiles.  Warp 12 issues the products, warps
+// the cache rows, into a ring of K and V tiles.  A thread of warp 12 issues the products, warps
 // 13-15 copy Q.  The last two groups give registers to the softmax.
+//
+// Bound: HBM's read of the cache for few rows, the tensor pipe (2048 cycles a tile of 256 rows x 128
+// tokens, D = 128) and the chain scores - softmax - values of each stream for many; a tile took
+// 3000 cycles when 2700 of them were HBM's.  Join included, of a copy's 6.8 TB/s: 2 sequences
+// of 131072 tokens, 8 cache heads, 64 rows a head 171 us, 6.3 TB/s; 256 rows 208 us, 5.2 TB/s and
+// 1320 TFLOP/s; 32 trees of 16 nodes, 512 to 16384 tokens, 192 rows 223 us, 5.2 TB/s; one node over
+// 1500 tokens 18 us, latency (the first tile's way, the join).
 //
 // The cache rows come by TMA where the page size is a multiple of 8: a tile is a stack of boxes
 // of 8 to 128 rows (the largest power of two in the page size), and 8 rows are one swizzle
 // atom, so boxes of any pages stack into the tile the products read.  Other page sizes are
-// gathered with 16-byte asynchronous copies, a row to half a warp.
+// gathered with 16-byte asynchronous copies, a row to half a warp (where both can be used: 208 us
+// by boxes, 246 gathered for 256 rows; 171 and 207 for 64).
 // Every wait is bounded; a thread that gave up goes through the rest of its schedule without
 // waiting and without touching the tensor core, and the status word says so.
 //
@@ -56,8 +64,8 @@ constexpr float kGrow = 8.f;                        // powers of two a maximum m
 struct Shared {
     uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done[2], o_free[2];
     uint64_t bad_nodes[8];                          // by piece: nodes with non-finite values
-    alignas(16) uint32_t missing[8][4];                         // by tile: its tokens without a page (a V tile is freed after its softmax, so the
-                                                    // copies are never more than 6 tiles past the one the softmax is at)
+    alignas(16) uint32_t missing[8][4];             // by tile: its tokens without a page (a V tile is freed after its
+                                                    // softmax, so the copies are at most 6 tiles past it)
     TreeSmem tree[2];                               // one for each stream: they may be at different pieces
     uint32_t tmem;
 };
@@ -431,6 +439,8 @@ __device__ __forceinline__ void multiply(const TreeAttnArgs& a, const attn::Shap
                 if (i + 2 >= items) umma_commit(&sm.o_done[w]);
             }
         };
+        // (one thread for all of it: with the whole warp in the waits and a thread elected for each
+        // group of products their issue took 3000 cycles a tile, now 2150 of the pipe's 2048)
         scores(0, 0);
         if (items > 1) scores(1, 1);
         for (int i = 0; i < items; i += 2) {        // both streams in turn
@@ -529,7 +539,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                 const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
                 const bool all = t0 + kBN <= pc.ctx && !(missing.x | missing.y | missing.z | missing.w);
                 const float2 sc2 = make_float2(sc, sc);
-                // (x - m) sc in this order: the difference is exact where it matters, however large the scores
+                // (x - m) sc in this order: the difference is exact where it matters, whatever the scores
                 auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -550,7 +560,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
                 // a piece's first tile, that of 32 tokens) while the tile's own is still being
                 // found, and stored over the scores once it is known that it may stand (nearly always).
                 // x sc - m sc in one operation: m sc's rounding is a factor that a row's weights share, and
-                // below 2^kTame it is 2^(kTame - 24) of a power of two where the maximum changes.
+                // up to kTame it is 2^-13 of a weight, below bf16's rounding, where the maximum changes.
                 if (all && !__any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame))) {
                     const float2 off = make_float2(-m * sc, -m * sc);
                     auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
@@ -805,6 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
     if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
+// 256-row units where 128 would not hold all rows of a (sequence, head): every tile is then read and
+// turned into operands once.  256 rows, 2 x 131072 tokens: 208 us wide, 324 in two units of 128;
+// 128 rows: 190 wide (half of it empty), 178 with both streams on them.
 bool wide_rows(int nodes, int group) { return nodes * group > 128; }
 attn::Shape shape_of(bool wide) { return {wide ? 256 : 128, kBN, kCtas, kHead}; }
 

@@ -13,14 +13,17 @@
 //     16        copies states in quarters of 16 KB (what keeps HBM busy), 18 the nodes' k, q, g and v,
 //               rows of 256 or 512 bytes: no other warp loads them, so none waits for memory
 //     4 - 7     split a state into tensor memory
-//     8 - 15    prepare a block (eight warps, or four each in turn where a unit is one block): G along the paths, e^G k and e^G q split into the B operand, and
-//               A_ij = <e^{G_i - G_j} k_i, k_j>, P_ij = <e^{G_i - G_j} q_i, k_j> on the ancestor pairs
-//               alone, each exponential of a difference <= 0 (a factored e^{-G_j} would overflow)
-//     17        issues the products
-//     0 - 3, 20 - 23   substitution and outputs: a unit of one block each in turn (the substitution
-//               is a chain of short steps, the longest of the roles); larger trees the first alone
-// Bound: the warps' issue slots (about 11 K instructions a block) beside HBM's one read of the state.
-// Every wait is bounded (Waiter).
+//     8 - 15    prepare a block (all eight, or four each in turn: groups_of): G along the paths, e^G k
+//               and e^G q split into the B operand, and A_ij = <e^{G_i - G_j} k_i, k_j>, P_ij =
+//               <e^{G_i - G_j} q_i, k_j> on the ancestor pairs alone, each
+//               exponential of a difference <= 0 (a factored e^{-G_j} would overflow)
+//     17        issues the products (an elected thread at a time; one thread throughout was no faster)
+//     0 - 3, 20 - 23   substitution and outputs, a chain of short steps: the first four alone, or
+//               in turn with the others (groups_of)
+// Bound: the warps' instructions (about 11 K a block, half of the issue slots) and their supply, with
+// the roles' code side by side in one instruction cache; HBM's one read of the state would allow
+// two and a half times the speed.  64 x 96 heads: 1 node 121 us, 3.5 TB/s; 8 nodes 154 us; 16 nodes 229 us,
+// 2.7 TB/s; 96 units of 6 nodes 9 us.  Every wait is bounded (Waiter).
 #include "kda_draft_launch.h"
 #include "kda_draft_sm100.cuh"
 #include "kda_tree.cuh"

@@ -18,7 +18,10 @@
 // sampled.  The quotient is formed only where it can win: rest / noise > best is first tested as
 // rest >= best (1 - 2^-21) noise, which no rounding can turn down wrongly, with the best of the
 // whole warp, so that after the first batch few elements get as far as a division.
-// Bound: HBM, 8 bytes (12 after a turned-down draft) per vocabulary entry.
+// Bound: HBM, 8 bytes (12 after a turned-down draft) per vocabulary entry, behind the walk's
+// latency (about 4 us).  One row of 32003: 7.7 us; 64 trees of 32 nodes over 131072: 22 us (67 MB,
+// 3.0 TB/s); 256 chains of 4 over 100003: 62 us (281 MB with the drafts' rows, 4.5 TB/s of the
+// copy's 6.8).  512 threads of 32 registers, 4 CTAs an SM: loads in flight are what it needs.
 #include <cooperative_groups.h>
 
 #include "kda_draft_launch.h"
