@@ -62,6 +62,39 @@ def test_verify_all_kept_and_all_turned_down(cuda_lib, draft, u):
     assert u > 0 or (got[1] == 5).all()
 
 
+def _offset(x, by, guard):
+    """x on the GPU, `by` elements into a buffer whose other elements are `guard`."""
+    flat = torch.full((x.size + 8,), guard, dtype=torch.from_numpy(x).dtype, device="cuda")
+    flat[by:by + x.size] = torch.from_numpy(x).cuda().flatten()
+    return flat[by:by + x.size].view(x.shape)
+
+
+@pytest.mark.parametrize("by", [(0, 0, 0), (1, 2, 3), (3, 1, 2), (2, 0, 1)])
+@pytest.mark.parametrize("V", [5, 8, 9, 70, 1031, 8200, 40003])
+def test_verify_any_entry_can_win_whatever_the_alignment(cuda_lib, V, by):
+    """One entry of each row stands out, at the ends of the row, of slices and of copies; what lies next
+    to the arrays would win if it were read.  Rows 1 on: a turned-down draft, so that its row counts."""
+    at = sorted({v for e in (0, V // 8 & ~3, V // 4 & ~3, V // 2, 1028, 2052, V) for v in range(e - 6, e + 7) if 0 <= v < V})
+    r = np.random.default_rng(V)
+    B = len(at)
+    target = r.random((B, 2, V), dtype=np.float32) * np.float32(1e-3)
+    target[np.arange(B), 0, at] = 1.0
+    noise = r.random((B, V), dtype=np.float32) + np.float32(0.5)
+    q = r.random((B, 1, V), dtype=np.float32) * np.float32(1e-4)
+    tokens = np.array([[(v + 1) % V] for v in at], np.int32)
+    q[np.arange(B), 0, tokens[:, 0]] = 1.0
+    parents = np.full((B, 1), -1, np.int32)
+    parents[0] = -2
+    u = np.full((B, 1), 0.5, np.float32)
+    c = lambda x: torch.from_numpy(x).cuda()
+    got = cuda_lib.verify_drafts(_offset(target, by[0], 1e30), c(tokens), c(parents), c(u), _offset(noise, by[1], 1e-30),
+                                 draft_probs=_offset(q, by[2], -1e30))
+    torch.cuda.synchronize()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+    assert np.array_equal(got[2].cpu().numpy(), np.array(at, np.int32))
+    _same([x.cpu().numpy() for x in got], R.verify(target, q, tokens, parents, u, noise))
+
+
 def test_verify_nothing_left_and_ties(cuda_lib):
     """p = q where p(x) = 0: nothing is left after the turned-down token, the row itself is drawn from;
     equal scores go to the lowest index."""
