@@ -5,8 +5,8 @@
 // running maximum and sum of the softmax; query heads of one group share each loaded tile.
 // Bound: for few rows latency (a tile's loads, scores, softmax and values follow one another, two
 // CTAs to an SM cover some of it), for many the CUDA cores' fp32 rate.  7 sequences of up to 3001
-// tokens, 5 nodes, 6 heads on 2 cache heads, D = 64: 30 us, 0.37 TB/s, join included; 16 with
-// 32 nodes: 79 us, 14 TFLOP/s.
+// tokens, 5 nodes, 6 heads on 2 cache heads, D = 64: 28 us, 0.40 TB/s, join included; 16 with
+// 32 nodes: 75 us, 15 TFLOP/s.
 //
 // A tile's values are zeroed where no row may see the token (past the last node, a page out
 // of range): a masked weight is 0, and 0 times whatever lies there must not be NaN.  In the
@@ -75,24 +75,41 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
         for (int tile = pc.first; live && tile < pc.last; ++tile) {
             const int t0 = tile * kBN;
             if (tile != pc.first) __syncthreads();
-            for (int idx = t; idx < kBN * (D / 4); idx += kThreads) {
-                const int j = idx / (D / 4), c = 4 * (idx - j * (D / 4)), pos = t0 + j;
-                float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-                bool on = false;
-                if (pos < n) {
-                    const int pg = pos / a.page_size, id = a.block_table[(size_t)b * a.table_cols + pg];
-                    on = id >= 0 && id < a.num_pages;
+            // a thread has four channels of every (kThreads / (D / 4))-th token; its page ids are read
+            // together, then four rows of K and V at a time: two trips to memory instead of two a token
+            // (7 sequences of up to 12000 tokens, D = 128: 114 -> 97 us)
+            constexpr int kRows = kBN * (D / 4) / kThreads, kStep = kThreads / (D / 4);
+            const int j0 = t / (D / 4), c = 4 * (t % (D / 4));
+            size_t at[kRows];
+            int id[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int pos = t0 + j0 + i * kStep, pg = pos / a.page_size;
+                at[i] = ((size_t)(pos - pg * a.page_size) * a.kv_heads + hk) * D + c;
+                id[i] = pos < n ? __ldg(a.block_table + (size_t)b * a.table_cols + pg) : -1;
+            }
+#pragma unroll
+            for (int i0 = 0; i0 < kRows; i0 += 4) {
+                float4 k4[4], v4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = id[i0 + i];
+                    const bool on = p >= 0 && p < a.num_pages;
+                    k4[i] = v4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (on) {
-                        const size_t off = ((size_t)(pos - pg * a.page_size) * a.kv_heads + hk) * D + c;
-                        k4 = load4(static_cast<const float*>(a.k_cache) + (size_t)id * a.k_page_stride + off);
-                        v4 = load4(static_cast<const float*>(a.v_cache) + (size_t)id * a.v_page_stride + off);
-                    } else {
-                        bad_page = true;
+                        k4[i] = load4(static_cast<const float*>(a.k_cache) + (size_t)p * a.k_page_stride + at[i0 + i]);
+                        v4[i] = load4(static_cast<const float*>(a.v_cache) + (size_t)p * a.v_page_stride + at[i0 + i]);
                     }
                 }
-                if (c == 0) s_on[j] = on;
-                *reinterpret_cast<float4*>(sk + j * LD + c) = k4;
-                *reinterpret_cast<float4*>(sv + j * LD + c) = v4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + (i0 + i) * kStep, p = id[i0 + i];
+                    const bool on = p >= 0 && p < a.num_pages;
+                    bad_page |= !on && t0 + j < n;
+                    if (c == 0) s_on[j] = on;
+                    *reinterpret_cast<float4*>(sk + j * LD + c) = k4[i];
+                    *reinterpret_cast<float4*>(sv + j * LD + c) = v4[i];
+                }
             }
             __syncthreads();
             float s[TM][4] = {};
@@ -197,7 +214,8 @@ cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 
 // rows of a unit: 16 while the whole (sequence, head) fits them (the other rows of a larger
 // block would be computed for nothing: 15 rows take 30 us, in a block of 64 40 us), 64 otherwise
-// (each loaded tile serves four times the rows: 96 rows take 79 us, in blocks of 16 107 us)
+// (each loaded tile serves four times the rows: 96 rows take 79 us, in blocks of 16 107 us; all
+// four before the page ids were read together)
 bool small_rows(int nodes, int group) { return nodes * group <= 16; }
 
 cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
