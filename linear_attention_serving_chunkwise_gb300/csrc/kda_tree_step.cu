@@ -14,9 +14,9 @@
 // Here: the step for dk = 64 on the CUDA cores (dk = 128: kda_tree_step_tc.cu), and the commit.
 // The step's bound: instruction issue and shared memory, 64 x 96 heads x 16 nodes 204 us, 1.05 TB/s;
 // at dk = 128 this form took 666 us where the tensor cores' takes 229.  The commit's: HBM, one read
-// and one write of the state; 256 x 96 heads, dk = 128: 530 us, 6.1 TB/s, 0.90 of a copy's rate.  A CTA
-// a state in registers (two to an SM) has its 64 KB in flight at once, and the path's few
-// vectors are folded while the state arrives.
+// and one write of the state; 256 x 96 heads, dk = 128: 464 us, 6.9 TB/s, the rate of a copy.  A CTA a
+// state in registers has its 64 KB in flight at once, and the path's few vectors are folded
+// while the state arrives.
 #include "kda_draft_launch.h"
 #include "kda_tree.cuh"
 
@@ -177,8 +177,11 @@ constexpr int kCommitThreads = 256;
 constexpr int kCommitChunk = 8;      // path tokens folded into one update of the state
 
 // One CTA per (sequence, head); a thread holds D / (256 / (D/4)) rows of one float4 column.
+// CTAs an SM has room for, which is what keeps HBM busy while each waits for its path's vectors:
+// 256 x 96 heads x 8 nodes took 530 us with two of dk = 128, 464 with three; of dk = 64 188 with
+// two, 162 with four, 132 with six, 145 with eight (whose 32 registers a thread spill).
 template <typename Tin, int D>
-__global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreeCommitArgs a)
+__global__ void __launch_bounds__(kCommitThreads, D == 128 ? 3 : 6) tree_commit_kernel(TreeCommitArgs a)
 {
     constexpr int C4 = D / 4, RG = kCommitThreads / C4, RP = D / RG, NW = kCommitThreads / 32;
     const int K = a.nodes, H = a.num_heads;
