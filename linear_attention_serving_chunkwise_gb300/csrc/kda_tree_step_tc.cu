@@ -5,7 +5,7 @@
 // X = (e^G k)^T S and Y = (e^G q)^T S, one MMA group gives all 32 rows of a block: the state is
 // the A operand in tensor memory (lane = value channel, column = key channel), the block's e^G k
 // and e^G q are the B operand.  The outputs are fp32, so both operands are split into two tf32
-// parts, x = hi + lo to 2^-24: D = S_hi (E_hi | E_lo) + S_lo E_hi, the dropped lo lo product
+// parts, x = hi + lo to 2^-23: D = S_hi (E_hi | E_lo) + S_lo E_hi, the dropped lo lo product
 // being of the size of an fp32 rounding.  A value channel's X and Y then lie in one lane, and the
 // forward substitution over the nodes runs there in registers, one thread per channel.
 //
@@ -87,11 +87,14 @@ __host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, 
     return p;
 }
 
-// x rounded to tf32 (half away from zero), in two integer operations: the conversion
-// instruction runs at a quarter of their rate and would be the state split's bound.
-__device__ __forceinline__ float to_tf32(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
-// the same for an operand of the tensor core, which drops the low bits itself
-__device__ __forceinline__ float as_tf32(float x) { return __uint_as_float(__float_as_uint(x) + 0x1000u); }
+// A value in two tf32 parts, high and low: the high one rounded to nearest (half away from zero) in two
+// integer operations (the conversion instruction runs at a quarter of their rate and would be
+// the state split's bound), the low one what is left of it, at most 12 significant bits of which the tensor core
+// drops the last: x = hi + lo to 2^-23 of x.  (Rounded once more in place of dropped, that bit
+// would count one up instead of one down.)  The addition wraps a NaN around: those of the GPU's own
+// arithmetic, 0x7fffffff, become a zero.  What is left of a NaN is a NaN, though, so it stays one in
+// the low part, which is therefore not touched again.
+__device__ __forceinline__ float tf32_high(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
 // A CTA's units: runs of `run` consecutive ones (heads of a sequence, which share its tree), dealt to
 // the CTAs in turn, since trees differ in depth and so in work (a contiguous share each: the last CTA
@@ -200,10 +203,10 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
                     const float kx = kk[s] * e[s], qx = qq[s] * e[s];
-                    kh[s] = to_tf32(kx);
-                    kl[s] = as_tf32(kx - kh[s]);
-                    qh[s] = to_tf32(qx);
-                    ql[s] = as_tf32(qx - qh[s]);
+                    kh[s] = tf32_high(kx);
+                    kl[s] = kx - kh[s];
+                    qh[s] = tf32_high(qx);
+                    ql[s] = qx - qh[s];
                 }
                 float4* at = reinterpret_cast<float4*>(et + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
                 at[0] = make_float4(kh[0], kh[1], kh[2], kh[3]);
@@ -289,9 +292,9 @@ __device__ __forceinline__ void split(const TreeDecodeArgs& a, const Plan& pl, U
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float x = src[(c + i) * D], h = to_tf32(x);
+                    const float x = src[(c + i) * D], h = tf32_high(x);
                     hi[i] = __float_as_uint(h);
-                    lo[i] = __float_as_uint(as_tf32(x - h));
+                    lo[i] = __float_as_uint(x - h);
                 }
                 tmem_st16u(tmem_addr(sm.tmem, quad, kColHi + 32 * k + c), hi);
                 tmem_st16u(tmem_addr(sm.tmem, quad, kColLo + 32 * k + c), lo);

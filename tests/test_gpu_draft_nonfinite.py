@@ -1,0 +1,102 @@
+"""Infinities and NaN in the inputs of KDA on draft trees: what they reach, and nothing else.
+
+A NaN has more than one bit pattern: what the GPU's own arithmetic produces is 0x7fffffff, what
+torch writes is 0x7fc00000, and any payload may come from elsewhere."""
+import numpy as np
+import pytest
+import torch
+
+import _draft_ref as R
+import kda_workloads as W
+
+pytestmark = pytest.mark.gpu
+TYPES = [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 128), (torch.float32, 64)]
+IDS = ["bf16-128", "bf16-64", "fp32-128", "fp32-64"]
+ORDER = ("q", "k", "v", "g", "beta")
+
+
+def _inputs(B, K, H, D, dtype, seed):
+    inp = W.make_decode_inputs(W.DecodeConfig("tree", B, H, D, D, dtype, K), seed=seed)
+    return {n: inp[n].transpose(0, 1).contiguous().cuda() for n in ORDER}, inp["state0"].cuda()
+
+
+def _step(kda, x, parents, state, **kw):
+    out, writes = kda.tree_decode(*(x[n] for n in ORDER), torch.from_numpy(parents).cuda(), state, **kw)
+    torch.cuda.synchronize()
+    assert kda.last_device_status() == kda.KDA_OK
+    return out.cpu(), writes.cpu()
+
+
+def _bits(word):
+    return torch.tensor([word - (1 << 32) if word >= 1 << 31 else word], dtype=torch.int32, device="cuda").view(torch.float32)
+
+
+@pytest.mark.parametrize("K", [1, 5, 16, 20])
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_tree_decode_shows_a_diverged_state(cuda_lib, dtype, D, K):
+    """One NaN or infinite element of a state: its value channel of that head, in every node, and nothing else."""
+    B, H, b, h, c, d = 2, 3, 1, 2, 37, 11
+    x, s0 = _inputs(B, K, H, D, dtype, seed=5 + K)
+    parents = R.trees("random", B, K, seed=K)
+    clean = _step(cuda_lib, x, parents, s0)
+    inf = torch.full((1,), float("inf"), device="cuda")
+    words = {"inf - inf": inf - inf, "inf": inf, "-inf": -inf}
+    words.update({hex(w): _bits(w) for w in (0x7fffffff, 0xffffffff, 0x7fc00000, 0x7f800001, 0xff801234)})
+    for name, word in words.items():
+        state = s0.clone()
+        state[b, h, c, d:d + 1] = word
+        for what, got, want in zip(("out", "writes"), _step(cuda_lib, x, parents, state), clean):
+            hit = torch.zeros(B, K, H, D, dtype=torch.bool)
+            hit[b, :, h, d] = True
+            assert torch.equal(got[~hit], want[~hit]), (name, what)
+            assert not got[hit].isfinite().any(), (name, what)
+            if "inf" not in name or name == "inf - inf":
+                assert got[hit].isnan().all(), (name, what)
+
+
+@pytest.mark.parametrize("word", [0x7fffffff, 0xffffffff, 0x7fc00000])
+@pytest.mark.parametrize("K,j", [(5, 2), (16, 3), (20, 1), (40, 18)])
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_tree_decode_passes_on_a_nodes_nan(cuda_lib, dtype, D, K, j, word):
+    """A NaN in one node's row: that node and those below it (q: that node's output alone)."""
+    B, H, h, c = 1, 2, 1, 50
+    x, s0 = _inputs(B, K, H, D, dtype, seed=9 + K)
+    parents = R.trees("random", B, K, seed=K + 1)
+    below = torch.tensor([j in R.path_to(parents[0], i) for i in range(K)])
+    own = torch.arange(K) == j
+    clean = _step(cuda_lib, x, parents, s0)
+    for name in ORDER:
+        bad = {n: x[n].clone() for n in ORDER}
+        at = bad[name][0, j, h]
+        (at if name == "beta" else at[c:c + 1]).copy_(_bits(word).to(bad[name].dtype).squeeze(0) if name == "beta" else _bits(word).to(bad[name].dtype))
+        got = _step(cuda_lib, bad, parents, s0)
+        for what, g, w in zip(("out", "writes"), got, clean):
+            hit = torch.zeros(B, K, H, D, dtype=torch.bool)
+            nodes = own & (what == "out") if name == "q" else below
+            if name == "v":
+                hit[0, nodes, h, c] = True
+            else:
+                hit[0, nodes, h] = True
+            assert torch.equal(g[~hit], w[~hit]), (name, what)
+            assert g[hit].isnan().all(), (name, what)
+
+
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_tree_commit_shows_what_is_on_the_path(cuda_lib, dtype, D):
+    """A NaN state element stays; rows that the path does not name are not looked at."""
+    B, K, H = 2, 6, 2
+    x, s0 = _inputs(B, K, H, D, dtype, seed=3)
+    w = torch.randn(B, K, H, D, device="cuda")
+    path = torch.tensor([[0, 2, 5, -1, -1, -1]] * B, dtype=torch.int32, device="cuda")
+    n = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    clean = cuda_lib.tree_commit(x["k"], x["g"], w, path, n, s0.clone())
+    bad = {m: x[m].clone() for m in ("k", "g")}
+    for t in (bad["k"], bad["g"], w):
+        t[:, [1, 3, 4]] = float("nan")
+    state = s0.clone()
+    state[1, 1, 7, 9:10] = _bits(0x7fffffff)
+    cuda_lib.tree_commit(bad["k"], bad["g"], w, path, n, state)
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+    hit = torch.zeros(B, H, D, D, dtype=torch.bool, device="cuda")
+    hit[1, 1, 7, 9] = True
+    assert state[hit].isnan().all() and torch.equal(state[~hit], clean[~hit])
