@@ -476,8 +476,8 @@ __device__ __forceinline__ void solve(const TreeDecodeArgs& a, const Plan& pl, U
                     }
                     float wi = beta[k] * (v[k] - xi);
                     yi = fmaf(own[k], wi, yi);
-                    if (cnt[k] < 0) wi = yi = 0.f;
                     if (a.gate) yi = gate1(yi, __ldg(a.gate + at));
+                    if (cnt[k] < 0) wi = yi = 0.f;              // an absent node, whatever its rows hold (its gate too)
                     sw[(i0 + i) * D] = wi;
                     a.writes[at] = wi;
                     a.out[at] = yi;

@@ -100,3 +100,21 @@ def test_tree_commit_shows_what_is_on_the_path(cuda_lib, dtype, D):
     hit = torch.zeros(B, H, D, D, dtype=torch.bool, device="cuda")
     hit[1, 1, 7, 9] = True
     assert state[hit].isnan().all() and torch.equal(state[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("K", [6, 16, 40])
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_absent_nodes_are_zero_whatever_their_rows_hold(cuda_lib, dtype, D, K):
+    """NaN in every input row of the absent nodes, the output gate's logits among them."""
+    B, H = 3, 2
+    x, s0 = _inputs(B, K, H, D, dtype, seed=2 + K)
+    parents = R.trees("ragged", B, K, seed=K)
+    gone = torch.from_numpy(parents == R.PAD)
+    assert gone.any()
+    z = torch.randn(B, K, H, D, device="cuda")
+    clean = _step(cuda_lib, x, parents, s0, gate=z)
+    for t in (*x.values(), z):
+        t[gone.cuda()] = float("nan")
+    for what, got, want in zip(("out", "writes"), _step(cuda_lib, x, parents, s0, gate=z), clean):
+        assert not got[gone].any(), what
+        assert torch.equal(got, want), what
