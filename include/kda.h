@@ -496,6 +496,7 @@ kda_status kda_tree_attention(const kda_tree_attention_desc* desc,
  *   writes  [B, K, H, dv] fp32, beta_i (v_i - S'_i^T k_i) with S'_i the decayed state of
  *           the parent: what kda_tree_commit needs;  zeros for absent nodes
  * prologue as kda_decode.  out and writes overlap nothing.  Depth is not limited below K.
+ * g may be -inf (or so low that e^g is zero): the node then starts from an empty state.
  */
 kda_status kda_tree_decode(int32_t batch, int32_t nodes, int32_t num_heads, int32_t dk, int32_t dv,
                            int32_t qkv_dtype, int32_t prologue,

@@ -11,6 +11,20 @@ namespace kda {
 constexpr int kTreeMaxNodes = 64;   // KDA_TREE_MAX_NODES: one bit of a 64-bit mask per node
 constexpr int kTreePad = -2;        // KDA_TREE_PAD
 
+// g as the tree kernels sum it along a path.  e^g is zero in fp32 below -104, and a g of -inf (the state is
+// forgotten there) would make differences of later sums inf - inf.  So g counts as -105 at least: G
+// stays finite, and e^{G_i - G_j} is zero where such a node lies between the two and untouched by
+// it elsewhere, but for G's rounding (2^-25 of |G|, which each such node makes 105 larger).
+// A NaN stays one.  With the prologue g is -5 or more.
+constexpr float kGLeast = -105.f;
+__device__ __forceinline__ float path_g(float g, int prologue)
+{
+    if (prologue & kProG) return g_of(g, prologue);
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(g), "f"(kGLeast));
+    return y;
+}
+
 struct TreeSmem {
     uint64_t anc[kTreeMaxNodes];    // bit j of anc[i]: node j is node i or above it; 0 for an absent node
     int up[kTreeMaxNodes];

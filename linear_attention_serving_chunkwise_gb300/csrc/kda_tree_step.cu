@@ -9,7 +9,7 @@
 //     o_i = (e^{G_i} q_i)^T S + sum_{j on i's path} <e^{G_i - G_j} q_i, k_j> w_j
 // so the state S is read once for all nodes and nothing of the size of a state is kept per
 // node.  e^{G_i - G_j} is formed as one exponential of a difference <= 0, for ancestor pairs
-// only: no factor of it can overflow, however deep the tree.  The commit is then
+// only: no factor of it can overflow, however deep the tree, and a g of -inf is a reset (path_g).  The commit is then
 //     S <- Diag(e^{G_n}) S + sum_{j on the path} (e^{G_n - G_j} k_j) w_j^T.
 // Here: the step for dk = 64 on the CUDA cores (dk = 128: kda_tree_step_tc.cu), and the commit.
 // The step's bound: instruction issue and shared memory, 64 x 96 heads x 16 nodes 204 us, 1.05 TB/s;
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(2 * D) tree_decode_kernel(TreeDecodeArgs a)
         const size_t at = (((size_t)b * K + j) * H + h) * D + c;
         sk[idx] = to_f32(static_cast<const Tin*>(a.k)[at]);
         sq[idx] = to_f32(static_cast<const Tin*>(a.q)[at]);
-        sg[idx] = g_of(a.g[at], a.prologue);
+        sg[idx] = path_g(a.g[at], a.prologue);
     }
     __syncthreads();
     if (!ts.ok) {

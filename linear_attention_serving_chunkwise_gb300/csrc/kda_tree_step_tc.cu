@@ -183,8 +183,8 @@ __device__ __forceinline__ void prepare(const TreeDecodeArgs& a, const Plan& pl,
                     float4 x = before ? out[(63 - __clzll((long long)before)) * (D / 4) + c] : make_float4(0.f, 0.f, 0.f, 0.f);
                     for (uint32_t in = (uint32_t)(path >> i0) & 0xffffu; in; in &= in - 1) {
                         const float4 y = g4[(__ffs(in) - 1) * (D / 4) + c];
-                        x = make_float4(fmaf(g_of(y.x, pro), kLog2e, x.x), fmaf(g_of(y.y, pro), kLog2e, x.y),
-                                        fmaf(g_of(y.z, pro), kLog2e, x.z), fmaf(g_of(y.w, pro), kLog2e, x.w));
+                        x = make_float4(fmaf(path_g(y.x, pro), kLog2e, x.x), fmaf(path_g(y.y, pro), kLog2e, x.y),
+                                        fmaf(path_g(y.z, pro), kLog2e, x.z), fmaf(path_g(y.w, pro), kLog2e, x.w));
                     }
                     out[(i0 + i) * (D / 4) + c] = x;
                 }

@@ -8,6 +8,7 @@ import torch
 
 import _draft_ref as R
 import kda_workloads as W
+from _parity import check
 
 pytestmark = pytest.mark.gpu
 TYPES = [(torch.bfloat16, 128), (torch.bfloat16, 64), (torch.float32, 128), (torch.float32, 64)]
@@ -118,3 +119,44 @@ def test_absent_nodes_are_zero_whatever_their_rows_hold(cuda_lib, dtype, D, K):
     for what, got, want in zip(("out", "writes"), _step(cuda_lib, x, parents, s0, gate=z), clean):
         assert not got[gone].any(), what
         assert torch.equal(got, want), what
+
+
+def _with_resets(x, seed):
+    """g with whole nodes and single channels at what e^g = 0 may look like."""
+    r = np.random.default_rng(seed)
+    g = x["g"].clone()
+    low = torch.tensor([-np.inf, -np.finfo(np.float32).max, -200.0, -1e4], dtype=torch.float32)
+    put = torch.from_numpy(r.random(g.shape) < 0.08)
+    pick = low[torch.from_numpy(r.integers(0, 4, g.shape))]
+    g[put] = pick[put]
+    g[0, g.shape[1] // 2] = -np.inf
+    return {**x, "g": g}
+
+
+@pytest.mark.parametrize("kind,K", [("chain", 1), ("chain", 7), ("random", 16), ("binary", 33), ("chain", 33), ("ragged", 64)])
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_resets_of_the_state(cuda_lib, dtype, D, kind, K):
+    """g = -inf (or any g whose e^g is zero) forgets what lies before the node and nothing after it.
+
+    Bar: 1e-4 of the RMS, as without resets.  A reset counts as some 150 powers of two in G, so a pair's
+    factor has a rounding error of 2^-25 |G| ln 2 for each node between the two: 2e-5 for the
+    five resets (|G| < 1024) that a path of 33 nodes has in one channel, and the pairs that matter
+    (e^g of 1/12 a node on average) have one to three nodes between them."""
+    B, H = 2, 2
+    x, s0 = _inputs(B, K, H, D, dtype, seed=60 + K)
+    x, s0 = {n: x[n].cpu() for n in ORDER}, s0.cpu()
+    x = _with_resets(x, K)
+    parents = R.trees(kind, B, K, seed=K)
+    ref_o, ref_w, states = R.kda_tree(x, s0, parents)
+    out, writes = _step(cuda_lib, {n: x[n].cuda() for n in ORDER}, parents, s0.cuda())
+    check("out", out, ref_o, 1e-4)
+    check("writes", writes, ref_w, 1e-4)
+    ends = [max(states[b]) for b in range(B)]
+    path = np.full((B, K), -1, np.int32)
+    n = np.zeros(B, np.int32)
+    for b in range(B):
+        p = R.path_to(parents[b], ends[b])
+        path[b, :len(p)], n[b] = p, len(p)
+    state = s0.cuda()
+    cuda_lib.tree_commit(x["k"].cuda(), x["g"].cuda(), writes.cuda(), torch.from_numpy(path).cuda(), torch.from_numpy(n).cuda(), state)
+    check("state", state, np.stack([states[b][ends[b]] for b in range(B)]), 1e-4)
