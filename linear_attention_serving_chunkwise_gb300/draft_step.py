@@ -55,19 +55,20 @@ class HybridLayers:
         self.state = torch.zeros((batch, heads, dim, dim), dtype=torch.float32, device=device)
         self.cache = torch.empty((num_pages, 2, page_size, kv_heads, dim), dtype=dtype, device=device)
         self.context_lens, self.pages_held = i32(batch), i32(batch)
-        self.block_table = i32(batch, table_cols)
+        self.block_table = torch.full((batch, table_cols), -1, dtype=torch.int32, device=device)
         self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=device)
 
     def reserve(self, tokens: int) -> torch.Tensor:
-        """Slots [B, tokens] for that many tokens after every context."""
+        """Slots [B, tokens] for that many tokens after every context.  Where the free pages, or a sequence's
+        table row, do not reach for all: RuntimeError, and the sequences they reach for keep their pages."""
         B = self.context_lens.numel()
         new = torch.full_like(self.context_lens, tokens)
         slots, _, self.pages_held, taken = page_tables(self.context_lens, new, self.pages_held, self.block_table, self.free_pages,
                                                        page_size=self.cache.shape[2], max_tokens=B * tokens)
-        taken = int(taken)
-        if taken == 0 and bool((slots < 0).any()):
-            raise RuntimeError("out of cache pages")
+        taken, refused = torch.stack([taken[0], (slots < 0).any().int()]).tolist()      # (one trip to the device)
         self.free_pages = self.free_pages[taken:]
+        if refused:
+            raise RuntimeError("out of cache pages, or of columns of the block table")
         return slots.view(B, tokens)
 
     def attend(self, q, k, v, slots, parents) -> torch.Tensor:

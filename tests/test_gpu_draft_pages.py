@@ -1,0 +1,46 @@
+"""Pages at their limits: requests that do not fit beside requests that do, and lengths at the ends of 32 bits."""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_serving_chunkwise_gb300 import draft_step
+
+pytestmark = pytest.mark.gpu
+
+
+def _layers(num_pages, page_size, cols, context=(0, 0), held=(0, 0)):
+    mem = draft_step.HybridLayers(2, 2, 64, 1, num_pages, page_size, cols)
+    mem.context_lens[:] = torch.tensor(context)
+    taken = 0
+    for b, n in enumerate(held):
+        mem.block_table[b, :n] = mem.free_pages[taken:taken + n]
+        taken += n
+    mem.pages_held[:] = torch.tensor(held)
+    mem.free_pages = mem.free_pages[taken:]
+    return mem
+
+
+def test_reserve_refuses_when_pages_reach_for_one_sequence_only(cuda_lib):
+    mem = _layers(num_pages=3, page_size=4, cols=4)
+    with pytest.raises(RuntimeError):
+        mem.reserve(8)                                    # two pages each, three there
+    # what the first sequence took is its own; the second has nothing
+    assert mem.pages_held.tolist() == [2, 0] and mem.free_pages.tolist() == [2]
+    assert mem.block_table.tolist() == [[0, 1, -1, -1], [-1] * 4]
+    assert mem.reserve(4).tolist() == [[0, 1, 2, 3], [8, 9, 10, 11]]
+    assert mem.free_pages.numel() == 0 and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def test_reserve_refuses_when_one_table_row_is_full(cuda_lib):
+    mem = _layers(num_pages=9, page_size=4, cols=2, context=(0, 6), held=(0, 2))
+    with pytest.raises(RuntimeError):
+        mem.reserve(4)
+    assert mem.pages_held.tolist() == [1, 2] and mem.free_pages.tolist() == [3, 4, 5, 6, 7, 8]
+    assert mem.block_table.tolist() == [[2, -1], [0, 1]]
+
+
+def test_reserve_refuses_when_no_page_is_left(cuda_lib):
+    mem = _layers(num_pages=1, page_size=4, cols=4)
+    with pytest.raises(RuntimeError):
+        mem.reserve(5)
+    assert mem.pages_held.tolist() == [0, 0] and mem.free_pages.tolist() == [0]
