@@ -377,16 +377,26 @@ def state_combine(transition, state_in, state_add, out=None, *, stream=None, che
 # These calls take a few microseconds on the GPU, so the marshalling is kept lean: pointers go
 # to ctypes as plain integers and the stream comes as its raw handle (outputs are allocations of
 # their own: a view of a fresh tensor costs three times an allocation).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _stream_on(stream, device: int) -> int:
-    return _raw_stream(device) if stream is None else stream.cuda_stream
+    """Handle of the stream for tensors on ``device``, which has to be the GPU that the library will use: the current one."""
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if device != _current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_current_device()}")
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _expect(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
-    """Address of ``t``.  The C calls know pointers only: a wrong type, shape, device or layout is found here."""
+    """Address of ``t``.  The C calls know pointers only: a wrong type, shape, layout, or device other than
+    the others' is found here, a device that is not the current GPU by ``_stream_on``, before anything is launched."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -419,10 +429,11 @@ def page_tables(context_lens, new_lens, pages_held, block_table, free_pages, *, 
     had = _expect("pages_held", pages_held, _I32, (B,), at)
     table = _expect("block_table", block_table, _I32, (B, cols), at)
     free = _expect("free_pages", free_pages, _I32, (F,), at)
+    queue = _stream_on(stream, at)
     slots = _fresh((max_tokens,), torch.int64, dev, stream)
     cu, held, taken = _fresh((B + 1,), _I32, dev, stream), _fresh((B,), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
     st = load().kda_page_tables(B, cols, F, page_size, max_tokens, ctx, new, had, table, free, slots.data_ptr(),
-                                cu.data_ptr(), held.data_ptr(), taken.data_ptr(), _stream_on(stream, at))
+                                cu.data_ptr(), held.data_ptr(), taken.data_ptr(), queue)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_page_tables")
     return slots, cu, held, taken
@@ -474,6 +485,7 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents, out=
     table = _expect("block_table", block_table, _I32, (B, cols), at)
     ctx = _expect("context_lens", context_lens, _I32, (B,), at)
     par = _expect("parents", parents, _I32, (B, K), at)
+    queue = _stream_on(stream, at)
     desc = ctypes.byref(TreeAttentionDesc(B, K, H, Hk, D, code, P, ps, cols, D ** -0.5 if scale is None else scale, ks, vs))
     if out is None:
         out = _fresh((B, K, H, D), dt, dev, stream)
@@ -483,8 +495,10 @@ def tree_attention(q, k_cache, v_cache, block_table, context_lens, parents, out=
     lib = load()
     if workspace is None:
         workspace = _fresh((lib.kda_tree_attention_workspace_bytes(desc),), torch.uint8, dev, stream)
+    elif workspace.get_device() != at or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
     st = lib.kda_tree_attention(desc, qp, kp, vp, table, ctx, par, op, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_on(stream, at))
+                                workspace.numel() * workspace.element_size(), queue)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_tree_attention")
     return out
@@ -504,12 +518,13 @@ def tree_decode(q, k, v, g, beta, parents, state, out=None, writes=None, *, stre
            _expect("g", g, _F32, (B, K, H, dk), at), _expect("beta", beta, _F32, (B, K, H), at),
            _expect("parents", parents, _I32, (B, K), at), None if gate is None else _expect("gate", gate, _F32, wide, at),
            _expect("state", state, _F32, (B, H, dk, dv), at))
+    queue = _stream_on(stream, at)
     if out is None:
         out = _fresh(wide, _F32, dev, stream)
     if writes is None:
         writes = _fresh(wide, _F32, dev, stream)
     st = load().kda_tree_decode(B, K, H, dk, dv, code, prologue, *ins, _expect("out", out, _F32, wide, at),
-                                _expect("writes", writes, _F32, wide, at), _stream_on(stream, at))
+                                _expect("writes", writes, _F32, wide, at), queue)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_tree_decode")
     return out, writes
@@ -545,10 +560,11 @@ def verify_drafts(target_probs, tokens, parents, uniforms, noise, draft_probs=No
     uni = _expect("uniforms", uniforms, _F32, (B, K), at)
     noi = _expect("noise", noise, _F32, (B, V), at)
     dra = None if draft_probs is None else _expect("draft_probs", draft_probs, _F32, (B, K, V), at)
+    queue = _stream_on(stream, at)
     path = _fresh((B, K), _I32, dev, stream)
     n_accept, next_token = _fresh((B,), _I32, dev, stream), _fresh((B,), _I32, dev, stream)
     st = load().kda_verify_drafts(B, K, V, target, dra, tok, par, uni, noi, path.data_ptr(), n_accept.data_ptr(),
-                                  next_token.data_ptr(), _stream_on(stream, at))
+                                  next_token.data_ptr(), queue)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_verify_drafts")
     return path, n_accept, next_token
