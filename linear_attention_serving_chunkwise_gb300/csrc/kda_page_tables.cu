@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(PageTablesArgs a)
         const int p0 = page0[b];
         if (p0 < 0) continue;
         const int held = a.pages_held[b];
-        const int need = max(0, (int)(((long long)a.context_lens[b] + (tok0[b + 1] - tok0[b]) + a.page_size - 1) / a.page_size) - held);
+        // (its own new tokens: tok0's difference is not them where the sum has passed 32 bits)
+        const int need = max(0, (int)(((long long)a.context_lens[b] + a.new_lens[b] + a.page_size - 1) / a.page_size) - held);
         for (int j = lane; j < need; j += 32) a.block_table[(size_t)b * a.table_cols + held + j] = a.free_pages[p0 + j];
     }
 

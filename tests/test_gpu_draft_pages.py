@@ -44,3 +44,18 @@ def test_reserve_refuses_when_no_page_is_left(cuda_lib):
     with pytest.raises(RuntimeError):
         mem.reserve(5)
     assert mem.pages_held.tolist() == [0, 0] and mem.free_pages.tolist() == [0]
+
+
+def _tables(kda, ctx, new, held, table, free, ps, max_tokens):
+    c = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    t = c(table)
+    slots, cu, out, taken = kda.page_tables(c(ctx), c(new), c(held), t, c(free), page_size=ps, max_tokens=max_tokens)
+    return slots.tolist(), out.tolist(), int(taken), t.tolist()
+
+
+def test_tables_after_a_request_of_two_billion_tokens(cuda_lib):
+    """It exceeds its row and is refused; the pages of those behind it are written all the same."""
+    slots, held, taken, table = _tables(cuda_lib, [0, 3, 0], [2 ** 31 - 1, 5, 9], [0, 1, 0], [[-1] * 3, [7, -1, -1], [-1] * 3], [40, 41, 42, 43], 4, 6)
+    assert held == [0, 2, 3] and taken == 4
+    assert table == [[-1] * 3, [7, 40, -1], [41, 42, 43]]
+    assert slots == [-1] * 6 and cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
