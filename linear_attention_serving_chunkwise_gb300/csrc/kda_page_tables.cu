@@ -129,10 +129,11 @@ __global__ void __launch_bounds__(kThreads) page_tables_kernel(PageTablesArgs a)
             }
             const int b = lo, p0 = page0[b];
             if (p0 >= 0) {
-                const int pos = a.context_lens[b] + (int)(i - tok0[b]);
-                const int pg = pos / a.page_size, held = a.pages_held[b];
+                // (a position may pass 31 bits where the context is near them, but not 32; its page does not)
+                const uint32_t pos = (uint32_t)a.context_lens[b] + (uint32_t)(i - tok0[b]);
+                const int pg = (int)(pos / (uint32_t)a.page_size), held = a.pages_held[b];
                 const long long id = pg < held ? a.block_table[(size_t)b * a.table_cols + pg] : a.free_pages[p0 + pg - held];
-                slot = id * a.page_size + (pos - pg * a.page_size);
+                slot = id * a.page_size + (pos - (uint32_t)pg * (uint32_t)a.page_size);
             }
         }
         a.slot_map[i] = slot;

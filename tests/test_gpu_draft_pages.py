@@ -59,3 +59,16 @@ def test_tables_after_a_request_of_two_billion_tokens(cuda_lib):
     assert held == [0, 2, 3] and taken == 4
     assert table == [[-1] * 3, [7, 40, -1], [41, 42, 43]]
     assert slots == [-1] * 6 and cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
+
+
+def test_tables_of_positions_past_31_bits(cuda_lib):
+    """A context of 2^31 - 10 tokens and 20 more: the last held page, and a new one."""
+    ps, ctx, new = 4096, 2 ** 31 - 10, 20
+    held = -(-ctx // ps)
+    table = torch.full((1, held + 1), -1, dtype=torch.int32, device="cuda")
+    table[0, held - 1] = 77
+    c = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    slots, cu, out, taken = cuda_lib.page_tables(c(ctx), c(new), c(held), table, c(123), page_size=ps, max_tokens=new)
+    assert slots.tolist() == [77 * ps + ps - 10 + t for t in range(10)] + [123 * ps + t for t in range(10)]
+    assert out.tolist() == [held + 1] and int(taken) == 1 and int(table[0, held]) == 123
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
