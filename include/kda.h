@@ -470,8 +470,8 @@ size_t kda_tree_attention_workspace_bytes(const kda_tree_attention_desc* desc);
  *                 two calls in flight at once need two
  * Whatever lies in the cache where a node may not look (past the last node, pages of others,
  * nodes of other paths) does not change its output, NaN included.  A sequence whose
- * context_lens is negative, or exceeds its table row with the K nodes added, or whose tree is
- * bad, gets zeros; a token whose page id is outside [0, num_pages) is left out; both make
+ * context_lens is negative, or exceeds its table row or 2^31 - 8192 tokens with the K nodes added, or
+ * whose tree is bad, gets zeros; a token whose page id is outside [0, num_pages) is left out; both make
  * kda_last_device_status() return KDA_ERR_INVALID_ARG.  Tables with room for more than 2^31
  * tiles of work (64 tokens of one block of rows; terabytes of cache) return
  * KDA_ERR_UNSUPPORTED.  bf16: the softmax's weights are

@@ -47,11 +47,15 @@ __host__ __forceinline__ bool line_fits(const TreeAttnArgs& a, const Shape& sh)
     return tiles * row_blocks(a, sh.BM) * a.kv_heads * a.batch < 2147483647.0;
 }
 
+// Tokens that a sequence may have: positions are 32-bit, and the last tile's go past the end by less than this
+// leaves (a lane of the copies numbers up to 31 boxes of 128 tokens past the tile's first).
+constexpr int kMostTokens = 0x7fffffff - 8191;
+
 // tokens of sequence b, or 0 for a length that its table cannot hold (the sequence is skipped)
 __device__ __forceinline__ int seq_tokens(const TreeAttnArgs& a, int b, bool& ok)
 {
     const int c = __ldg(a.context_lens + b);
-    ok = c >= 0 && (long long)c + a.nodes <= (long long)a.table_cols * a.page_size;
+    ok = c >= 0 && c <= kMostTokens - a.nodes && (long long)c + a.nodes <= (long long)a.table_cols * a.page_size;
     return ok ? c + a.nodes : 0;
 }
 __device__ __forceinline__ int tiles_of(int n, int BN) { return n > 0 ? (n - 1) / BN + 1 : 1; }   // a skipped sequence still gets its zero rows

@@ -72,3 +72,22 @@ def test_tables_of_positions_past_31_bits(cuda_lib):
     assert slots.tolist() == [77 * ps + ps - 10 + t for t in range(10)] + [123 * ps + t for t in range(10)]
     assert out.tolist() == [held + 1] and int(taken) == 1 and int(table[0, held]) == 123
     assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("ps", [4096, 4100], ids=["boxes", "gathered"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_attention_of_lengths_at_the_end_of_31_bits(cuda_lib, dtype, ps):
+    """Table rows that could hold more than 2^31 tokens (all of them on one page): a sequence that has so many is
+    refused, the one beside it is not."""
+    K, D = 64, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(2, K, 1, D, generator=g, device="cuda").to(dtype)
+    kv = torch.randn(1, 2, ps, 1, D, generator=g, device="cuda").to(dtype)
+    table = torch.zeros((2, 2 ** 31 // ps + 2), dtype=torch.int32, device="cuda")
+    parents = torch.arange(-1, K - 1, dtype=torch.int32, device="cuda").expand(2, K).contiguous()
+    lens = lambda a, b: torch.tensor([a, b], dtype=torch.int32, device="cuda")
+    small = cuda_lib.tree_attention(q, kv[:, 0], kv[:, 1], table[:, :1].contiguous(), lens(100, 100), parents)
+    for long in (2 ** 31 - 1, 2 ** 31 - K, 2 ** 31 - 100, 2 ** 31 - 8191 - K):
+        out = cuda_lib.tree_attention(q, kv[:, 0], kv[:, 1], table, lens(100, long), parents)
+        assert cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
+        assert not out[1].any() and torch.equal(out[0], small[0])
