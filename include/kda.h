@@ -542,8 +542,11 @@ kda_status kda_tree_commit(int32_t batch, int32_t nodes, int32_t num_heads, int3
  *   path     [B, K] int32: kept nodes in order, then -1;  n_accept [B] int32;  next_token [B] int32
  * path and n_accept are kda_tree_commit's; for chains n_accept is kda_decode_multi's n_apply.
  * A bad tree, or a token outside [0, V): path -1, n_accept 0, next_token -1, and
- * kda_last_device_status() returns KDA_ERR_INVALID_ARG.
+ * kda_last_device_status() returns KDA_ERR_INVALID_ARG.  V above KDA_VERIFY_MAX_VOCAB returns
+ * KDA_ERR_UNSUPPORTED.
  */
+#define KDA_VERIFY_MAX_VOCAB (1 << 30)
+
 kda_status kda_verify_drafts(int32_t batch, int32_t nodes, int32_t vocab,
                              const float* target, const float* draft, const int32_t* tokens, const int32_t* parents,
                              const float* uniforms, const float* noise,

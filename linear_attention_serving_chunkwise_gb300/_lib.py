@@ -42,6 +42,7 @@ KDA_STATIC_SCRATCH_BYTES = 64 << 20
 KDA_TREE_MAX_NODES = 64
 KDA_TREE_PAD = -2          # parents entry of an absent node
 KDA_PAGE_TABLES_MAX_BATCH = 16384
+KDA_VERIFY_MAX_VOCAB = 1 << 30
 
 
 class KDAError(RuntimeError):

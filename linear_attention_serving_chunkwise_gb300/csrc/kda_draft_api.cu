@@ -187,6 +187,7 @@ kda_status kda_verify_drafts(int32_t batch, int32_t nodes, int32_t vocab, const 
                              int32_t* path, int32_t* n_accept, int32_t* next_token, void* stream)
 {
     if (batch < 0 || nodes < 1 || nodes > KDA_TREE_MAX_NODES || vocab < 1 || batch > (1 << 24)) return KDA_ERR_INVALID_ARG;
+    if (vocab > KDA_VERIFY_MAX_VOCAB) return KDA_ERR_UNSUPPORTED;
     if (batch == 0) return KDA_OK;
     if (!target || !tokens || !parents || !uniforms || !noise || !path || !n_accept || !next_token) return KDA_ERR_INVALID_ARG;
     const void* words[] = {target, draft, tokens, parents, uniforms, noise, path, n_accept, next_token};

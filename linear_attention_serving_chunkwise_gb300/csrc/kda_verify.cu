@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(VerifyArgs a)
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int b = blockIdx.x / C, t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int V = a.vocab;
+    const int V = a.vocab;                      // (at most KDA_VERIFY_MAX_VOCAB: a slice's end and a chunk past it stay in 31 bits)
     extern __shared__ __align__(16) unsigned char ring[];       // [stage][p, noise, q][kSlot]
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ Walk wk;

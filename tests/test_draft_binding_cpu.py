@@ -84,3 +84,11 @@ def test_a_workspace_with_gaps_is_refused(monkeypatch):
     monkeypatch.setattr(_lib, "_lib", _Never())
     with pytest.raises(ValueError, match="workspace"):
         _calls()["tree_attention"](workspace=_z(64, 2, dt=torch.uint8)[:, 0])
+
+
+@pytest.mark.parametrize("vocab,status", [(kda.KDA_VERIFY_MAX_VOCAB + 1, kda.KDA_ERR_UNSUPPORTED), (2 ** 31 - 1, kda.KDA_ERR_UNSUPPORTED),
+                                          (0, kda.KDA_ERR_INVALID_ARG)])
+def test_verify_refuses_a_vocabulary_past_its_indexes(lib, vocab, status):
+    """The ends of the vocabulary's slices are 32-bit; rows of 2^30 entries are 4 GB each."""
+    at = [None if i == 1 else (i + 1) << 40 for i in range(9)]           # no draft
+    assert kda.load().kda_verify_drafts(1, 1, vocab, *at, None) == status
