@@ -56,7 +56,7 @@ kda_status validate_attn(const kda_tree_attention_desc* d)
     }
     kda::TreeAttnArgs a = {};
     a.batch = d->batch; a.nodes = d->nodes; a.heads = d->num_heads; a.kv_heads = d->num_kv_heads;
-    a.page_size = d->page_size; a.table_cols = d->table_cols; a.bf16 = d->dtype == KDA_BF16;
+    a.page_size = d->page_size; a.table_cols = d->table_cols; a.dim = d->dim; a.bf16 = d->dtype == KDA_BF16;
     return kda::tree_attn_fits(a) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 

@@ -3,8 +3,8 @@
 // the sequence's context_lens[b] cached tokens and to the nodes on its own path, whose keys and
 // values lie in the cache at the logical positions context + j.  One pass over the tokens with the
 // running maximum and sum of the softmax; query heads of one group share each loaded tile.
-// Bound: for few rows latency (a tile's loads, scores, softmax and values follow one another, two
-// CTAs to an SM cover some of it), for many the CUDA cores' fp32 rate.  7 sequences of up to 3001
+// Bound: for few rows latency (a tile's loads, scores, softmax and values follow one another; where two
+// CTAs fit an SM they cover some of it), for many the CUDA cores' fp32 rate.  7 sequences of up to 3001
 // tokens, 5 nodes, 6 heads on 2 cache heads, D = 64: 28 us, 0.40 TB/s, join included; 16 with
 // 32 nodes: 75 us, 15 TFLOP/s.
 //
@@ -194,15 +194,19 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
     if (bad_page) report_status(a.status, kDevBadSeqlens);
 }
 
-constexpr int kSimtCtas = 304;        // two to an SM
-
 template <int D, int TM>
 constexpr size_t simt_smem() { return (size_t)(16 * TM * (D + 4) + 2 * kBN * (D + 4) + 16 * TM * (kBN + 4)) * 4; }
+
+// As many CTAs as run at once: two to an SM, one where two do not fit its 228 KB (D = 128, 64 rows: 117 KB
+// each; with 304 shares there, in two waves, 7 sequences of up to 3001 tokens, 16 nodes, 6 heads on 2
+// took 58 us instead of 43, 2 x 20000 tokens, 64 nodes, 8 heads on 2 433 instead of 414).
+template <int D, int TM>
+constexpr attn::Shape simt_shape() { return {16 * TM, kBN, 152 * (simt_smem<D, TM>() > 112 * 1024 ? 1 : 2), 1}; }
 
 template <int D, int TM>
 cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 {
-    const attn::Shape sh = {16 * TM, kBN, kSimtCtas, 1};
+    const attn::Shape sh = simt_shape<D, TM>();
     constexpr size_t smem = simt_smem<D, TM>();
     static KernelSetup setup;
     cudaError_t e = setup(tree_attn_simt_kernel<D, TM>, smem);
@@ -218,6 +222,12 @@ cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
 // four before the page ids were read together)
 bool small_rows(int nodes, int group) { return nodes * group <= 16; }
 
+attn::Shape simt_shape_of(int nodes, int group, int dim)
+{
+    if (dim == 128) return small_rows(nodes, group) ? simt_shape<128, 1>() : simt_shape<128, 4>();
+    return small_rows(nodes, group) ? simt_shape<64, 1>() : simt_shape<64, 4>();
+}
+
 cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
 {
     const bool small = small_rows(a.nodes, a.heads / a.kv_heads);
@@ -229,15 +239,13 @@ cudaError_t launch_simt_dim(const TreeAttnArgs& a, cudaStream_t stream)
 
 bool tree_attn_fits(const TreeAttnArgs& a)
 {
-    const int BM = small_rows(a.nodes, a.heads / a.kv_heads) ? 16 : 64;
-    return a.bf16 ? tree_attn_tc_fits(a) : attn::line_fits(a, {BM, kBN, kSimtCtas, 1});
+    return a.bf16 ? tree_attn_tc_fits(a) : attn::line_fits(a, simt_shape_of(a.nodes, a.heads / a.kv_heads, a.dim));
 }
 
 size_t tree_attn_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int dim, bool bf16)
 {
     if (bf16) return tree_attn_tc_workspace_bytes(nodes, heads / kv_heads, dim);
-    const int BM = small_rows(nodes, heads / kv_heads) ? 16 : 64;
-    return attn::workspace_bytes({BM, kBN, kSimtCtas, 1}, dim);
+    return attn::workspace_bytes(simt_shape_of(nodes, heads / kv_heads, dim), dim);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t stream)

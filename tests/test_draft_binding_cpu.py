@@ -92,3 +92,11 @@ def test_verify_refuses_a_vocabulary_past_its_indexes(lib, vocab, status):
     """The ends of the vocabulary's slices are 32-bit; rows of 2^30 entries are 4 GB each."""
     at = [None if i == 1 else (i + 1) << 40 for i in range(9)]           # no draft
     assert kda.load().kda_verify_drafts(1, 1, vocab, *at, None) == status
+
+
+@pytest.mark.parametrize("dim,nodes,rows,ctas", [(128, 16, 16, 304), (128, 17, 64, 152), (64, 16, 16, 304), (64, 17, 64, 304)])
+def test_fp32_attention_cuts_its_work_for_the_ctas_that_run_at_once(dim, nodes, rows, ctas):
+    """The workspace holds a record and two parts for each CTA: two to an SM, one where two do not fit its shared memory."""
+    page = 16 * 2 * dim
+    desc = kda.make_tree_attention_desc(2, nodes, 2, 2, dim, kda.KDA_F32, 10, 16, 5, 0.1, page, page)
+    assert kda.tree_attention_workspace_bytes(desc) == ctas * (16 + 2 * rows * (dim + 2) * 4)
