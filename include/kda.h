@@ -393,14 +393,16 @@ kda_status kda_state_combine(int32_t count, int32_t dk, int32_t dv,
  * ---- The draft step: operators around a tree of drafted tokens per sequence ----
  *
  * (llm-atlas K3_RESEARCH.md, Q28: draft tokens verified by the target; Q03 and Q31: KDA
- * layers beside attention layers with a paged cache.)  They share one description of the
+ * layers beside attention layers with a paged cache.  Those layers are MLA there; the attention
+ * here is that of key and value heads of one width, not of a latent cache.)  They share one description of the
  * trees, `parents` [B, K] int32, 1 <= K <= KDA_TREE_MAX_NODES:
  *   parents[b][i] = -1            node i follows the context
  *   0 <= parents[b][i] < i        node i follows that node
  *   parents[b][i] = KDA_TREE_PAD  there is no node i (trees of a batch may differ in size);
  *                                 no node may follow an absent one
  * A chain is parents[b][i] = i - 1.  A tree that breaks these rules is found on the device:
- * its sequence is skipped and kda_last_device_status() returns KDA_ERR_INVALID_ARG.
+ * its sequence is skipped and kda_last_device_status() returns KDA_ERR_INVALID_ARG (what then
+ * becomes of its outputs stands at each call).
  */
 #define KDA_TREE_MAX_NODES 64
 #define KDA_TREE_PAD (-2)
@@ -496,7 +498,8 @@ kda_status kda_tree_attention(const kda_tree_attention_desc* desc,
  *   writes  [B, K, H, dv] fp32, beta_i (v_i - S'_i^T k_i) with S'_i the decayed state of
  *           the parent: what kda_tree_commit needs;  zeros for absent nodes
  * prologue as kda_decode.  out and writes overlap nothing.  Depth is not limited below K.
- * g may be -inf (or so low that e^g is zero): the node then starts from an empty state.
+ * g may be -inf (or so low that e^g is zero): the node then starts from an empty state.  The rows of
+ * out and writes of a sequence whose tree is bad are not written: they hold what they held.
  */
 kda_status kda_tree_decode(int32_t batch, int32_t nodes, int32_t num_heads, int32_t dk, int32_t dv,
                            int32_t qkv_dtype, int32_t prologue,

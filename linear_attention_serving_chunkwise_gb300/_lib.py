@@ -510,7 +510,9 @@ def tree_decode(q, k, v, g, beta, parents, state, out=None, writes=None, *, stre
     """KDA for every node of draft trees through ``kda_tree_decode``: q, k [B,K,H,dk], v
     [B,K,H,dv] (fp32 or bf16); g [B,K,H,dk], beta [B,K,H] fp32; parents [B,K] int32; ``state``
     [B,H,dk,dv] fp32 is only read; ``prologue``: KDA_PROLOGUE_* bits; ``gate``: output gate logits
-    [B,K,H,dv] fp32.  Returns (out, writes), both [B,K,H,dv] fp32; ``tree_commit`` takes writes."""
+    [B,K,H,dv] fp32.  Returns (out, writes), both [B,K,H,dv] fp32; ``tree_commit`` takes writes.  A sequence
+    whose tree is bad (``last_device_status``) is skipped: its rows are not written, so in tensors allocated here
+    they are undefined."""
     B, K, H, dk = q.shape
     dv, dt, dev, at = v.shape[3], q.dtype, q.device, q.get_device()
     code = _dtype_code(q)

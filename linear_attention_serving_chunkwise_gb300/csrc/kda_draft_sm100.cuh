@@ -12,7 +12,7 @@ constexpr uint64_t kDraftWaitNs = 2000000000ull;
 // The roles of a kernel share its instruction cache, so what is in line at every wait counts:
 // with a clock read and the report there tree_decode took 234 us instead of 228 (64 x 96 heads x
 // 16 nodes), and with the first test inside the loop's block the attention took 272 us
-// instead of 267 (32 trees of 32 nodes).  It gives up after 2^20 suspensions of about a
+// instead of 267 (32 trees of 16 nodes).  It gives up after 2^20 suspensions of about a
 // microsecond.  A thread that gave up does not wait again: it goes through the rest of its
 // schedule at once (its other barriers, which count threads, still see it), so that no other
 // thread waits for it beyond its own bound; the owner calls finish() at the end, which reports it.

@@ -13,7 +13,8 @@
 // writes and one launch does all.  Bound: latency, of the launch and of four dependent reads (the
 // lengths, their scan, a page's id, the slot); the only stream is the slot map, 8 bytes a token.
 // 48 requests of 16 tokens: 5.9 us a call inside a graph; 32 prompts of up to 16384 tokens (264 K
-// slots, 2.1 MB): 10.7 us, 0.2 TB/s.  2048 tokens a CTA: 129 CTAs there, one wave.
+// slots, 2.1 MB): 10.7 us, 0.2 TB/s; 16384 requests of one token: 132 us, every CTA's scan and a warp to each
+// request's entries.  2048 tokens a CTA: 129 CTAs for the prompts, one wave.
 #include "kda_common.cuh"
 #include "kda_draft_launch.h"
 

@@ -22,7 +22,10 @@
 // 3000 cycles when 2700 of them were HBM's.  Join included, of a copy's 6.8 TB/s: 2 sequences
 // of 131072 tokens, 8 cache heads, 64 rows a head 171 us, 6.3 TB/s; 256 rows 208 us, 5.2 TB/s and
 // 1320 TFLOP/s; 32 trees of 16 nodes, 512 to 16384 tokens, 192 rows 223 us, 5.2 TB/s; one node over
-// 1500 tokens 18 us, latency (the first tile's way, the join).
+// 1500 tokens 18 us, latency (the first tile's way, the join); 128 sequences of 4096 to 32768 tokens, one node, 4 rows
+// a head 1396 us, 7.0 TB/s.  D = 64 (half the bytes and products, the same softmax): the 32 trees 181 us, 2 x 131072
+// tokens 170 us.  Times of a short loop in a CUDA graph: a long stream of calls runs at the clock of sustained
+// load, 230 us for 2 x 131072 and 244 for the 32 trees (1196 and 894 TFLOP/s).
 //
 // The cache rows come by TMA where the page size is a multiple of 8: a tile is a stack of boxes
 // of 8 to 128 rows (the largest power of two in the page size), and 8 rows are one swizzle

@@ -12,9 +12,9 @@
 // only: no factor of it can overflow, however deep the tree, and a g of -inf is a reset (path_g).  The commit is then
 //     S <- Diag(e^{G_n}) S + sum_{j on the path} (e^{G_n - G_j} k_j) w_j^T.
 // Here: the step for dk = 64 on the CUDA cores (dk = 128: kda_tree_step_tc.cu), and the commit.
-// The step's bound: instruction issue and shared memory, 64 x 96 heads x 16 nodes 204 us, 1.05 TB/s;
+// The step's bound: instruction issue and shared memory, 64 x 96 heads x 16 nodes 205 us, 1.04 TB/s;
 // at dk = 128 this form took 666 us where the tensor cores' takes 229.  The commit's: HBM, one read
-// and one write of the state; 256 x 96 heads, dk = 128: 464 us, 6.9 TB/s, the rate of a copy.  A CTA a
+// and one write of the state; 256 x 96 heads, dk = 128: 466 us, 6.9 TB/s, the rate of a copy (with the prologue 525).  A CTA a
 // state in registers has its 64 KB in flight at once, and the path's few vectors are folded
 // while the state arrives.
 #include "kda_draft_launch.h"

@@ -20,10 +20,11 @@
 //     17        issues the products (an elected thread at a time; one thread throughout was no faster)
 //     0 - 3, 20 - 23   substitution and outputs, a chain of short steps: the first four alone, or
 //               in turn with the others (groups_of)
-// Bound: the warps' instructions (about 11 K a block, half of the issue slots) and their supply, with
+// Bound: the warps' instructions (about 21 K a block of 16 nodes, half of the issue slots) and their supply, with
 // the roles' code side by side in one instruction cache; HBM's one read of the state would allow
-// two and a half times the speed.  64 x 96 heads: 1 node 121 us, 3.5 TB/s; 8 nodes 154 us; 16 nodes 229 us,
-// 2.7 TB/s; 96 units of 6 nodes 9 us.  Every wait is bounded (Waiter).
+// two and a half times the speed.  64 x 96 heads: 1 node 115 us, 3.6 TB/s; 8 nodes 149 us; 16 nodes 229 us,
+// 2.7 TB/s (fp32 rows 374 us; with the input prologue 314, with the output gate too 366); 96 units of 6 nodes
+// 9 us.  Every wait is bounded (Waiter).
 #include "kda_draft_launch.h"
 #include "kda_draft_sm100.cuh"
 #include "kda_tree.cuh"
@@ -62,7 +63,9 @@ struct Shared {
 
 // Units handled side by side by the preparation and by the substitution (trees of one block only).  One
 // group's code is fetched by more warps at the same time, two shorten the chain of steps that a
-// block is: 64 x 96 heads x 12 nodes take 189 us with one and 209 with two, x 16 nodes 240 and 229.
+// block is.  With one and with two, 64 x 96 heads: 12 nodes 186 and 205 us, 13 nodes 212 both, 14 nodes 221 and 216,
+// 16 nodes 237 and 227; 16 x 96 heads: 8 nodes 55 and 52, 16 nodes 78 and 68.  A CTA with one unit has nothing for the
+// second: 96 units of 13 nodes 11.1 and 12.0 us, of 16 nodes 12.8 and 14.3.
 __host__ __device__ constexpr int groups_of(int K) { return K > 12 && K <= NB ? 2 : 1; }
 
 __host__ __device__ constexpr Plan plan_of(int K, int esz, int tiles, int raws, int vals, int keys)
@@ -596,7 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    // (64 x 96 heads x 16 nodes: 235 us in runs of one unit, 229 of four; 16 x 96: 66 and 72)
+    // (In runs of one unit and of four, 16 nodes: 64 x 96 heads 230 and 223 us, 51 x 96 187 both, 32 x 96 121 and 130,
+    // 16 x 96 66 and 73; one node: 64 x 96 157 and 108, 16 x 96 41 and 35.  The rule goes by the deep trees.)
     const Units un(total, total >= 32 * (int)gridDim.x ? 4 : 1);
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSolveRegs));
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_decode_tc_kernel(TreeDecodeA
 }
 
 // Buffers for K nodes: as much in double (v, which waits for the last of the roles, in fourfold: 154 us
-// for 64 x 96 heads x 8 nodes, 208 with two of v and one unit's k) as leaves the states three
+// for 64 x 96 heads x 8 nodes when it was taken, 208 with two of v and one unit's k) as leaves the states three
 // quarters or more (48 KB in flight cover HBM's latency).
 constexpr Plan choose_plan(int K, int esz)
 {
