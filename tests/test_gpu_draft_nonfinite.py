@@ -1,4 +1,4 @@
-"""Infinities and NaN in the inputs of KDA on draft trees: what they reach, and nothing else.
+"""Infinities and NaN in the inputs of KDA on draft trees (and of the verification): what they reach, and nothing else.
 
 A NaN has more than one bit pattern: what the GPU's own arithmetic produces is 0x7fffffff, what
 torch writes is 0x7fc00000, and any payload may come from elsewhere."""
@@ -160,3 +160,26 @@ def test_resets_of_the_state(cuda_lib, dtype, D, kind, K):
     state = s0.cuda()
     cuda_lib.tree_commit(x["k"].cuda(), x["g"].cuda(), writes.cuda(), torch.from_numpy(path).cuda(), torch.from_numpy(n).cuda(), state)
     check("state", state, np.stack([states[b][ends[b]] for b in range(B)]), 1e-4)
+
+
+@pytest.mark.parametrize("V", [9, 1031, 20011])
+@pytest.mark.parametrize("draft", [False, True])
+def test_verify_of_probabilities_that_are_none(cuda_lib, draft, V):
+    """NaN beside the drafted tokens counts as zero; a whole row of NaN keeps nothing and still names a token."""
+    r = np.random.default_rng(V)
+    B, K = 6, 2
+    target = r.random((B, K + 1, V), dtype=np.float32)
+    target /= target.sum(-1, keepdims=True)
+    tokens = np.tile(np.array([[1, 2]], np.int32), (B, 1))
+    parents = np.tile(np.array([[-1, 0]], np.int32), (B, 1))
+    q = r.random((B, K, V), dtype=np.float32) if draft else None
+    u, noise = r.random((B, K), dtype=np.float32), r.random((B, V), dtype=np.float32) + np.float32(0.1)
+    none = r.random((B, K + 1, V)) < 0.3
+    none[:, :, 1:3] = False
+    c = lambda x: None if x is None else torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    run = lambda p: [x.tolist() for x in cuda_lib.verify_drafts(c(p), c(tokens), c(parents), c(u), c(noise), draft_probs=c(q))]
+    want = R.verify(np.where(none, np.float32(0), target), q, tokens, parents, u, noise)
+    assert run(np.where(none, np.float32("nan"), target)) == [x.tolist() for x in want]
+    path, n, nxt = run(np.full_like(target, np.float32("nan")))
+    assert n == [0] * B and path == [[-1] * K] * B and all(0 <= t < V for t in nxt)
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
