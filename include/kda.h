@@ -556,6 +556,191 @@ kda_status kda_verify_drafts(int32_t batch, int32_t nodes, int32_t vocab,
                              int32_t* path, int32_t* n_accept, int32_t* next_token, void* stream);
 
 /*
+ * ---- The attention layers' prompt path, and the upkeep of their cache ----
+ *
+ * (llm-atlas K3_RESEARCH.md, Q31 and section 8's serving engine: a paged cache whose prefixes are shared, copied on
+ * write and given back; blog-mushroom and agihunt: long prompts taken in chunks.)  A prompt's chunk goes through an
+ * attention layer as kda_page_tables (slots), kda_norm_rotate (queries ready, keys and values in the cache) and
+ * kda_chunk_attention; single tokens and drafts as the same two and kda_tree_attention.
+ */
+
+/* Most query heads that may share a cache head in kda_chunk_attention. */
+#define KDA_CHUNK_MAX_GROUP 64
+
+/* Shape of one kda_chunk_attention call. */
+typedef struct kda_chunk_attention_desc {
+    int32_t batch;          /* B >= 0 */
+    int32_t total_tokens;   /* T: rows of q and out */
+    int32_t num_heads;      /* query heads Hq, a multiple of num_kv_heads */
+    int32_t num_kv_heads;   /* cache heads Hk >= 1 */
+    int32_t dim;            /* channels per head: 64 or 128 */
+    int32_t dtype;          /* a kda_dtype, of q, the caches and out */
+    int32_t num_pages;      /* pages of the caches */
+    int32_t page_size;      /* tokens of a page >= 1 */
+    int32_t table_cols;     /* pages a sequence's table row can hold */
+    float scale;            /* factor of the scores, finite */
+    int64_t k_page_stride;  /* elements from one page to the next, >= page_size * Hk * dim, */
+    int64_t v_page_stride;  /*   a multiple of 16 bytes */
+} kda_chunk_attention_desc;
+
+/* Bytes of device scratch kda_chunk_attention needs for `desc`; 0 for one it would reject. */
+size_t kda_chunk_attention_workspace_bytes(const kda_chunk_attention_desc* desc);
+
+/*
+ * kda_chunk_attention -- softmax attention of chunks of new tokens over a paged key/value cache.  Sequence b's
+ * chunk is rows cu_seqlens[b] .. cu_seqlens[b + 1] of q; its token i stands at logical position context_lens[b] + i
+ * and attends to the positions up to its own, whose keys and values (the chunk's own among them) are in the cache.
+ * Chunks may differ in length; an empty one does nothing.
+ *
+ *   q             [T, Hq, dim] dtype
+ *   k_cache, v_cache, block_table, context_lens   as kda_tree_attention's
+ *   cu_seqlens    [B + 1] int32: 0 first, not decreasing, T at most (kda_page_tables' output)
+ *   out           [T, Hq, dim] dtype; rows from cu_seqlens[B] on are left as they are
+ *   workspace     kda_chunk_attention_workspace_bytes(desc) bytes, 16-byte aligned, clobbered;
+ *                 two calls in flight at once need two
+ * Whatever lies in the cache where a token may not look (behind it, pages of others) does not change its
+ * output, NaN included.  A sequence whose context_lens is negative, or with its chunk exceeds its table row or
+ * 2^31 - 8192 tokens, gets zeros; a token whose page id is outside [0, num_pages) is left out (a row that has nothing
+ * else becomes zero); bad cu_seqlens leave out as it was; all make kda_last_device_status() return
+ * KDA_ERR_INVALID_ARG.  bf16: the softmax's weights are rounded to bf16 before they meet the values (their sum is
+ * kept in fp32), fp32: fp32 throughout.
+ */
+kda_status kda_chunk_attention(const kda_chunk_attention_desc* desc,
+                               const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* context_lens, const int32_t* cu_seqlens,
+                               void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Flags of kda_norm_rotate_desc. */
+#define KDA_ROTATE_INTERLEAVED 1    /* pairs of channels (2i, 2i + 1) instead of (i, i + rot_dim / 2) */
+#define KDA_ROTATE_NO_NORM 2        /* rotation only */
+
+/* Shape of one kda_norm_rotate call. */
+typedef struct kda_norm_rotate_desc {
+    int32_t total_tokens;   /* T */
+    int32_t num_heads;      /* query heads Hq */
+    int32_t num_kv_heads;   /* cache heads Hk */
+    int32_t dim;            /* channels per head: 64 or 128 */
+    int32_t dtype;          /* a kda_dtype, of q, k, v, q_out and the caches */
+    int32_t rot_dim;        /* channels that are rotated, the first ones: a multiple of 16, 0 .. dim */
+    int32_t flags;          /* KDA_ROTATE_* */
+    int32_t num_pages;      /* pages of the caches */
+    int32_t page_size;      /* tokens of a page >= 1 */
+    float eps;              /* of the norms, >= 0 */
+    int64_t q_stride;       /* elements from one token to the next, >= its heads * dim, */
+    int64_t k_stride;       /*   a multiple of 16 bytes: q, k and v may be parts of one */
+    int64_t v_stride;       /*   projection's rows */
+    int64_t k_page_stride;  /* as kda_tree_attention's */
+    int64_t v_page_stride;
+} kda_norm_rotate_desc;
+
+/*
+ * kda_norm_rotate -- queries and keys normed per head and rotated by their positions, keys and values written into the
+ * cache, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight,   then for each pair (a, b) of rotated channels, with frequency f,
+ *     (y_a, y_b) <- (y_a cos(p f) - y_b sin(p f), y_a sin(p f) + y_b cos(p f)),   p the token's position
+ *
+ *   q [T, Hq, dim], k, v [T, Hk, dim] dtype, tokens at their strides
+ *   q_weight, k_weight  [dim] fp32, or NULL for ones
+ *   inv_freq      [rot_dim / 2] fp32, radians a token (may be NULL when rot_dim is 0)
+ *   positions     [T] int32 (may be NULL when rot_dim is 0)
+ *   slots         [T] int64: where the token's key and value go (kda_page_tables' slot_map); negative:
+ *                 nowhere.  No slot may come twice.
+ *   q_out         [T, Hq, dim] dtype
+ *   k_cache, v_cache  as kda_tree_attention's; only the slots' rows are written
+ * fp32 arithmetic, rounded once; angles are exact to 1e-8 of a turn for positions up to 2^24 whatever the frequency.
+ * q_out overlaps nothing, the caches no input.  A slot past the caches is left out and makes
+ * kda_last_device_status() return KDA_ERR_INVALID_ARG.
+ */
+kda_status kda_norm_rotate(const kda_norm_rotate_desc* desc, const void* q, const void* k, const void* v,
+                           const float* q_weight, const float* k_weight, const float* inv_freq,
+                           const int32_t* positions, const int64_t* slots,
+                           void* q_out, void* k_cache, void* v_cache, void* stream);
+
+/*
+ * kda_page_fork -- table rows that share another row's first tokens.  Fork i gives the empty row children[i] the
+ * first lens[i] tokens of row parents[i]: its whole pages by reference, and for a last page that they fill only partly a page of its
+ * own, into which kda_cache_copy copies the rows.  `shares` counts the rows that hold a page beyond the first, so that
+ * kda_page_release knows when it is free; pages of kda_page_tables start at 0.
+ *
+ *   parents, children, lens  [num_forks] int32; a parent may come many times, a child once
+ *   pages_held     [rows] int32; 0 for a child
+ *   block_table    [rows, table_cols] int32, in place: the children's first entries are written
+ *   shares         [num_pages] int32, in place
+ *   free_pages     [num_free] int32 page ids, taken from index 0 on in the order of the forks (may be NULL when 0)
+ *   pages_held_out [rows] int32: pages_held, and for the children what they hold now
+ *   copies         [num_forks, 3] int32: source page, target page and rows to copy; (-1, -1, 0) for none
+ *   pages_taken    [1] int32: free_pages entries used up
+ * A fork for which the free pages do not reach is refused: its child stays empty, its copy is none; no later one takes a page
+ * then.  A row out of range, a length that is negative or that the parent's pages do not cover, a child that
+ * holds pages, comes twice or is a parent in the same call: the fork does nothing.  A page id
+ * out of range is passed on without a share.  Both make kda_last_device_status() return KDA_ERR_INVALID_ARG.
+ * No output may overlap an input or another output.  num_forks <= rows <= KDA_PAGE_TABLES_MAX_BATCH.
+ */
+kda_status kda_page_fork(int32_t num_forks, int32_t rows, int32_t table_cols, int32_t num_pages, int32_t num_free, int32_t page_size,
+                         const int32_t* parents, const int32_t* children, const int32_t* lens, const int32_t* pages_held,
+                         int32_t* block_table, int32_t* shares, const int32_t* free_pages,
+                         int32_t* pages_held_out, int32_t* copies, int32_t* pages_taken, void* stream);
+
+/*
+ * kda_page_release -- table rows cut to their first keep_lens tokens (0: given up; at least what is held: untouched).
+ * The pages behind those are given back: each loses a share, and those that no row holds any more are returned.
+ *
+ *   keep_lens, pages_held  [rows] int32
+ *   block_table    [rows, table_cols] int32, only read: entries from pages_held_out on mean nothing afterwards
+ *   shares         [num_pages] int32 >= 0, in place
+ *   pages_held_out [rows] int32
+ *   freed          [num_pages] int32: the freed pages in ascending order, then -1;  num_freed [1] int32
+ * A row that would be cut inside a page which others hold as well is refused (what it appends there would be theirs:
+ * kda_page_fork gives a row a copy); a negative length or pages_held out of range leave the row as it is; an
+ * entry outside [0, num_pages) is passed over; a page given back more often than it is held is freed once.  All of
+ * these make kda_last_device_status() return KDA_ERR_INVALID_ARG.  No output may overlap an input or another output.
+ */
+kda_status kda_page_release(int32_t rows, int32_t table_cols, int32_t num_pages, int32_t page_size,
+                            const int32_t* keep_lens, const int32_t* pages_held, const int32_t* block_table,
+                            int32_t* shares, int32_t* pages_held_out, int32_t* freed, int32_t* num_freed, void* stream);
+
+/* The key/value caches of all layers that share their block tables.  Layer l, page p, offset s, head h begin at
+ * l * layer_stride + p * page_stride + (s * num_kv_heads + h) * dim elements. */
+typedef struct kda_cache_desc {
+    int32_t num_layers;     /* >= 0 */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_kv_heads;
+    int32_t dim;            /* any, with rows of num_kv_heads * dim elements a multiple of 16 bytes */
+    int32_t dtype;          /* a kda_dtype */
+    int64_t k_layer_stride; /* of layers and of pages: elements, at least a page, a multiple of 16 bytes; */
+    int64_t v_layer_stride; /*   not looked at where there is one layer, or one page */
+    int64_t k_page_stride;
+    int64_t v_page_stride;
+} kda_cache_desc;
+
+/*
+ * kda_cache_copy -- rows of pages copied in every layer: the first copies[i][2] rows of page copies[i][0] to page
+ * copies[i][1], keys and values.
+ *
+ *   copies  [num_copies, 3] int32, as kda_page_fork writes them; 0 rows: nothing
+ *   k_cache, v_cache  in place
+ * No target may come twice or be a source.  Pages out of range or more rows than a page has are
+ * left out and make kda_last_device_status() return KDA_ERR_INVALID_ARG.
+ */
+kda_status kda_cache_copy(const kda_cache_desc* desc, int32_t num_copies, const int32_t* copies,
+                          void* k_cache, void* v_cache, void* stream);
+
+/*
+ * kda_cache_keep_path -- the kept nodes' rows of a draft step moved to the front of the step's tokens, in every layer:
+ * what kda_tree_commit does for the states.  For e < n_accept[b] the row of slots[b][path[b][e]] goes to
+ * slots[b][e], as if all were read before any is written.
+ *
+ *   slots     [B, K] int64: where the step's nodes are in the cache; all different
+ *   path      [B, K] int32, ascending in its first n_accept[b] entries;  n_accept [B] int32, 0 .. K
+ *   k_cache, v_cache  in place
+ * A path that does not ascend within [0, K), a count out of range, or a slot that is to move from or to somewhere outside the caches leaves
+ * that sequence untouched and makes kda_last_device_status() return KDA_ERR_INVALID_ARG.
+ */
+kda_status kda_cache_keep_path(const kda_cache_desc* desc, int32_t batch, int32_t nodes, const int64_t* slots,
+                               const int32_t* path, const int32_t* n_accept, void* k_cache, void* v_cache, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word of the
  * current device: KDA_OK, KDA_ERR_INVALID_ARG (bad cu_seqlens seen on the
  * device) or KDA_ERR_TIMEOUT (a bounded wait gave up).  KDA_ERR_CUDA if the

@@ -36,13 +36,17 @@ EXPORTED = ("kda_abi_version", "kda_status_string", "kda_prefill_workspace_bytes
             "kda_prefill_host", "kda_prefill_host_static", "kda_decode", "kda_decode_gated", "kda_decode_multi",
             "kda_decode_multi_gated", "kda_state_combine", "kda_last_device_status", "kda_page_tables",
             "kda_tree_attention_workspace_bytes", "kda_tree_attention", "kda_tree_decode", "kda_tree_commit",
-            "kda_verify_drafts")
+            "kda_verify_drafts", "kda_chunk_attention_workspace_bytes", "kda_chunk_attention", "kda_norm_rotate",
+            "kda_page_fork", "kda_page_release", "kda_cache_copy", "kda_cache_keep_path")
 KDA_DECODE_MULTI_MAX_TOKENS = 64
 KDA_STATIC_SCRATCH_BYTES = 64 << 20
 KDA_TREE_MAX_NODES = 64
 KDA_TREE_PAD = -2          # parents entry of an absent node
 KDA_PAGE_TABLES_MAX_BATCH = 16384
 KDA_VERIFY_MAX_VOCAB = 1 << 30
+KDA_CHUNK_MAX_GROUP = 64
+KDA_ROTATE_INTERLEAVED = 1
+KDA_ROTATE_NO_NORM = 2
 
 
 class KDAError(RuntimeError):
@@ -61,6 +65,23 @@ class TreeAttentionDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("batch", "nodes", "num_heads", "num_kv_heads", "dim", "dtype", "num_pages",
                                               "page_size", "table_cols")] + \
                [("scale", ctypes.c_float), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64)]
+
+
+class ChunkAttentionDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "total_tokens", "num_heads", "num_kv_heads", "dim", "dtype", "num_pages",
+                                              "page_size", "table_cols")] + \
+               [("scale", ctypes.c_float), ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64)]
+
+
+class NormRotateDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("total_tokens", "num_heads", "num_kv_heads", "dim", "dtype", "rot_dim", "flags",
+                                              "num_pages", "page_size")] + [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "k_page_stride", "v_page_stride")]
+
+
+class CacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_layers", "num_pages", "page_size", "num_kv_heads", "dim", "dtype")] + \
+               [(n, ctypes.c_int64) for n in ("k_layer_stride", "v_layer_stride", "k_page_stride", "v_page_stride")]
 
 
 class PrefillPlan(ctypes.Structure):
@@ -128,6 +149,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_tree_commit.argtypes = [i32] * 7 + [vp] * 7
     lib.kda_verify_drafts.restype = ctypes.c_int
     lib.kda_verify_drafts.argtypes = [i32] * 3 + [vp] * 10
+    lib.kda_chunk_attention_workspace_bytes.restype = sz
+    lib.kda_chunk_attention_workspace_bytes.argtypes = [ctypes.POINTER(ChunkAttentionDesc)]
+    lib.kda_chunk_attention.restype = ctypes.c_int
+    lib.kda_chunk_attention.argtypes = [ctypes.POINTER(ChunkAttentionDesc)] + [vp] * 8 + [sz, vp]
+    lib.kda_norm_rotate.restype = ctypes.c_int
+    lib.kda_norm_rotate.argtypes = [ctypes.POINTER(NormRotateDesc)] + [vp] * 12
+    lib.kda_page_fork.restype = ctypes.c_int
+    lib.kda_page_fork.argtypes = [i32] * 6 + [vp] * 11
+    lib.kda_page_release.restype = ctypes.c_int
+    lib.kda_page_release.argtypes = [i32] * 4 + [vp] * 8
+    lib.kda_cache_copy.restype = ctypes.c_int
+    lib.kda_cache_copy.argtypes = [ctypes.POINTER(CacheDesc), i32] + [vp] * 4
+    lib.kda_cache_keep_path.restype = ctypes.c_int
+    lib.kda_cache_keep_path.argtypes = [ctypes.POINTER(CacheDesc), i32, i32] + [vp] * 6
     lib.kda_last_device_status.restype = ctypes.c_int
     lib.kda_last_device_status.argtypes = [vp]
     if path is None:
@@ -571,6 +606,202 @@ def verify_drafts(target_probs, tokens, parents, uniforms, noise, draft_probs=No
     if check and st != KDA_OK:
         raise KDAError(st, "kda_verify_drafts")
     return path, n_accept, next_token
+
+
+def make_chunk_attention_desc(batch, total_tokens, num_heads, num_kv_heads, dim, dtype, num_pages, page_size, table_cols, scale,
+                              k_page_stride, v_page_stride) -> ChunkAttentionDesc:
+    return ChunkAttentionDesc(batch, total_tokens, num_heads, num_kv_heads, dim, dtype, num_pages, page_size, table_cols, scale,
+                              k_page_stride, v_page_stride)
+
+
+def chunk_attention_workspace_bytes(desc: ChunkAttentionDesc) -> int:
+    return int(load().kda_chunk_attention_workspace_bytes(ctypes.byref(desc)))
+
+
+def chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out=None, *, scale: Optional[float] = None,
+                    workspace=None, stream=None, check=True):
+    """Attention of chunks of new tokens over a paged cache, through ``kda_chunk_attention``.
+
+    q [T,Hq,D] (fp32 or bf16), the chunks one after another; cu_seqlens [B+1] int32, as ``page_tables``
+    returns it; k_cache, v_cache, block_table and context_lens as for ``tree_attention``.  Token i of sequence b's
+    chunk stands at logical position context_lens[b] + i and sees the positions up to its own; the chunk's own keys and
+    values are in the cache already (``norm_rotate``).  ``scale`` defaults to 1 / sqrt(D); ``workspace``: uint8 scratch of
+    ``chunk_attention_workspace_bytes``, allocated if not given.  Returns out [T,Hq,D] of q's type; rows behind
+    the last chunk are not written, so in a tensor allocated here they are undefined."""
+    T, H, D = q.shape
+    P, ps, Hk, _ = k_cache.shape
+    dt, dev, at = q.dtype, q.device, q.get_device()
+    code = _dtype_code(q)
+    qp = _expect("q", q, dt, (T, H, D), at)
+    kp, ks = _cache("k_cache", k_cache, dt, (P, ps, Hk, D), at)
+    vp, vs = _cache("v_cache", v_cache, dt, (P, ps, Hk, D), at)
+    B, cols = block_table.shape
+    table = _expect("block_table", block_table, _I32, (B, cols), at)
+    ctx = _expect("context_lens", context_lens, _I32, (B,), at)
+    cu = _expect("cu_seqlens", cu_seqlens, _I32, (B + 1,), at)
+    queue = _stream_on(stream, at)
+    desc = ctypes.byref(ChunkAttentionDesc(B, T, H, Hk, D, code, P, ps, cols, D ** -0.5 if scale is None else scale, ks, vs))
+    if out is None:
+        out = _fresh((T, H, D), dt, dev, stream)
+        op = out.data_ptr()
+    else:
+        op = _expect("out", out, dt, (T, H, D), at)
+    lib = load()
+    if workspace is None:
+        workspace = _fresh((lib.kda_chunk_attention_workspace_bytes(desc),), torch.uint8, dev, stream)
+    elif workspace.get_device() != at or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
+    st = lib.kda_chunk_attention(desc, qp, kp, vp, table, ctx, cu, op, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), queue)
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_chunk_attention")
+    return out
+
+
+def _tokens(name: str, t: torch.Tensor, dtype, shape, device: int):
+    """(address, elements from token to token) of a tensor [T, heads, dim] whose tokens are contiguous each."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
+    T, h, d = shape
+    stride = t.stride()
+    if T > 0 and stride[1:] != (d, 1) and not t[0].is_contiguous():
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), stride[0] if T > 1 else h * d
+
+
+def norm_rotate(q, k, v, positions, inv_freq, slots, k_cache, v_cache, out=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                norm: bool = True, interleaved: bool = False, stream=None, check=True):
+    """Norms of queries and keys per head, their rotation by position, and keys and values into the cache, through
+    ``kda_norm_rotate``.
+
+    q [T,Hq,D], k, v [T,Hk,D] (fp32 or bf16; parts of one projection's rows are fine, the heads of a token being contiguous);
+    positions [T] int32; inv_freq [R/2] fp32, radians a token, for the first R channels (a multiple of 16; R = 0: no
+    rotation); slots [T] int64 as ``page_tables`` returns them (negative: not written); k_cache, v_cache as for
+    ``tree_attention``, written in place; q_weight, k_weight [D] fp32 or None for ones; ``norm=False``: rotation only;
+    ``interleaved``: pairs of neighbouring channels instead of (i, i + R/2).  Returns the queries [T,Hq,D]."""
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    P, ps = k_cache.shape[:2]
+    dt, dev, at = q.dtype, q.device, q.get_device()
+    code, R = _dtype_code(q), 2 * inv_freq.numel()
+    qp, qs = _tokens("q", q, dt, (T, H, D), at)
+    kp, kst = _tokens("k", k, dt, (T, Hk, D), at)
+    vp, vst = _tokens("v", v, dt, (T, Hk, D), at)
+    kc, kps = _cache("k_cache", k_cache, dt, (P, ps, Hk, D), at)
+    vc, vps = _cache("v_cache", v_cache, dt, (P, ps, Hk, D), at)
+    pos = _expect("positions", positions, _I32, (T,), at)
+    freq = _expect("inv_freq", inv_freq, _F32, (R // 2,), at)
+    slot = _expect("slots", slots, torch.int64, (T,), at)
+    wq = None if q_weight is None else _expect("q_weight", q_weight, _F32, (D,), at)
+    wk = None if k_weight is None else _expect("k_weight", k_weight, _F32, (D,), at)
+    queue = _stream_on(stream, at)
+    if out is None:
+        out = _fresh((T, H, D), dt, dev, stream)
+        op = out.data_ptr()
+    else:
+        op = _expect("out", out, dt, (T, H, D), at)
+    flags = (KDA_ROTATE_INTERLEAVED if interleaved else 0) | (0 if norm else KDA_ROTATE_NO_NORM)
+    desc = NormRotateDesc(T, H, Hk, D, code, R, flags, P, ps, eps, qs, kst, vst, kps, vps)
+    st = load().kda_norm_rotate(ctypes.byref(desc), qp, kp, vp, wq, wk, freq, pos, slot, op, kc, vc, queue)
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_norm_rotate")
+    return out
+
+
+def page_fork(parents, children, lens, pages_held, block_table, shares, free_pages, *, page_size: int, stream=None, check=True):
+    """Table rows that share another row's first tokens, through ``kda_page_fork``: parents, children, lens [n] int32
+    (fork i gives the empty row children[i] the first lens[i] tokens of row parents[i]); pages_held [R] int32;
+    block_table [R, cols] int32 and shares [num_pages] int32 (holders of a page beyond the first), both updated in place; free_pages
+    [F] int32, taken from index 0 on, one for every length that is no multiple of ``page_size``.  Returns (pages_held after
+    the call [R] int32, copies [n, 3] int32 for ``cache_copy``, pages_taken [1] int32)."""
+    dev, (R, cols) = block_table.device, block_table.shape
+    at, n, F, P = block_table.get_device(), parents.numel(), free_pages.numel(), shares.numel()
+    par = _expect("parents", parents, _I32, (n,), at)
+    chi = _expect("children", children, _I32, (n,), at)
+    length = _expect("lens", lens, _I32, (n,), at)
+    had = _expect("pages_held", pages_held, _I32, (R,), at)
+    table = _expect("block_table", block_table, _I32, (R, cols), at)
+    sha = _expect("shares", shares, _I32, (P,), at)
+    free = _expect("free_pages", free_pages, _I32, (F,), at)
+    queue = _stream_on(stream, at)
+    held, copies, taken = _fresh((R,), _I32, dev, stream), _fresh((n, 3), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
+    st = load().kda_page_fork(n, R, cols, P, F, page_size, par, chi, length, had, table, sha, free, held.data_ptr(), copies.data_ptr(),
+                              taken.data_ptr(), queue)
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_page_fork")
+    return held, copies, taken
+
+
+def page_release(keep_lens, pages_held, block_table, shares, *, page_size: int, stream=None, check=True):
+    """Table rows cut to their first keep_lens tokens (0: given up), through ``kda_page_release``: keep_lens, pages_held [R]
+    int32; block_table [R, cols] int32, only read; shares [num_pages] int32, updated in place.  Returns (pages_held after the
+    call [R] int32, freed [num_pages] int32: the pages that nobody holds any more in ascending order, then -1, num_freed
+    [1] int32)."""
+    dev, (R, cols) = block_table.device, block_table.shape
+    at, P = block_table.get_device(), shares.numel()
+    keep = _expect("keep_lens", keep_lens, _I32, (R,), at)
+    had = _expect("pages_held", pages_held, _I32, (R,), at)
+    table = _expect("block_table", block_table, _I32, (R, cols), at)
+    sha = _expect("shares", shares, _I32, (P,), at)
+    queue = _stream_on(stream, at)
+    held, freed, count = _fresh((R,), _I32, dev, stream), _fresh((P,), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
+    st = load().kda_page_release(R, cols, P, page_size, keep, had, table, sha, held.data_ptr(), freed.data_ptr(), count.data_ptr(), queue)
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_page_release")
+    return held, freed, count
+
+
+def _cache_layers(k_cache, v_cache, device: int):
+    """(descriptor, addresses) of the caches of all layers, [layers, pages, page_size, heads, dim], or of one, without the first."""
+    dt, shape = k_cache.dtype, k_cache.shape
+    code = _dtype_code(k_cache)
+    if len(shape) not in (4, 5):
+        raise ValueError("k_cache must be [pages, page_size, heads, dim], or that for each layer")
+    L, (P, ps, h, d) = (1 if len(shape) == 4 else shape[0]), shape[-4:]
+    at, strides = [], []
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dtype is not dt:
+            raise TypeError(f"{name} must be {dt}, got {c.dtype}")
+        if c.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(c.shape)}")
+        if c.get_device() != device:
+            raise ValueError(f"{name} is on {c.device}, not on the device of the other tensors")
+        stride = c.stride()
+        if stride[-3:] != (h * d, d, 1) and L > 0 and P > 0 and not (c[0, 0] if len(shape) == 5 else c[0]).is_contiguous():
+            raise ValueError(f"{name}: each page must be contiguous")
+        at.append(c.data_ptr())
+        strides.append((stride[0] if len(shape) == 5 else 0, stride[-4]))
+    return CacheDesc(L, P, ps, h, d, code, strides[0][0], strides[1][0], strides[0][1], strides[1][1]), at
+
+
+def cache_copy(copies, k_cache, v_cache, *, stream=None, check=True):
+    """Rows of pages copied in every layer, through ``kda_cache_copy``: copies [n, 3] int32 (source page, target page,
+    rows) as ``page_fork`` returns them; k_cache, v_cache [layers, pages, page_size, Hk, D] (or one layer's, without
+    the first) of fp32 or bf16, each page contiguous, in place."""
+    at, n = copies.get_device(), copies.shape[0]
+    pairs = _expect("copies", copies, _I32, (n, 3), at)
+    desc, (kp, vp) = _cache_layers(k_cache, v_cache, at)
+    st = load().kda_cache_copy(ctypes.byref(desc), n, pairs, kp, vp, _stream_on(stream, at))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_cache_copy")
+
+
+def cache_keep_path(slots, path, n_accept, k_cache, v_cache, *, stream=None, check=True):
+    """The kept nodes' rows of a draft step moved to the front of the step's tokens in every layer, through
+    ``kda_cache_keep_path``: slots [B,K] int64, where the nodes are in the cache; path [B,K] and n_accept [B] int32 as
+    ``verify_drafts`` returns them; k_cache, v_cache as for ``cache_copy``, in place."""
+    at, (B, K) = slots.get_device(), slots.shape
+    where = _expect("slots", slots, torch.int64, (B, K), at)
+    kept = _expect("path", path, _I32, (B, K), at)
+    count = _expect("n_accept", n_accept, _I32, (B,), at)
+    desc, (kp, vp) = _cache_layers(k_cache, v_cache, at)
+    st = load().kda_cache_keep_path(ctypes.byref(desc), B, K, where, kept, count, kp, vp, _stream_on(stream, at))
+    if check and st != KDA_OK:
+        raise KDAError(st, "kda_cache_keep_path")
 
 
 def last_device_status(stream=None) -> int:

@@ -1,0 +1,225 @@
+// Softmax attention of chunks of new tokens over a paged fp32 key/value cache, on the CUDA cores
+// (fp32 throughout).
+//
+// A thread has 8 query rows and BN / 16 tokens of a tile's scores, then 8 rows and D / 16 channels of
+// the output: 12 shared-memory reads to 128 multiply-adds.  One pass over the tiles with the running maximum
+// and sum of the softmax.  A tile's values are zeroed where no row of the unit may see the token (past its last one, a page
+// out of range); in the tiles that only some rows see whole, a weight of 0 is skipped: 0 times whatever lies there
+// must not be NaN.
+#include "kda_chunk_attn.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128, kBM = 64, kTM = 8;
+
+template <int D>
+struct Tile {
+    static constexpr int BN = D == 128 ? 32 : 64, CD = D / 16, TN = BN / 16, LD = D + 4, LP = BN + 4;
+    static constexpr size_t kSmem = (size_t)(kBM * LD + 2 * BN * LD + kBM * LP) * 4;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs a, attn::Shape sh)
+{
+    using L = Tile<D>;
+    constexpr int BN = L::BN, CD = L::CD, TN = L::TN, LD = L::LD, LP = L::LP;
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;                   // [kBM][LD]
+    float* sk = sq + kBM * LD;        // [BN][LD]
+    float* sv = sk + BN * LD;         // [BN][LD]
+    float* sp = sv + BN * LD;         // [kBM][LP]
+    __shared__ unsigned char s_on[BN];     // the tile's tokens that exist
+
+    const int t = threadIdx.x, lane = t & 31, ty = t >> 4, tx = t & 15;
+    const int G = a.heads / a.kv_heads;
+    const float sc = a.scale * 1.4426950408889634f;     // scores in powers of two
+
+    chunk::Line line;
+    const bool good = line.begin(a, sh, blockIdx.x, lane);
+    if (!good && blockIdx.x == 0 && t == 0) report_status(a.status, kDevBadSeqlens);
+    chunk::Piece pc;
+    chunk::Recorder rec(a, sh);
+    bool bad = false;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    while (line.next(a, sh, blockIdx.x, pc)) {
+        rec.see(line, pc);
+        const int rows = pc.tokens * G;
+        bad |= !pc.ok;
+        __syncthreads();              // the last unit's reads of shared memory are done
+        for (int i = t; i < kBM * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = 4 * (i % (D / 4));
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) x = load4(static_cast<const T*>(a.q) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D + c);
+            *reinterpret_cast<float4*>(sq + r * LD + c) = x;
+        }
+        float m[kTM], l[kTM], o[kTM][CD];
+        int seen[kTM];                // tokens that the row sees
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+            const int r = ty * kTM + i;
+            seen[i] = pc.ok && r < rows ? pc.ctx + pc.tok + r / G + 1 : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < CD; ++k) o[i][k] = 0.f;
+        }
+        for (int tile = pc.first; pc.ok && tile < pc.last; ++tile) {
+            const int t0 = tile * BN;
+            __syncthreads();
+            // a thread has four channels of every kStep-th token; the page ids are read together, then four rows at a time
+            constexpr int kStep = kThreads / (D / 4), kRows = BN / kStep;
+            const int j0 = t / (D / 4), c = 4 * (t % (D / 4));
+            int id[kRows];
+            size_t at[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int pos = t0 + j0 + i * kStep, pg = pos / a.page_size;
+                at[i] = ((size_t)(pos - pg * a.page_size) * a.kv_heads + pc.hk) * D + c;
+                id[i] = pos < pc.seen ? __ldg(a.block_table + (size_t)pc.b * a.table_cols + pg) : -1;
+            }
+#pragma unroll
+            for (int i0 = 0; i0 < kRows; i0 += 4) {
+                float4 k4[4], v4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = id[i0 + i];
+                    k4[i] = v4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p >= 0 && p < a.num_pages) {
+                        k4[i] = load4(static_cast<const T*>(a.k_cache) + (size_t)p * a.k_page_stride + at[i0 + i]);
+                        v4[i] = load4(static_cast<const T*>(a.v_cache) + (size_t)p * a.v_page_stride + at[i0 + i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + (i0 + i) * kStep, p = id[i0 + i];
+                    const bool on = p >= 0 && p < a.num_pages;
+                    bad |= !on && t0 + j < pc.seen;
+                    if (c == 0) s_on[j] = on;
+                    *reinterpret_cast<float4*>(sk + j * LD + c) = k4[i];
+                    *reinterpret_cast<float4*>(sv + j * LD + c) = v4[i];
+                }
+            }
+            __syncthreads();
+            float s[kTM][TN] = {};
+#pragma unroll 2
+            for (int ch = 0; ch < D; ch += 4) {
+                float4 k4[TN];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) k4[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + ch);
+#pragma unroll
+                for (int i = 0; i < kTM; ++i) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(sq + (ty * kTM + i) * LD + ch);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        s[i][j] = fmaf(q4.x, k4[j].x, fmaf(q4.y, k4[j].y, fmaf(q4.z, k4[j].z, fmaf(q4.w, k4[j].w, s[i][j]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kTM; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    s[i][j] = s_on[tx + 16 * j] && t0 + tx + 16 * j < seen[i] ? s[i][j] * sc : -INFINITY;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float nm = fmaxf(m[i], top), base = nm == -INFINITY ? 0.f : nm;
+                const float f = exp2f(m[i] - base);
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const float p = exp2f(s[i][j] - base);
+                    sum += p;
+                    sp[(ty * kTM + i) * LP + tx + 16 * j] = p;
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[i] = l[i] * f + sum;
+                m[i] = nm;
+#pragma unroll
+                for (int k = 0; k < CD; ++k) o[i][k] *= f;
+            }
+            __syncwarp();             // a row's weights are written and read by the same half warp
+            const bool partial = t0 + BN > pc.ctx + pc.tok + 1;      // (for the first row)
+            for (int j = 0; j < BN; j += 4) {
+                float4 p4[kTM];
+#pragma unroll
+                for (int i = 0; i < kTM; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty * kTM + i) * LP + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v[CD];
+#pragma unroll
+                    for (int k = 0; k < CD; k += 4) {
+                        const float4 v4 = *reinterpret_cast<const float4*>(sv + (j + e) * LD + tx * 4 + 16 * k);
+                        v[k] = v4.x; v[k + 1] = v4.y; v[k + 2] = v4.z; v[k + 3] = v4.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kTM; ++i) {
+                        const float p = e == 0 ? p4[i].x : e == 1 ? p4[i].y : e == 2 ? p4[i].z : p4[i].w;
+                        if (partial && p == 0.f) continue;
+#pragma unroll
+                        for (int k = 0; k < CD; ++k) o[i][k] = fmaf(p, v[k], o[i][k]);
+                    }
+                }
+            }
+        }
+        // the unit is done here, or its part goes to the workspace
+        float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+            const int r = ty * kTM + i;
+            if (r >= rows) continue;
+            if (pc.whole()) {
+                T* dst = static_cast<T*>(a.out) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D;
+                const float inv = 1.f / l[i];
+#pragma unroll
+                for (int k = 0; k < CD; ++k) {
+                    const float y = l[i] == 0.f ? 0.f : o[i][k] * inv;
+                    if constexpr (sizeof(T) == 2) dst[tx * 4 + 16 * (k & ~3) + (k & 3)] = __float2bfloat16_rn(y);
+                    else dst[tx * 4 + 16 * (k & ~3) + (k & 3)] = y;
+                }
+            } else {
+                if (tx == 0) { ws[r] = m[i]; ws[kBM + r] = l[i]; }
+#pragma unroll
+                for (int k = 0; k < CD; k += 4)
+                    attn::slot_out(ws, kBM)[(size_t)(tx + 4 * k) * kBM + r] = make_float4(o[i][k], o[i][k + 1], o[i][k + 2], o[i][k + 3]);
+            }
+        }
+    }
+    if (t == 0) rec.leave(a, blockIdx.x);
+    if (bad) report_status(a.status, kDevBadSeqlens);
+}
+
+template <int D>
+constexpr attn::Shape simt_shape() { return {kBM, Tile<D>::BN, 152 * (D == 128 ? 2 : 3), 1}; }
+
+template <typename T, int D>
+cudaError_t launch_simt(const ChunkAttnArgs& a, cudaStream_t stream)
+{
+    const attn::Shape sh = simt_shape<D>();
+    static KernelSetup setup;
+    cudaError_t e = setup(chunk_attn_simt_kernel<T, D>, Tile<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    chunk_attn_simt_kernel<T, D><<<sh.ctas, kThreads, Tile<D>::kSmem, stream>>>(a, sh);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return attn::launch_join<T, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, kBM, stream);
+}
+
+attn::Shape shape_of(const ChunkAttnArgs& a) { return a.dim == 128 ? simt_shape<128>() : simt_shape<64>(); }
+
+}  // namespace
+
+bool chunk_attn_fits(const ChunkAttnArgs& a) { return a.heads / a.kv_heads <= shape_of(a).BM && chunk::line_fits(a, shape_of(a)); }
+
+size_t chunk_attn_workspace_bytes(const ChunkAttnArgs& a) { return attn::workspace_bytes(shape_of(a), a.dim); }
+
+cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream)
+{
+    if (a.bf16) return a.dim == 128 ? launch_simt<__nv_bfloat16, 128>(a, stream) : launch_simt<__nv_bfloat16, 64>(a, stream);
+    return a.dim == 128 ? launch_simt<float, 128>(a, stream) : launch_simt<float, 64>(a, stream);
+}
+
+}  // namespace kda

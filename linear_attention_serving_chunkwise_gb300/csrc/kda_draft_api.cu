@@ -4,33 +4,12 @@
 #include <math.h>
 
 #include "../../include/kda.h"
+#include "kda_api_checks.h"
 #include "kda_draft_launch.h"
 
 namespace {
 
-struct Span {
-    uintptr_t lo, hi;   // [lo, hi); empty for a null pointer
-};
-Span span(const void* p, size_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return p ? Span{lo, lo + bytes} : Span{0, 0};
-}
-bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// the outputs (the first `n_out` spans) overlap neither one another nor an input
-template <int N>
-bool apart(const Span (&s)[N], int n_out)
-{
-    for (int i = 0; i < n_out; ++i)
-        for (int j = i + 1; j < N; ++j)
-            if (meet(s[i], s[j])) return false;
-    return true;
-}
-
-bool known_dtype(int32_t t) { return t == KDA_F32 || t == KDA_BF16; }
-kda_status of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+using namespace kda::checks;
 
 kda_status validate_tree_shape(int32_t batch, int32_t nodes, int32_t heads, int32_t dk, int32_t dv, int32_t dtype, int32_t prologue)
 {

@@ -1,0 +1,303 @@
+// Rows of a block table that share another row's first tokens, and rows cut short.
+//
+// shares[p] counts the rows that hold page p beyond the first, so a page that only page_tables
+// handed out needs no entry.  A fork of `len` tokens adds the parent's floor(len / page_size) whole pages
+// to the child by reference (shares + 1) and takes one page of its own for the rest, into which the
+// parent's rows are to be copied: no row ever appends to a page that another holds.  A release gives
+// back the entries from ceil(keep / page_size) on: shares - 1 each, and a page that nobody holds any more (its
+// entry has become -1) is free.
+#include <cooperative_groups.h>
+
+#include "kda_common.cuh"
+#include "kda_prompt_launch.h"
+
+namespace kda {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kMaxRows = 16384;        // KDA_PAGE_TABLES_MAX_BATCH
+constexpr int kBlock = 256;            // table columns that a warp takes at a time: eight reads in flight a lane
+
+// ------------------------------------------------------------------ forks
+// As in page_tables, every CTA works the forks out for itself (12 bytes each, from L2) and then does
+// its share of the table entries, so one launch does all.  Bound: latency, of the launch and of four dependent reads
+// (the fork, its parent's pages held, the parent's entry, the share).
+constexpr int kForkThreads = 256, kForkWarps = kForkThreads / 32;
+constexpr int kRefused = -2, kNoPage = -1;
+
+struct ForkSmem {
+    uint32_t child[kMaxRows / 32], twice[kMaxRows / 32];    // rows that are a child; of two forks or more
+    int warp_need[kForkWarps];
+    int taken;
+    int page[1];                       // [forks]: index in free_pages, kNoPage or kRefused
+};
+
+__global__ void __launch_bounds__(kForkThreads) page_fork_kernel(PageForkArgs a)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    ForkSmem& sm = *reinterpret_cast<ForkSmem*>(raw);
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, ps = a.page_size;
+    const bool first = blockIdx.x == 0;
+    const auto bit = [](const uint32_t* set, int i) { return set[i >> 5] >> (i & 31) & 1; };
+    const int words = (a.rows + 31) / 32;
+    for (int i = t; i < words; i += kForkThreads) sm.child[i] = sm.twice[i] = 0;
+    if (t == 0) sm.taken = 0;
+    __syncthreads();
+    for (int i = t; i < a.forks; i += kForkThreads) {
+        const int c = a.children[i];
+        if (c < 0 || c >= a.rows) continue;
+        const uint32_t m = 1u << (c & 31);
+        if (atomicOr(&sm.child[c >> 5], m) & m) atomicOr(&sm.twice[c >> 5], m);
+    }
+    __syncthreads();
+
+    int base = 0;                      // pages that the forks before this round need
+    bool bad = false;
+    for (int i0 = 0; i0 < a.forks; i0 += kForkThreads) {
+        const int i = i0 + t;
+        bool valid = false, need = false;
+        if (i < a.forks) {
+            const int p = a.parents[i], c = a.children[i], n = a.lens[i];
+            valid = p >= 0 && p < a.rows && c >= 0 && c < a.rows && n >= 0;
+            // a row that is forked in this call has no pages that could be forked from or written twice
+            valid = valid && !bit(sm.child, p) && !bit(sm.twice, c) && a.pages_held[c] == 0;
+            if (valid) {
+                const int held = a.pages_held[p];
+                valid = held >= 0 && held <= a.table_cols && (long long)held * ps >= n;
+            }
+            bad |= !valid;
+            need = valid && n % ps != 0;
+        }
+        const unsigned ballot = __ballot_sync(0xffffffffu, need);
+        if (lane == 0) sm.warp_need[w] = __popc(ballot);
+        __syncthreads();
+        int before = __popc(ballot & ((1u << lane) - 1u)), all = 0;
+#pragma unroll
+        for (int k = 0; k < kForkWarps; ++k) {
+            if (k < w) before += sm.warp_need[k];
+            all += sm.warp_need[k];
+        }
+        if (i < a.forks) {
+            const int at = base + before;
+            // first come, first served: past the last free page nobody takes any
+            const bool got = need && at < a.num_free;
+            sm.page[i] = !valid || (need && !got) ? kRefused : need ? at : kNoPage;
+            if (got) atomicMax(&sm.taken, at + 1);
+        }
+        base += all;
+        __syncthreads();               // before the next round writes the warps' counts
+    }
+    if (first) {
+        if (bad) report_status(a.status, kDevBadSeqlens);
+        if (t == 0) a.pages_taken[0] = sm.taken;
+        for (int r = t; r < a.rows; r += kForkThreads)
+            if (!bit(sm.child, r)) a.pages_held_out[r] = a.pages_held[r];
+        for (int i = t; i < a.forks; i += kForkThreads) {
+            const int page = sm.page[i], c = a.children[i], n = a.lens[i];
+            int src = -1, dst = -1, rows = 0;
+            if (page != kRefused) {
+                a.pages_held_out[c] = n / ps + (page >= 0);
+                if (page >= 0) {
+                    const int s = a.block_table[(size_t)a.parents[i] * a.table_cols + n / ps], d = a.free_pages[page];
+                    if (s >= 0 && s < a.num_pages && d >= 0 && d < a.num_pages) {
+                        src = s;
+                        dst = d;
+                        rows = n % ps;
+                    } else {
+                        report_status(a.status, kDevBadSeqlens);
+                    }
+                }
+            } else if (c >= 0 && c < a.rows) {
+                a.pages_held_out[c] = a.pages_held[c];      // (the same value from every fork of this child)
+            }
+            a.copies[3 * i] = src;
+            a.copies[3 * i + 1] = dst;
+            a.copies[3 * i + 2] = rows;
+        }
+    }
+
+    // the children's entries: a warp to kBlock columns of a fork
+    const int blocks = (a.table_cols + kBlock - 1) / kBlock;
+    const long long items = (long long)a.forks * blocks;
+    for (long long it = (long long)blockIdx.x * kForkWarps + w; it < items; it += (long long)gridDim.x * kForkWarps) {
+        const int i = (int)(it / blocks), page = sm.page[i];
+        if (page == kRefused) continue;
+        const int full = a.lens[i] / ps, j0 = (int)(it % blocks) * kBlock;
+        if (j0 > full) continue;
+        const int32_t* src = a.block_table + (size_t)a.parents[i] * a.table_cols;
+        int32_t* dst = a.block_table + (size_t)a.children[i] * a.table_cols;
+        int id[kBlock / 32];
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) {
+            const int j = j0 + 32 * k + lane;
+            id[k] = j < full ? src[j] : j == full && page >= 0 ? a.free_pages[page] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) {
+            const int j = j0 + 32 * k + lane;
+            if (j < full) {
+                dst[j] = id[k];
+                if (id[k] >= 0 && id[k] < a.num_pages) atomicAdd(a.shares + id[k], 1);
+                else report_status(a.status, kDevBadSeqlens);
+            } else if (j == full && page >= 0) {
+                dst[j] = id[k];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ releases
+// One cluster of CTAs in three steps with its barrier between them:
+//   1. what each row keeps (a row that would cut a page which others hold too is refused: appending to it would write
+//      into their tokens; decided before any share changes);
+//   2. shares - 1 for every entry given back;
+//   3. the pages whose entry is below zero, in ascending order: each warp counts those of its stretch of pages, the cluster
+//      exchanges the counts, each warp writes its own behind those of the warps before it.
+// Integer sums only, and no order of arrival shows in the outputs.
+constexpr int kCluster = 16, kReleaseThreads = 1024, kReleaseWarps = kReleaseThreads / 32;
+
+__global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageReleaseArgs a)
+{
+    __shared__ int warp_count[kReleaseWarps];
+    __shared__ int cta_count;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5, ps = a.page_size;
+    const int rank = (int)cluster.block_rank(), all_t = rank * kReleaseThreads + t, all_w = rank * kReleaseWarps + w;
+    bool bad = false;
+
+    for (int r = all_t; r < a.rows; r += kCluster * kReleaseThreads) {
+        const int keep = a.keep_lens[r], held = a.pages_held[r];
+        int left = held;
+        if (keep < 0 || held < 0 || held > a.table_cols) {
+            bad = true;
+        } else {
+            const int pages = (int)(((long long)keep + ps - 1) / ps);
+            if (pages < held) {
+                left = pages;
+                if (keep % ps) {
+                    const int id = a.block_table[(size_t)r * a.table_cols + pages - 1];
+                    if (id < 0 || id >= a.num_pages || a.shares[id] > 0) {
+                        bad = true;
+                        left = held;
+                    }
+                }
+            }
+        }
+        a.pages_held_out[r] = left;
+    }
+    cluster.sync();
+
+    // a warp to kBlock columns of a row; the rows' numbers are read by a lane each, 32 items at a time
+    const int blocks = (a.table_cols + kBlock - 1) / kBlock;
+    const long long items = (long long)a.rows * blocks;
+    for (long long i0 = (long long)all_w * 32; i0 < items; i0 += (long long)kCluster * kReleaseWarps * 32) {
+        const long long mine = i0 + lane;
+        int lo = 0, hi = 0;
+        if (mine < items) {
+            const int r = (int)(mine / blocks), j0 = (int)(mine % blocks) * kBlock;
+            const int held = a.pages_held[r];
+            lo = max(__ldcg(a.pages_held_out + r), j0);
+            hi = held <= a.table_cols ? min(held, j0 + kBlock) : 0;
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, lo < hi); left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const int from = __shfl_sync(0xffffffffu, lo, k), to = __shfl_sync(0xffffffffu, hi, k);
+            const int32_t* row = a.block_table + (size_t)((i0 + k) / blocks) * a.table_cols;
+            int id[kBlock / 32];
+#pragma unroll
+            for (int x = 0; x < kBlock / 32; ++x) {
+                const int j = from + 32 * x + lane;
+                id[x] = j < to ? row[j] : -1;
+            }
+#pragma unroll
+            for (int x = 0; x < kBlock / 32; ++x) {
+                if (id[x] >= 0 && id[x] < a.num_pages) atomicSub(a.shares + id[x], 1);
+                else bad |= from + 32 * x + lane < to;
+            }
+        }
+    }
+    cluster.sync();
+
+    // this warp's pages [p0, p1)
+    const long long warps = (long long)kCluster * kReleaseWarps;
+    const int each = (int)(((long long)a.num_pages + warps * 32 - 1) / (warps * 32)) * 32;
+    const int p0 = (int)min((long long)a.num_pages, (long long)all_w * each), p1 = (int)min((long long)a.num_pages, (long long)p0 + each);
+    int count = 0;
+#pragma unroll 4
+    for (int p = p0 + lane; p < p1; p += 32) count += __ldcg(a.shares + p) < 0;
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0) warp_count[w] = count;
+    __syncthreads();
+    if (w == 0) {
+        const int n = warp_count[lane];
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        warp_count[lane] = incl - n;
+        if (lane == 31) cta_count = incl;
+    }
+    cluster.sync();
+    int before = warp_count[w], total = 0;
+    for (int c = 0; c < kCluster; ++c) {
+        const int n = *cluster.map_shared_rank(&cta_count, c);
+        if (c < rank) before += n;
+        total += n;
+    }
+    for (int q = p0; q < p1; q += 32) {
+        const int p = q + lane, s = p < p1 ? __ldcg(a.shares + p) : 0;
+        const unsigned gone = __ballot_sync(0xffffffffu, s < 0);
+        if (s < 0) {
+            a.freed[before + __popc(gone & ((1u << lane) - 1u))] = p;
+            a.shares[p] = 0;
+            bad |= s < -1;             // given back more often than it was held
+        }
+        before += __popc(gone);
+    }
+    for (int i = total + all_t; i < a.num_pages; i += kCluster * kReleaseThreads) a.freed[i] = -1;
+    if (all_t == 0) a.num_freed[0] = total;
+    if (bad) report_status(a.status, kDevBadSeqlens);
+    cluster.sync();                    // no CTA ends while another reads its count
+}
+
+}  // namespace
+
+cudaError_t launch_page_fork(const PageForkArgs& a, cudaStream_t stream)
+{
+    static_assert(sizeof(ForkSmem) + kMaxRows * 4 <= 227 * 1024, "the forks fit shared memory");
+    static KernelSetup setup;
+    const cudaError_t e = setup(page_fork_kernel, sizeof(ForkSmem) + kMaxRows * sizeof(int));
+    if (e != cudaSuccess) return e;
+    const long long items = (long long)a.forks * ((a.table_cols + kBlock - 1) / kBlock), ctas = (items + kForkWarps - 1) / kForkWarps;
+    const int grid = (int)(ctas < 1 ? 1 : ctas > 152 ? 152 : ctas);
+    page_fork_kernel<<<grid, kForkThreads, sizeof(ForkSmem) + (size_t)a.forks * sizeof(int), stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_page_release(const PageReleaseArgs& a, cudaStream_t stream)
+{
+    static unsigned long long done = 0;     // a bit per device: more CTAs to a cluster than the portable eight are allowed
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_RELAXED) >> dev & 1)) {
+        if ((e = cudaFuncSetAttribute(page_release_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+        if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kReleaseThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, page_release_kernel, a);
+}
+
+}  // namespace kda

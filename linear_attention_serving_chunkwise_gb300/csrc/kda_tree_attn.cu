@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
     attn::Line line;
     line.begin(a, sh, blockIdx.x, lane);
     attn::Piece pc;
-    attn::Recorder rec;
+    attn::Recorder rec(a, sh);
     int masks_of = -1;
     bool bad_page = false;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(TreeAttnArgs a
             }
         }
         // the unit is done here, or its part goes to the workspace
-        float* ws = attn::slot_of(a, sh, D, pc.slot);
+        float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = ty * TM + i, row = r0 + r;
@@ -213,7 +213,7 @@ cudaError_t launch_simt(const TreeAttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     tree_attn_simt_kernel<D, TM><<<sh.ctas, kThreads, smem, stream>>>(a, sh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return attn::launch_join<float, D>(a, sh, stream);
+    return attn::launch_join<float, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, a.nodes * (a.heads / a.kv_heads), stream);
 }
 
 // rows of a unit: 16 while the whole (sequence, head) fits them (the other rows of a larger

@@ -358,7 +358,7 @@ __device__ __forceinline__ void query(const TreeAttnArgs& a, const attn::Shape& 
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
     Waiter wait{a.status};
     attn::Piece pc;
-    attn::Recorder rec;
+    attn::Recorder rec(a, sh);
     for (uint32_t piece = 0; line.next(a, sh, blockIdx.x, pc); ++piece) {
         rec.see(line, pc);
         int r = t / CH, node = (pc.r0 + r) / G, head = pc.r0 + r - node * G;
@@ -683,7 +683,7 @@ __device__ __forceinline__ void softmax(const TreeAttnArgs& a, const attn::Shape
             l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
         }
         const float norm = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        float* ws = attn::slot_of(a, sh, D, pc.slot);
+        float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
         const int rl = row - pc.r0;                 // row of the unit
         if (row < R && !pc.whole() && c0 == 0) {
             ws[rl] = m == -INFINITY ? m : m * sc;
@@ -876,7 +876,7 @@ cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     kernel<<<sh.ctas, kThreads, L::kBytes, stream>>>(a, sh, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return attn::launch_join<__nv_bfloat16, D>(a, sh, stream);
+    return attn::launch_join<__nv_bfloat16, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, a.nodes * (a.heads / a.kv_heads), stream);
 }
 
 template <int D>
