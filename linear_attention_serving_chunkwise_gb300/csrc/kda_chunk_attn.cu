@@ -19,8 +19,8 @@ struct Tile {
     static constexpr size_t kSmem = (size_t)(kBM * LD + 2 * BN * LD + kBM * LP) * 4;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs a, attn::Shape sh)
+template <int D>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_kernel(ChunkAttnArgs a, attn::Shape sh)
 {
     using L = Tile<D>;
     constexpr int BN = L::BN, CD = L::CD, TN = L::TN, LD = L::LD, LP = L::LP;
@@ -36,22 +36,22 @@ __global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs
     const float sc = a.scale * 1.4426950408889634f;     // scores in powers of two
 
     chunk::Line line;
-    const bool good = line.begin(a, sh, blockIdx.x, lane);
+    const bool good = line.begin(a, sh, sh.ctas, blockIdx.x, lane);
     if (!good && blockIdx.x == 0 && t == 0) report_status(a.status, kDevBadSeqlens);
     chunk::Piece pc;
-    chunk::Recorder rec(a, sh);
+    if (t == 0) chunk::clear_records(a, sh, sh.ctas, blockIdx.x);
     bool bad = false;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    while (line.next(a, sh, blockIdx.x, pc)) {
-        rec.see(line, pc);
+    while (line.next(a, sh, pc)) {
+        if (t == 0) chunk::record(a, sh, line, pc);
         const int rows = pc.tokens * G;
         bad |= !pc.ok;
         __syncthreads();              // the last unit's reads of shared memory are done
         for (int i = t; i < kBM * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) x = load4(static_cast<const T*>(a.q) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D + c);
+            if (r < rows) x = load4(static_cast<const float*>(a.q) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D + c);
             *reinterpret_cast<float4*>(sq + r * LD + c) = x;
         }
         float m[kTM], l[kTM], o[kTM][CD];
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs
                     const int p = id[i0 + i];
                     k4[i] = v4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (p >= 0 && p < a.num_pages) {
-                        k4[i] = load4(static_cast<const T*>(a.k_cache) + (size_t)p * a.k_page_stride + at[i0 + i]);
-                        v4[i] = load4(static_cast<const T*>(a.v_cache) + (size_t)p * a.v_page_stride + at[i0 + i]);
+                        k4[i] = load4(static_cast<const float*>(a.k_cache) + (size_t)p * a.k_page_stride + at[i0 + i]);
+                        v4[i] = load4(static_cast<const float*>(a.v_cache) + (size_t)p * a.v_page_stride + at[i0 + i]);
                     }
                 }
 #pragma unroll
@@ -173,13 +173,12 @@ __global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs
             const int r = ty * kTM + i;
             if (r >= rows) continue;
             if (pc.whole()) {
-                T* dst = static_cast<T*>(a.out) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D;
+                float* dst = static_cast<float*>(a.out) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D;
                 const float inv = 1.f / l[i];
 #pragma unroll
-                for (int k = 0; k < CD; ++k) {
-                    const float y = l[i] == 0.f ? 0.f : o[i][k] * inv;
-                    if constexpr (sizeof(T) == 2) dst[tx * 4 + 16 * (k & ~3) + (k & 3)] = __float2bfloat16_rn(y);
-                    else dst[tx * 4 + 16 * (k & ~3) + (k & 3)] = y;
+                for (int k = 0; k < CD; k += 4) {
+                    const float4 y = make_float4(o[i][k] * inv, o[i][k + 1] * inv, o[i][k + 2] * inv, o[i][k + 3] * inv);
+                    *reinterpret_cast<float4*>(dst + tx * 4 + 16 * k) = l[i] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : y;
                 }
             } else {
                 if (tx == 0) { ws[r] = m[i]; ws[kBM + r] = l[i]; }
@@ -189,37 +188,39 @@ __global__ void __launch_bounds__(kThreads) chunk_attn_simt_kernel(ChunkAttnArgs
             }
         }
     }
-    if (t == 0) rec.leave(a, blockIdx.x);
     if (bad) report_status(a.status, kDevBadSeqlens);
 }
 
 template <int D>
 constexpr attn::Shape simt_shape() { return {kBM, Tile<D>::BN, 152 * (D == 128 ? 2 : 3), 1}; }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt(const ChunkAttnArgs& a, cudaStream_t stream)
 {
     const attn::Shape sh = simt_shape<D>();
     static KernelSetup setup;
-    cudaError_t e = setup(chunk_attn_simt_kernel<T, D>, Tile<D>::kSmem);
+    cudaError_t e = setup(chunk_attn_simt_kernel<D>, Tile<D>::kSmem);
     if (e != cudaSuccess) return e;
-    chunk_attn_simt_kernel<T, D><<<sh.ctas, kThreads, Tile<D>::kSmem, stream>>>(a, sh);
+    chunk_attn_simt_kernel<D><<<sh.ctas, kThreads, Tile<D>::kSmem, stream>>>(a, sh);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return attn::launch_join<T, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, kBM, stream);
+    return attn::launch_join<float, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, kBM, stream);
 }
 
 attn::Shape shape_of(const ChunkAttnArgs& a) { return a.dim == 128 ? simt_shape<128>() : simt_shape<64>(); }
 
 }  // namespace
 
-bool chunk_attn_fits(const ChunkAttnArgs& a) { return a.heads / a.kv_heads <= shape_of(a).BM && chunk::line_fits(a, shape_of(a)); }
+bool chunk_attn_fits(const ChunkAttnArgs& a) { return a.bf16 ? chunk_attn_tc_fits(a) : chunk::line_fits(a, shape_of(a)); }
 
-size_t chunk_attn_workspace_bytes(const ChunkAttnArgs& a) { return attn::workspace_bytes(shape_of(a), a.dim); }
+size_t chunk_attn_workspace_bytes(const ChunkAttnArgs& a)
+{
+    return a.bf16 ? chunk_attn_tc_workspace_bytes(a) : attn::workspace_bytes(shape_of(a), a.dim);
+}
 
 cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream)
 {
-    if (a.bf16) return a.dim == 128 ? launch_simt<__nv_bfloat16, 128>(a, stream) : launch_simt<__nv_bfloat16, 64>(a, stream);
-    return a.dim == 128 ? launch_simt<float, 128>(a, stream) : launch_simt<float, 64>(a, stream);
+    if (a.bf16) return launch_chunk_attn_tc(a, stream);
+    return a.dim == 128 ? launch_simt<128>(a, stream) : launch_simt<64>(a, stream);
 }
 
 }  // namespace kda

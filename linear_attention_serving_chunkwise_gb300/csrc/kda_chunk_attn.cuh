@@ -3,14 +3,18 @@
 // A unit is one (sequence, key/value head, block of the chunk's tokens): its query rows are
 // (token, head of the group), as many whole tokens as a block of rows holds.  It reads the context and the chunk
 // up to its own last token, in tiles.  All units form one line (sequence-major, then head, then block),
-// in which a unit has a place for every token that it reads and `head` tiles' worth for its fixed cost; CTA c of N takes
-// the places [start(c), start(c + 1)), start(c) = floor(T c / N), and works the tiles whose first token lies
-// there.  So every CTA gets the same share whatever the mix of chunks and contexts, and a causal block counts
-// what it reads.  Places before a block are a quadratic in its number, so a CTA finds its start with a scan over the
+// in which a unit has a place for every token that it reads and `head` tiles' worth for its fixed cost; range r of N
+// is the places [start(r), start(r + 1)), start(r) = floor(T r / N), and its work the tiles whose first token lies
+// there.  So every range is the same share whatever the mix of chunks and contexts, and a causal block counts
+// what it reads.  Places before a block are a quadratic in its number, so a range's start is found with a scan over the
 // sequences and a bisection; lengths are read on the device.
 //
-// Units that several CTAs share are joined as those of the tree attention are (kda_attn_join.cuh): a CTA leaves its part of
-// a unit that began before its range in slot 2 c, of one that goes on past it in slot 2 c + 1.
+// CTA c of C works the ranges c, c + C, c + 2 C ... in turn, as many waves of them as keep what
+// all CTAs read at a time within L2 (kResident): the blocks of a chunk read the same keys and values, and in a single
+// wave the CTAs would be spread over the whole line, each behind another's reads by more than L2 holds.
+//
+// Units that several ranges share are joined as those of the tree attention are (kda_attn_join.cuh): a range leaves its part of
+// a unit that began before it in slot 2 r, of one that goes on past it in slot 2 r + 1.
 #pragma once
 
 #include "kda_attn_join.cuh"
@@ -24,6 +28,10 @@ using attn::Shape;
 
 // Tokens that a sequence may have: positions are 32-bit, and the copies number a little past the last tile.
 constexpr int kMostTokens = 0x7fffffff - 8191;
+constexpr int kMaxWaves = 8;
+// Bytes of keys and values that the CTAs may be at work on together, and the least tiles to a range of several waves.
+constexpr double kResident = 48e6;
+constexpr int kLeastTiles = 24;
 
 // One sequence of the call: its chunk and context, and the line's numbers for one of its (sequence, head)s.
 struct Seq {
@@ -52,7 +60,7 @@ struct Seq {
     __device__ __forceinline__ long long per_head(long long head) const { return blocks ? before(blocks - 1, head) + head + last : 0; }
 };
 
-// A CTA's part of one unit: tiles [first, last) of `tiles`.
+// A range's part of one unit: tiles [first, last) of `tiles`.
 struct Piece {
     int b, hk;
     int tok, tokens;        // first token of the block within the chunk, and how many
@@ -60,8 +68,8 @@ struct Piece {
     int ctx, n;             // of the sequence
     bool ok;
     int first, last, tiles;
-    int slot;               // workspace slot of the part, when it is not the whole unit
-    int seen;               // tokens that the block's last one sees, itself included
+    int range, slot;        // the range, and the workspace slot of the part when it is not the whole unit
+    int seen, common;       // tokens that the block's last one sees, itself included, and those that all see
     long long at;           // the line's place of the unit's first token
     __device__ __forceinline__ bool begins() const { return first == 0; }
     __device__ __forceinline__ bool ends() const { return last == tiles; }
@@ -69,9 +77,9 @@ struct Piece {
 };
 
 struct Line {
-    long long T, lo, hi, us;    // places in all, of this CTA; the current unit's first place
+    long long T, lo, hi, us;    // places in all, of this range; the current unit's first place
     long long head;
-    int N, TB, b, hk, j;
+    int N, range, TB, b, hk, j;
     Seq s;
 
     __device__ __forceinline__ long long start(int c) const
@@ -79,34 +87,41 @@ struct Line {
         const long long q = T / N, r = T - q * N;
         return q * c + r * c / N;
     }
-    // the CTA with place x
+    // the range with place x
     __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * N - 1) / T); }
 
-    // a full warp; false: the sequences' ends are no sums of lengths, and nothing may be done
-    __device__ __forceinline__ bool begin(const ChunkAttnArgs& a, const Shape& sh, int cta, int lane)
+    // A full warp, for one of sh.ctas ranges that `ctas` CTAs take; false: the sequences' ends are no sums of lengths, and nothing may be done.
+    __device__ __forceinline__ bool begin(const ChunkAttnArgs& a, const Shape& sh, int ctas, int range_, int lane)
     {
         head = (long long)sh.head * sh.BN;
         TB = sh.BM / (a.heads / a.kv_heads);
-        long long sum = 0;
+        range = range_;
+        long long sum = 0, again = 0;           // (again: tokens that several blocks read)
         bool good = true;
         for (int i = lane; i < a.batch; i += 32) {
             Seq x;
             x.read(a, i, TB);
             good = good && x.n >= 0 && (i > 0 || x.tok0 == 0) && (i < a.batch - 1 || (long long)x.tok0 + x.n <= a.tokens);
             sum += x.per_head(head);
+            again += x.blocks > 1 ? x.last : 0;
         }
-        lo = hi = us = 0;              // (nothing for a CTA that returns early: `next` ends at once)
+        lo = hi = us = 0;              // (nothing for a range of which this returns early: `next` ends at once)
         T = 0;
         if (!__all_sync(0xffffffffu, good)) return false;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            again += __shfl_xor_sync(0xffffffffu, again, o);
+        }
         T = sum * a.kv_heads;
-        // (at least a tile's places to a CTA, so that each one between a unit's first and last has a tile of it)
-        N = (int)min((long long)sh.ctas, T / sh.BN);
+        const double bytes = (double)again * a.kv_heads * a.dim * (a.bf16 ? 4 : 8);
+        const int waves = (int)max(1., min(min((double)(sh.ctas / ctas), ceil(bytes / kResident)), (double)(T / ((long long)ctas * kLeastTiles * sh.BN))));
+        // (at least a tile's places to a range, so that each one between a unit's first and last has a tile of it)
+        N = (int)min((long long)ctas * waves, T / sh.BN);
         if (N < 1) N = 1;
-        if (T == 0 || cta >= N) return true;
-        lo = start(cta);
-        hi = start(cta + 1);
+        if (T == 0 || range >= N) return true;
+        lo = start(range);
+        hi = start(range + 1);
         // the sequence that holds place lo, and where it begins
         long long b0 = 0;
         b = a.batch - 1;
@@ -147,7 +162,7 @@ struct Line {
         return true;
     }
     // any thread
-    __device__ __forceinline__ bool next(const ChunkAttnArgs& a, const Shape& sh, int cta, Piece& p)
+    __device__ __forceinline__ bool next(const ChunkAttnArgs& a, const Shape& sh, Piece& p)
     {
         while (us < hi) {
             p.b = b;
@@ -159,12 +174,14 @@ struct Line {
             p.n = s.n;
             p.ok = s.ok;
             p.seen = s.ok ? s.ctx + p.tok + p.tokens : 0;
+            p.common = s.ok ? s.ctx + p.tok + 1 : 0;
+            p.range = range;
             p.tiles = s.ok ? (p.seen - 1) / sh.BN + 1 : 1;
             p.at = us + head;
             const long long x = lo - p.at, y = hi - p.at;
             p.first = x <= 0 ? 0 : (int)min((long long)p.tiles, (x + sh.BN - 1) / sh.BN);
             p.last = y <= 0 ? 0 : (int)min((long long)p.tiles, (y + sh.BN - 1) / sh.BN);
-            p.slot = 2 * cta + (p.first == 0 ? 1 : 0);
+            p.slot = 2 * range + (p.first == 0 ? 1 : 0);
             // on to the next unit
             const long long places = head + (j == s.blocks - 1 ? s.last : s.base + s.step * (j + 1));
             us += places;
@@ -184,27 +201,24 @@ struct Line {
     }
 };
 
-// One thread of each CTA, piece by piece and once at the end.
-struct Recorder {
-    Record r = {};
-    int G, BN;
-    __device__ __forceinline__ Recorder(const ChunkAttnArgs& a, const Shape& sh) : G(a.heads / a.kv_heads), BN(sh.BN) {}
-    __device__ __forceinline__ void see(const Line& line, const Piece& p)
-    {
-        if (!p.begins() || p.ends()) return;
-        r.last = line.owner(p.at + (long long)(p.tiles - 1) * BN);
-        r.row0 = p.row0 * G;
-        r.hk = p.hk;
-        r.rows = p.tokens * G;
-    }
-    __device__ __forceinline__ void leave(const ChunkAttnArgs& a, int cta) { static_cast<Record*>(a.workspace)[cta] = r; }
-};
+// What the join reads, by one thread of each CTA: none of its ranges' records at first, then piece by piece.
+__device__ __forceinline__ void clear_records(const ChunkAttnArgs& a, const Shape& sh, int ctas, int cta)
+{
+    for (int r = cta; r < sh.ctas; r += ctas) static_cast<Record*>(a.workspace)[r] = {0, 0, 0, 0};
+}
+__device__ __forceinline__ void record(const ChunkAttnArgs& a, const Shape& sh, const Line& line, const Piece& p)
+{
+    if (!p.begins() || p.ends()) return;
+    const int G = a.heads / a.kv_heads;
+    static_cast<Record*>(a.workspace)[p.range] = {line.owner(p.at + (long long)(p.tiles - 1) * sh.BN), p.row0 * G, p.hk, p.tokens * G};
+}
 
 // The line's places fit what its products count: false for tables of many terabytes.
 __host__ __forceinline__ bool line_fits(const ChunkAttnArgs& a, const Shape& sh)
 {
     const int TB = sh.BM / (a.heads / a.kv_heads);
-    const double units = ((double)a.tokens / TB + a.batch) * a.kv_heads, most = (double)a.table_cols * a.page_size + (double)sh.head * sh.BN + 1;
+    const double units = ((double)a.tokens / TB + a.batch) * a.kv_heads;
+    const double most = (double)a.table_cols * a.page_size + (double)sh.head * sh.BN + 1;
     return units * (most < 2147483648.0 ? most : 2147483648.0) * sh.ctas < 4.0e18;
 }
 

@@ -84,8 +84,11 @@ bool keep_path_fits(const KeepPathArgs& a);
 cudaError_t launch_norm_rotate(const NormRotateArgs& a, cudaStream_t stream);
 // bf16 on the tensor cores (kda_chunk_attn_tc.cu), fp32 on the CUDA cores (kda_chunk_attn.cu)
 cudaError_t launch_chunk_attn(const ChunkAttnArgs& a, cudaStream_t stream);
-// whether a unit holds a token of every head of a group, and the tables no more than the kernels count
+cudaError_t launch_chunk_attn_tc(const ChunkAttnArgs& a, cudaStream_t stream);
+// whether the tables hold no more than the kernels count
 bool chunk_attn_fits(const ChunkAttnArgs& a);
+bool chunk_attn_tc_fits(const ChunkAttnArgs& a);
 size_t chunk_attn_workspace_bytes(const ChunkAttnArgs& a);
+size_t chunk_attn_tc_workspace_bytes(const ChunkAttnArgs& a);
 
 }  // namespace kda

@@ -39,20 +39,15 @@
 // of range are zero in shared memory.  A draft node's values may be seen by some rows only, so
 // non-finite ones are replaced by zero in the tile and added back in the epilogue of the
 // rows that see the node (a positive weight times infinity or NaN is itself).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "kda_draft_sm100.cuh"
+#include "kda_attn_tc.cuh"
 #include "kda_tree_attn.cuh"
 
 namespace kda {
 namespace {
 
-using namespace sm100;
+using namespace attn;
 
-constexpr int kBN = 128;
+constexpr int kBN = kTileTokens;
 constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmaxThreads + kProducerThreads + 128;
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads start with 128 each
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
@@ -86,113 +81,7 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory");
 };
 
-struct Maps {
-    CUtensorMap k, v;       // [pages][page_size][kv_heads][D], boxes of box_rows x 64 channels
-    int box_rows;
-};
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there)
-{
-    const int n = there ? 16 : 0;                   // 0: the 16 bytes become zero
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ bool finite_bf16(uint32_t h) { return (h & 0x7f80u) != 0x7f80u; }
-
 // ------------------------------------------------------------------ the cache rows
-// Where a tile's tokens lie: lane l of producer warp w has token 32 w + l.
-struct Rows {
-    size_t koff, voff;      // elements from the caches' starts
-    unsigned exists, lost;  // of the warp's 32 tokens: on a page; without one although the sequence has them
-};
-
-__device__ __forceinline__ Rows rows_of(const TreeAttnArgs& a, const attn::Piece& pc, int pos, int id, size_t row_stride, int D)
-{
-    const bool there = id >= 0 && id < a.num_pages;
-    const size_t in_page = (size_t)(pos % a.page_size) * row_stride + (size_t)pc.hk * D;
-    Rows r;
-    r.lost = __ballot_sync(0xffffffffu, !there && pos < pc.n);
-    r.exists = __ballot_sync(0xffffffffu, there);
-    r.koff = there ? (size_t)id * a.k_page_stride + in_page : 0;
-    r.voff = there ? (size_t)id * a.v_page_stride + in_page : 0;
-    return r;
-}
-
-// The warp's 32 rows of a tile through registers; rows that do not exist become zero.  In the
-// rows of draft nodes (node 0 in row `node0`, which may be negative) non-finite values become
-// zero too and their nodes are noted.
-template <int D>
-__device__ __forceinline__ void copy_rows(uint8_t* dst, const __nv_bfloat16* src, size_t off, unsigned exists, int w, int lane,
-                                          int node0, uint64_t* bad_nodes)
-{
-    constexpr int CH = D / 8, RPI = 32 / CH;        // 16-byte chunks of a row; rows a warp copies at once
-    const int sub = lane / CH, chunk = lane % CH;
-    uint32_t bad = 0;
-    for (int i0 = 0; i0 < 32; i0 += 8 * RPI) {
-        uint4 x[8];                                 // eight loads in flight
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = i0 + k * RPI + sub;
-            const size_t o = __shfl_sync(0xffffffffu, off, r);
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (exists >> r & 1) x[k] = *(reinterpret_cast<const uint4*>(src + o) + chunk);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = i0 + k * RPI + sub;
-            if (32 * w + r >= node0) {
-                uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool lo = finite_bf16(h[e]), hi = finite_bf16(h[e] >> 16);
-                    if (!(lo && hi)) bad |= 1u << r;
-                    h[e] = (lo ? h[e] & 0xffffu : 0u) | (hi ? h[e] & 0xffff0000u : 0u);
-                }
-                x[k] = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            *reinterpret_cast<uint4*>(dst + sw128_chunk(32 * w + r, chunk, 128)) = x[k];
-        }
-    }
-    bad = __reduce_or_sync(0xffffffffu, bad);
-    if (bad && lane == 0) {
-        for (int r = 0; r < 32; ++r)
-            if (bad >> r & 1) atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (32 * w + r - node0));
-    }
-}
-
-// The same for a V tile that came by TMA; rows past the last token (from row `rows` on) become zero.
-constexpr int kCleanThreads = 96;
-
-template <int D>
-__device__ __forceinline__ void clean_rows(uint8_t* tile, int node0, int rows, int t, uint64_t* bad_nodes)
-{
-    constexpr int CH = D / 8, STEP = kCleanThreads / CH;
-    const int chunk = t % CH;
-#pragma unroll 4
-    for (int r = max(0, node0) + t / CH; r < kBN; r += STEP) {
-        uint4* at = reinterpret_cast<uint4*>(tile + sw128_chunk(r, chunk, 128));
-        if (r >= rows) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint4 x = *at;
-        uint32_t h[4] = {x.x, x.y, x.z, x.w};
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool lo = finite_bf16(h[e]), hi = finite_bf16(h[e] >> 16);
-            bad |= !(lo && hi);
-            h[e] = (lo ? h[e] & 0xffffu : 0u) | (hi ? h[e] & 0xffff0000u : 0u);
-        }
-        if (bad) {
-            *at = make_uint4(h[0], h[1], h[2], h[3]);
-            atomicOr(reinterpret_cast<unsigned long long*>(bad_nodes), 1ull << (r - node0));
-        }
-    }
-}
-
 // By TMA.  Warp 0 of the four issues the boxes, a lane to a box; a V tile with draft nodes is
 // handed over by the other three once they have cleaned it.  A tile with tokens that have no
 // page passes through registers, by all four.
@@ -228,12 +117,12 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
                 if (w == 0 && fill >= (uint32_t)L::kSlots) wait(&sm.kv_empty[s], (fill / L::kSlots - 1) & 1);
                 if (lost) {
                     const int p = t0 + 32 * w + lane;
-                    const Rows rows = rows_of(a, pc, p, p < pc.n ? __ldg(table + p / a.page_size) : -1, (size_t)a.kv_heads * D, D);
+                    const Rows rows = rows_of(a, pc.hk, p, pc.n, p < pc.n ? __ldg(table + p / a.page_size) : -1, (size_t)a.kv_heads * D, D);
                     bad_page |= rows.lost != 0;
                     bar_sync(10, kProducerThreads); // the slot is free
                     if (kv == 0 && lane == 0) sm.missing[fill / 2 & 7][w] = rows.lost;
                     copy_rows<D>(dst, static_cast<const __nv_bfloat16*>(kv ? a.v_cache : a.k_cache), kv ? rows.voff : rows.koff, rows.exists,
-                                 w, lane, kv ? pc.ctx - t0 : kBN, &sm.bad_nodes[piece & 7]);
+                                 w, lane, kv ? pc.ctx - t0 : kBN, reinterpret_cast<uint32_t*>(&sm.bad_nodes[piece & 7]));
                     fence_proxy_async_smem();
                     bar_sync(10, kProducerThreads);
                     if (t == 0) mbar_arrive(&sm.kv_full[s]);
@@ -258,7 +147,7 @@ __device__ __forceinline__ void produce_boxes(const TreeAttnArgs& a, const attn:
                 } else if (kv && nodes) {
                     wait(landed, raw_phase >> s & 1);
                     raw_phase ^= 1u << s;
-                    clean_rows<D>(dst, pc.ctx - t0, pc.n - t0, t - 32, &sm.bad_nodes[piece & 7]);
+                    clean_rows<D>(dst, pc.ctx - t0, pc.n - t0, t - 32, reinterpret_cast<uint32_t*>(&sm.bad_nodes[piece & 7]));
                     fence_proxy_async_smem();
                     bar_sync(11, kCleanThreads);
                     if (t == 32) mbar_arrive(&sm.kv_full[s]);
@@ -307,7 +196,7 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
         int id = look_up(pc.first);
         for (int tile = pc.first; tile < pc.last; ++tile) {
             const int t0 = tile * kBN;
-            const Rows rows = rows_of(a, pc, t0 + 32 * w + lane, id, row_stride, D);
+            const Rows rows = rows_of(a, pc.hk, t0 + 32 * w + lane, pc.n, id, row_stride, D);
             bad_page |= rows.lost != 0;
             id = look_up(tile + 1);
 #pragma unroll
@@ -319,7 +208,7 @@ __device__ __forceinline__ void produce_gather(const TreeAttnArgs& a, const attn
                 const __nv_bfloat16* src = kv ? vc : kc;
                 const size_t off = kv ? rows.voff : rows.koff;
                 if (kv == 1 && t0 + kBN > pc.ctx) {
-                    copy_rows<D>(dst, src, off, rows.exists, w, lane, pc.ctx - t0, &sm.bad_nodes[piece & 7]);
+                    copy_rows<D>(dst, src, off, rows.exists, w, lane, pc.ctx - t0, reinterpret_cast<uint32_t*>(&sm.bad_nodes[piece & 7]));
                 } else {
 #pragma unroll 4
                     for (int i = 0; i < 32; i += RPI) {
@@ -473,31 +362,6 @@ __device__ __forceinline__ void tile_mask(uint64_t see, int t0, int ctx, uint4 l
             else if (at < 64) x = (uint32_t)(see >> at);
         }
         mw[k] = x & ~missing[k];
-    }
-}
-
-__device__ __forceinline__ float max_of(const float (&x)[32])
-{
-    float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-        a0 = fmaxf(a0, fmaxf(x[k], x[k + 1]));
-        a1 = fmaxf(a1, fmaxf(x[k + 2], x[k + 3]));
-    }
-    return fmaxf(a0, a1);
-}
-
-// One step of the transpose of 4 x 4 pieces over four lanes: lanes that differ in bit `by`
-// exchange the later of two pieces for the earlier one.
-__device__ __forceinline__ void swap_pieces(uint4& lo, uint4& hi, bool upper, int by)
-{
-    uint32_t* l = reinterpret_cast<uint32_t*>(&lo);
-    uint32_t* h = reinterpret_cast<uint32_t*>(&hi);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? l[e] : h[e], by);
-        if (upper) l[e] = got;
-        else h[e] = got;
     }
 }
 
@@ -823,40 +687,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_tc_kernel(TreeAttnArgs 
 // 128 rows: 190 wide (half of it empty), 178 with both streams on them.
 bool wide_rows(int nodes, int group) { return nodes * group > 128; }
 attn::Shape shape_of(bool wide) { return {wide ? 256 : 128, kBN, kCtas, kHead}; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
-}
-
-// Whether the cache can be read in boxes: see the top; a map holds strides below 2^40 bytes.
-bool in_boxes(const TreeAttnArgs& a)
-{
-    const size_t most = ((size_t)1 << 40) / 2 - 1;
-    return a.page_size % 8 == 0 && a.num_pages > 0 && a.k_page_stride <= most && a.v_page_stride <= most;
-}
-
-bool make_map(CUtensorMap* m, const void* cache, size_t page_stride, const TreeAttnArgs& a, int rows)
-{
-    const auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t D = (cuuint64_t)a.dim, H = (cuuint64_t)a.kv_heads;
-    const cuuint64_t dims[4] = {D, H, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages};
-    const cuuint64_t strides[3] = {D * 2, H * D * 2, (cuuint64_t)page_stride * 2};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1}, es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, a.dim == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int D, bool kWide, bool kBoxes>
 cudaError_t launch(const TreeAttnArgs& a, cudaStream_t stream)
