@@ -10,8 +10,8 @@
 //     wide     they take 128 rows each of a 256-row unit, and every tile serves both;
 //     narrow   (chunks of 128 rows at most, on average) the streams take the tiles in turn over the same rows, and
 //              their two parts are joined in the epilogue.
-// O is multiplied only when a row's maximum has grown by more than 2^8 since the last time
-// (until then the weights are at most 2^8, which bf16 and the fp32 sums hold as well).
+// A row's maximum is set anew, and O multiplied, only when its weights of a tile sum to more than 2^15 (until then no
+// weight is more, which bf16 and the fp32 sums hold as well).
 //
 // Warps 0-3 and 4-7: softmax and epilogue of stream 0 and 1, a row to a thread.  Warps 8-11:
 // the cache rows, into a ring of K and V tiles.  A thread of warp 12 issues the products, warps
@@ -44,7 +44,7 @@ constexpr int kCtas = 152;                          // one to an SM
 constexpr int kHead = 4;                            // a unit's fixed cost (Q, first tile, epilogue), in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTame = 4096.f;                     // largest m sc of the form with one operation
-constexpr float kGrow = 8.f;                        // powers of two a maximum may grow before O is multiplied
+constexpr float kMostSum = 32768.f;                 // most that a row's weights of a tile may sum to before its maximum is set anew
 
 struct Shared {
     uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done[2], o_free[2];
@@ -375,6 +375,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
     const uint32_t quad = 32 * (warp & 3);                            // the lanes this warp reaches
     const uint32_t tS = tmem_addr(sm.tmem, quad, L::kColS + 128 * w), tO = tmem_addr(sm.tmem, quad, L::kColO);
     const float sc = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;  // scores in powers of two
+    const float2 sc2 = make_float2(sc, sc);
     Waiter wait{a.status};
     Walk walk(sm, waves);
     chunk::Piece pc;
@@ -393,39 +394,22 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
 
         for (int i = kWide ? 0 : w; i < tiles; i += kWide ? 1 : 2) {
             const int t0 = (pc.first + i) * kBN;
+            // (no maximum to begin with, or one out of kTame's range)
+            bool again = !begun || __any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame));
             wait(&sm.s_full[w], used & 1);
             ++used;
             __syncwarp();
             tc_fence_after_sync();
             if (busy) {
                 const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
-                const bool all = t0 + kBN <= pc.common && !(missing.x | missing.y | missing.z | missing.w);
-                const float2 sc2 = make_float2(sc, sc);
-                // (x - m) sc in this order: the difference is exact where it matters, whatever the scores
-                auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), off), sc2);
-                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                        sum = __fadd2_rn(sum, e);
-                        p[k] = pack_bf16x2(e.x, e.y);
-                    }
-                };
-                bool stored = false;
-                if (all && !begun) {
-                    float x[32];
-                    tmem_ld32(tS, x);
-                    tmem_wait_ld();
-                    m = see ? max_of(x) : INFINITY;
-                }
-                // A tile that every row sees whole: the weights are formed from the last maximum (in
-                // a piece's first tile, that of 32 tokens) while the tile's own is still being
-                // found, and stored over the scores once it is known that it may stand (nearly always).
-                // x sc - m sc in one operation: m sc's rounding is a factor that a row's weights share, and
-                // up to kTame it is 2^-13 of a weight, below bf16's rounding, where the maximum changes.
-                if (all && !__any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame))) {
+                again |= t0 + kBN > pc.common || (missing.x | missing.y | missing.z | missing.w);
+                if (!again) {
+                    // The weights are formed from the last maximum and stored over the scores unless one is past what
+                    // may stand, which their sum tells: no maximum is looked for.
+                    // x sc - m sc in one operation: m sc's rounding is a factor that a row's weights share, and
+                    // up to kTame it is 2^-13 of a weight, below bf16's rounding, where the maximum changes.
                     const float2 off = make_float2(-m * sc, -m * sc);
-                    auto weigh = [&](const float (&x)[32], float2 off, float2& sum, uint32_t (&p)[16]) {
+                    auto weigh = [&](const float (&x)[32], float2& sum, uint32_t (&p)[16]) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), sc2, off);
@@ -435,41 +419,36 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                         }
                     };
                     float2 sum = make_float2(0.f, 0.f);
-                    float top = -INFINITY;
                     uint32_t p[4][16];
                     float xa[32], xb[32];
                     tmem_ld32(tS, xa);
                     tmem_wait_ld();
                     tmem_ld32(tS + 32, xb);
-                    top = fmaxf(top, max_of(xa));
-                    weigh(xa, off, sum, p[0]);
+                    weigh(xa, sum, p[0]);
                     tmem_wait_ld();
                     tmem_ld32(tS + 64, xa);
-                    top = fmaxf(top, max_of(xb));
-                    weigh(xb, off, sum, p[1]);
+                    weigh(xb, sum, p[1]);
                     tmem_wait_ld();
                     tmem_ld32(tS + 96, xb);
-                    top = fmaxf(top, max_of(xa));
-                    weigh(xa, off, sum, p[2]);
+                    weigh(xa, sum, p[2]);
                     tmem_wait_ld();
-                    top = fmaxf(top, max_of(xb));
-                    weigh(xb, off, sum, p[3]);
-                    if (!__any_sync(0xffffffffu, (top - m) * sc > kGrow)) {
+                    weigh(xb, sum, p[3]);
+                    again = __any_sync(0xffffffffu, sum.x + sum.y > kMostSum);
+                    if (!again) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
                         l += sum.x + sum.y;
-                        stored = true;
                     }
                 }
-                if (!stored) {
-                    // masks, the first maximum, or one that has grown: the maximum first, then the weights
+                if (again) {
+                    // masks, a first maximum, or one that has grown or is out of kTame's range: the maximum first, then the weights
                     // (word c's go to columns 16 c, over scores that have been read)
-                    uint32_t mw[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (!all) tile_mask(see, t0, missing, mw);
+                    uint32_t mw[4];                 // which of the tokens the row sees
+                    tile_mask(see, t0, missing, mw);
                     auto read = [&](int c, float (&x)[32]) {
-                        const uint32_t on = c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3];
                         tmem_ld32(tS + 32 * c, x);
                         tmem_wait_ld();
+                        const uint32_t on = c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
                     };
@@ -479,11 +458,9 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                         read(c, x);
                         top = fmaxf(top, max_of(x));
                     }
-                    const bool grow = (top - m) * sc > kGrow;
-                    const float nm = grow ? top : m;
-                    const float f = grow ? ex2((m - nm) * sc) : 1.f;   // 0 for the first maximum
+                    const bool grow = top > m;
+                    const float f = grow ? ex2((m - top) * sc) : 1.f;  // 0 for the first maximum
                     l *= f;
-                    m = nm;
                     if (begun && __any_sync(0xffffffffu, grow)) {      // (S is ready: the stream's last products into O are done)
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -494,13 +471,21 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                             tmem_st32(tO + D * w + c, x);
                         }
                     }
+                    if (grow) m = top;
+                    // (x - m) sc in this order: the difference is exact where it matters, whatever the scores
                     const float2 off = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t p[16];
                         read(c, x);
-                        weigh(x, off, sum, p);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[2 * k], x[2 * k + 1]), off), sc2);
+                            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                            sum = __fadd2_rn(sum, e);
+                            p[k] = pack_bf16x2(e.x, e.y);
+                        }
                         tmem_st16u(tS + 16 * c, p);
                     }
                     l += sum.x + sum.y;
