@@ -401,8 +401,11 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
             __syncwarp();
             tc_fence_after_sync();
             if (busy) {
+                float xa[32], xb[32];
+                tmem_ld32(tS, xa);                  // (of use to the first of the two forms only)
                 const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
                 again |= t0 + kBN > pc.common || (missing.x | missing.y | missing.z | missing.w);
+                tmem_wait_ld();
                 if (!again) {
                     // The weights are formed from the last maximum and stored over the scores unless one is past what
                     // may stand, which their sum tells: no maximum is looked for.
@@ -420,9 +423,6 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                     };
                     float2 sum = make_float2(0.f, 0.f);
                     uint32_t p[4][16];
-                    float xa[32], xb[32];
-                    tmem_ld32(tS, xa);
-                    tmem_wait_ld();
                     tmem_ld32(tS + 32, xb);
                     weigh(xa, sum, p[0]);
                     tmem_wait_ld();

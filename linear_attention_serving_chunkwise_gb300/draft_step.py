@@ -9,7 +9,11 @@ probabilities keep, and moves both memories to the end of the kept path:
     tree_decode     KDA layers: outputs of every node from one read of the state
     tree_attention  attention layers: every node over the cache and its own path
     verify_drafts   kept path and the token after it (the next pending token)
-    tree_commit     KDA states at the end of the path;  ``keep_path`` the same for the cache
+    tree_commit     KDA states at the end of the path;  ``cache_keep_path`` the same for the cache
+
+Before it a prompt goes through ``prefill`` in the KDA layers and, in the attention layers, through ``norm_rotate`` (keys and
+values into the cache) and ``chunk_attention``; ``page_fork`` with ``cache_copy`` lets several sequences go on from one
+prompt, ``page_release`` gives a sequence's pages back.
 
 The pending token is node 0 of the model's tree and drafted node i is node i + 1, so the target's
 row 0 is the one after the pending token.  ``HybridLayers`` holds the two memories of one KDA layer and
@@ -20,8 +24,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (KDA_PROLOGUE_ALL, KDA_TREE_PAD, page_tables, prefill, tree_attention, tree_commit, tree_decode,
-               verify_drafts)
+from . import (KDA_PROLOGUE_ALL, KDA_TREE_PAD, cache_copy, cache_keep_path, chunk_attention, norm_rotate, page_fork, page_release,
+               page_tables, prefill, tree_attention, tree_commit, tree_decode, verify_drafts)
 
 
 def with_pending(parents: torch.Tensor) -> torch.Tensor:
@@ -39,11 +43,8 @@ def with_pending_path(path: torch.Tensor, n_accept: torch.Tensor):
 def keep_path(cache: torch.Tensor, slots: torch.Tensor, path: torch.Tensor, n: torch.Tensor) -> None:
     """The kept nodes' rows of ``cache`` [pages, 2, page_size, heads, dim] moved to the front of the step's
     tokens.  slots [B, K]: where the nodes were written.  Entry e of a path is node e or a later
-    one, so every row moves towards the front; the rows are read before any is written."""
-    rows = cache.shape[2]
-    on = torch.arange(path.shape[1], device=path.device) < n[:, None]
-    src, dst = slots.gather(1, path.clamp_min(0).long())[on], slots[on]
-    cache[dst // rows, :, dst % rows] = cache[src // rows, :, src % rows]
+    one, so every row moves towards the front, as if all were read before any is written."""
+    cache_keep_path(slots.contiguous(), path.contiguous(), n, cache[:, 0], cache[:, 1])
 
 
 class HybridLayers:
@@ -57,6 +58,8 @@ class HybridLayers:
         self.context_lens, self.pages_held = i32(batch), i32(batch)
         self.block_table = torch.full((batch, table_cols), -1, dtype=torch.int32, device=device)
         self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=device)
+        self.shares = i32(num_pages)                       # holders of a page beyond the first
+        self.no_turns = torch.zeros(0, device=device)
 
     def reserve(self, tokens: int) -> torch.Tensor:
         """Slots [B, tokens] for that many tokens after every context.  Where the free pages, or a sequence's
@@ -71,13 +74,48 @@ class HybridLayers:
             raise RuntimeError("out of cache pages, or of columns of the block table")
         return slots.view(B, tokens)
 
-    def attend(self, q, k, v, slots, parents) -> torch.Tensor:
-        """Keys and values of the nodes into their slots, then the nodes over the cache."""
-        rows = self.cache.shape[2]
-        page, at = slots // rows, slots % rows
-        self.cache[page, 0, at] = k
-        self.cache[page, 1, at] = v
+    def write(self, q, k, v, slots, positions=None, inv_freq=None, **norms) -> torch.Tensor:
+        """Keys and values of any tokens into their slots.  With positions (shaped as the slots) and ``inv_freq``: queries and
+        keys rotated first; with q_weight, k_weight or eps: normed before that.  Returns the queries."""
+        flat = lambda t: t.reshape(-1, *t.shape[-2:])
+        kc, vc = self.cache.unbind(1)
+        if positions is None:
+            positions, inv_freq = slots.to(torch.int32), self.no_turns       # (nothing is rotated)
+        out = norm_rotate(flat(q), flat(k), flat(v), positions.reshape(-1), inv_freq, slots.reshape(-1), kc, vc, norm=bool(norms), **norms)
+        return out.view(q.shape)
+
+    def attend(self, q, k, v, slots, parents, **turn) -> torch.Tensor:
+        """Keys and values of the nodes into their slots, then the nodes over the cache.  ``turn``: as for ``write``."""
+        q = self.write(q, k, v, slots, **turn)
         return tree_attention(q, self.cache[:, 0], self.cache[:, 1], self.block_table, self.context_lens, parents)
+
+    def attend_chunks(self, q, k, v, slots, cu_seqlens, **turn) -> torch.Tensor:
+        """The same for chunks of prompts, packed: q [T, heads, dim], slots [T], cu_seqlens [B + 1]."""
+        q = self.write(q, k, v, slots, **turn)
+        return chunk_attention(q, self.cache[:, 0], self.cache[:, 1], self.block_table, self.context_lens, cu_seqlens)
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
+        """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages
+        shared, the last one copied.  The KDA state is that of the parent's whole context, so a shorter child has to replay its
+        tokens into it.  Where the free pages do not reach: RuntimeError, and the children they reach for are forked."""
+        self.pages_held, copies, taken = page_fork(parents, children, lens, self.pages_held, self.block_table, self.shares, self.free_pages,
+                                                   page_size=self.cache.shape[2])
+        cache_copy(copies, self.cache[:, 0], self.cache[:, 1])
+        p, c, ps = parents.long(), children.long(), self.cache.shape[2]
+        got = self.pages_held[c] == (lens + ps - 1) // ps
+        self.state[c] = torch.where(got[:, None, None, None], self.state[p], self.state[c])
+        self.context_lens[c] = torch.where(got, lens, self.context_lens[c])
+        taken, refused = torch.stack([taken[0], (~got).any().int()]).tolist()
+        self.free_pages = self.free_pages[taken:]
+        if refused:
+            raise RuntimeError("out of cache pages, or a fork of a row that holds pages")
+
+    def release(self, keep_lens: torch.Tensor) -> None:
+        """Every sequence's pages behind its first ``keep_lens`` [B] tokens given back (0: the sequence ends, its state becomes zero)."""
+        self.pages_held, freed, count = page_release(keep_lens, self.pages_held, self.block_table, self.shares, page_size=self.cache.shape[2])
+        self.context_lens = torch.minimum(self.context_lens, keep_lens)
+        self.state[keep_lens == 0] = 0
+        self.free_pages = torch.cat([self.free_pages, freed[:count.item()]])
 
 
 class ToyHybrid:
@@ -102,13 +140,12 @@ class ToyHybrid:
         q, k, v = (heads(y) for y in (x @ self.kda_in).chunk(3, -1))
         return q, k, v, heads((x @ self.decay).float()), (x @ self.beta).float().contiguous()
 
-    def _attention(self, h, slots, parents):
+    def _attention(self, h, attend):
+        """``attend``: the memory's call on packed q, k and v, parts of one projection's rows."""
         B, K, _ = h.shape
-        y = h @ self.att_in
-        q, k, v = y.split((self.width, self.kv_heads * self.dim, self.kv_heads * self.dim), -1)
-        view = lambda t, n: t.reshape(B, K, n, self.dim).contiguous()
-        o = self.mem.attend(view(q, self.heads), view(k, self.kv_heads), view(v, self.kv_heads), slots, parents)
-        return h + o.view(B, K, self.width) @ self.att_out
+        y = (h @ self.att_in).view(B * K, -1, self.dim)
+        o = attend(*y.split((self.heads, self.kv_heads, self.kv_heads), 1))
+        return h + o.reshape(B, K, self.width) @ self.att_out
 
     def _probs(self, h):
         h = h.float()
@@ -122,12 +159,10 @@ class ToyHybrid:
         q, k, v, g, beta = (t.reshape(B * T, *t.shape[2:]) for t in self._kda_inputs(x))
         o, self.mem.state = prefill(q, k, v, g, beta, num_seqs=B, init_state=self.mem.state, prologue=KDA_PROLOGUE_ALL)
         h = x + (o.view(B, T, self.width).to(torch.bfloat16) @ self.kda_out)
-        for t in range(0, T, 64):                      # the attention layer takes the prompt in chains of 64
-            part = h[:, t:t + 64]
-            n = part.shape[1]
-            chain = torch.arange(-1, n - 1, dtype=torch.int32, device=h.device).expand(B, n).contiguous()
-            last = self._attention(part, self.mem.reserve(n), chain)
-            self.mem.context_lens = self.mem.context_lens + n
+        slots = self.mem.reserve(T)
+        cu = torch.arange(0, (B + 1) * T, T, dtype=torch.int32, device=h.device)
+        last = self._attention(h, lambda q, k, v: self.mem.attend_chunks(q, k, v, slots.view(-1), cu))
+        self.mem.context_lens = self.mem.context_lens + T
         return self._probs(last[:, -1])
 
     def forward(self, tokens: torch.Tensor, parents: torch.Tensor):
@@ -138,7 +173,9 @@ class ToyHybrid:
         q, k, v, g, beta = self._kda_inputs(x)
         o, writes = tree_decode(q, k, v, g, beta, parents, self.mem.state, prologue=KDA_PROLOGUE_ALL)
         slots = self.mem.reserve(K)
-        h = self._attention(x + o.view(B, K, self.width).to(torch.bfloat16) @ self.kda_out, slots, parents)
+        nodes = lambda t: t.view(B, K, -1, self.dim)
+        h = self._attention(x + o.view(B, K, self.width).to(torch.bfloat16) @ self.kda_out,
+                            lambda q, k, v: self.mem.attend(nodes(q), nodes(k), nodes(v), slots, parents))
         self._step = (k, g, writes, slots)
         return self._probs(h)
 
