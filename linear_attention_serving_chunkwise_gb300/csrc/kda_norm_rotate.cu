@@ -19,8 +19,8 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMostTokens = 8;         // of a CTA
+constexpr int kThreads = 256;
+constexpr int kMostTokens = 8;         // of a CTA: a warp each
 
 __device__ __forceinline__ void unpack(uint4 u, float (&x)[8])
 {
@@ -51,123 +51,149 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4])
 }
 
 template <typename T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) norm_rotate_kernel(NormRotateArgs a, int per_cta)
+__global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(NormRotateArgs a, int per_cta)
 {
     constexpr int V = 16 / sizeof(T), CH = D / V, LANES = CH / 2, ROWS = 32 / LANES;   // a row's chunks and lanes, rows of a warp
     constexpr int U = 2;               // groups of rows whose loads are in flight together
-    __shared__ float2 s_turn[kMostTokens][D / 2];           // cosine, sine
-    __shared__ float s_w[2][D];
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5, l = lane % LANES, sub = lane / LANES;
+    __shared__ float4 s_turn[kMostTokens][V / 2][LANES];    // cosine, sine of a lane's V pairs, two at a time
+    const int t = threadIdx.x, lane = t & 31, l = lane % LANES, sub = lane / LANES;
     const int t0 = blockIdx.x * per_cta, tokens = min(per_cta, a.tokens - t0), half = a.rot / 2;
+    const int turned = a.rot / (2 * V);                     // chunks of each of the halves
 
-    for (int c = t; c < 2 * D; c += kThreads) {
-        const float* src = c < D ? a.q_weight : a.k_weight;
-        s_w[c / D][c % D] = src ? src[c % D] : 1.f;
-    }
     for (int i = t; i < tokens * half; i += kThreads) {
         const int k = i / half, c = i - k * half;
         double turn = (double)a.inv_freq[c] * 0.15915494309189533577;
         turn -= floor(turn);
         const unsigned long long f = (unsigned long long)(turn * 18446744073709551616.0) * (unsigned long long)(long long)a.positions[t0 + k];
         const float h = (float)(int)(f >> 32) * 4.656612873077393e-10f;   // half turns, from -1 to 1
-        s_turn[k][c] = make_float2(cospif(h), sinpif(h));
+        // pair c is the (c % V)-th of lane c / V, in both orders
+        reinterpret_cast<float2*>(&s_turn[k][c % V / 2][c / V])[c & 1] = make_float2(cospif(h), sinpif(h));
     }
     __syncthreads();
 
-    // this lane's chunks of a row
-    const int turned = a.rot / (2 * V);                     // chunks of each of the halves
-    int c0, c1;
-    if (kPairs) { c0 = 2 * l; c1 = 2 * l + 1; }
-    else if (l < turned) { c0 = l; c1 = l + turned; }
-    else { c0 = 2 * l; c1 = 2 * l + 1; }                    // (2 turned + 2 (l - turned))
-
-    const int rows = a.heads + 2 * a.kv_heads, groups = (rows + ROWS - 1) / ROWS, items = tokens * groups;
-    for (int i0 = w * U; i0 < items; i0 += kWarps * U) {
-        uint4 in[U][2];
-        T* dst[U];
-        int token[U], kind[U];         // query, key, value; -1: nothing
+    // this warp's token, and its share of the token's rows
+    const int each = kThreads / 32 / per_cta, k = (t >> 5) / each, part = (t >> 5) % each, tok = t0 + k;
+    if (k >= tokens) return;
+    // this lane's chunks of a row, and whether it has pairs to turn
+    int c0 = 2 * l, c1 = 2 * l + 1;                         // (of what is not turned: 2 turned + 2 (l - turned))
+    if (!kPairs && l < turned) { c0 = l; c1 = l + turned; }
+    float2 turn[V];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (i0 + u) / groups, r = (i0 + u - k * groups) * ROWS + sub, tok = t0 + k;
-            token[u] = k;
-            kind[u] = -1;
-            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
-            if (i0 + u >= items || r >= rows) continue;
-            const T* src;
-            if (r < a.heads) {
-                kind[u] = 0;
-                src = static_cast<const T*>(a.q) + (size_t)tok * a.q_stride + (size_t)r * D;
-                dst[u] = static_cast<T*>(a.q_out) + ((size_t)tok * a.heads + r) * D;
-            } else {
-                const bool value = r >= a.heads + a.kv_heads;
-                const int h = r - a.heads - (value ? a.kv_heads : 0);
-                const long long slot = a.slots[tok];
-                if (slot < 0) continue;
-                if (slot >= a.num_slots) {
-                    report_status(a.status, kDevBadSeqlens);
-                    continue;
-                }
-                kind[u] = value ? 2 : 1;
-                src = static_cast<const T*>(value ? a.v : a.k) + (size_t)tok * (value ? a.v_stride : a.k_stride) + (size_t)h * D;
-                const long long page = slot / a.page_size;
-                dst[u] = static_cast<T*>(value ? a.v_cache : a.k_cache) + (size_t)page * (value ? a.v_page_stride : a.k_page_stride) +
-                         ((size_t)(slot - page * a.page_size) * a.kv_heads + h) * D;
-            }
-            in[u][0] = *(reinterpret_cast<const uint4*>(src) + c0);
-            in[u][1] = *(reinterpret_cast<const uint4*>(src) + c1);
+    for (int i = 0; i < V; i += 2) {
+        float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (l * V < half) e = s_turn[k][i / 2][l];
+        turn[i] = make_float2(e.x, e.y);
+        turn[i + 1] = make_float2(e.z, e.w);
+    }
+    float wx[V], wy[V];
+    auto weights = [&](const float* w) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 x = w ? make_float4(w[c0 * V + i], w[c0 * V + i + 1], w[c0 * V + i + 2], w[c0 * V + i + 3]) : one;
+            const float4 y = w ? make_float4(w[c1 * V + i], w[c1 * V + i + 1], w[c1 * V + i + 2], w[c1 * V + i + 3]) : one;
+            wx[i] = x.x; wx[i + 1] = x.y; wx[i + 2] = x.z; wx[i + 3] = x.w;
+            wy[i] = y.x; wy[i + 1] = y.y; wy[i + 2] = y.z; wy[i + 3] = y.w;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[V], y[V];
-            unpack(in[u][0], x);
-            unpack(in[u][1], y);
+    };
+    // a row's norm and rotation, all lanes of a warp together
+    auto apply = [&](uint4 (&in)[2]) {
+        float x[V], y[V];
+        unpack(in[0], x);
+        unpack(in[1], y);
+        if (a.norm) {
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < V; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (kind[u] < 0) continue;
-            if (kind[u] != 2) {
-                if (a.norm) {
-                    const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-                    const float* wt = s_w[kind[u]];
+            const float inv = 1.f / sqrtf(sum * (1.f / D) + a.eps);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        x[i] = x[i] * inv * wt[c0 * V + i];
-                        y[i] = y[i] * inv * wt[c1 * V + i];
-                    }
-                }
-                const float2* turn = s_turn[token[u]];
-                if (kPairs) {
-#pragma unroll
-                    for (int i = 0; i < V; i += 2) {
-                        if (c0 * V < a.rot) {
-                            const float2 e = turn[(c0 * V + i) / 2];
-                            const float p = x[i], q = x[i + 1];
-                            x[i] = p * e.x - q * e.y;
-                            x[i + 1] = p * e.y + q * e.x;
-                        }
-                        if (c1 * V < a.rot) {
-                            const float2 e = turn[(c1 * V + i) / 2];
-                            const float p = y[i], q = y[i + 1];
-                            y[i] = p * e.x - q * e.y;
-                            y[i + 1] = p * e.y + q * e.x;
-                        }
-                    }
-                } else if (l < turned) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float2 e = turn[c0 * V + i];
-                        const float p = x[i], q = y[i];
-                        x[i] = p * e.x - q * e.y;
-                        y[i] = p * e.y + q * e.x;
-                    }
-                }
-                in[u][0] = pack(x);
-                in[u][1] = pack(y);
+            for (int i = 0; i < V; ++i) {
+                x[i] = x[i] * inv * wx[i];
+                y[i] = y[i] * inv * wy[i];
             }
-            *(reinterpret_cast<uint4*>(dst[u]) + c0) = in[u][0];
-            *(reinterpret_cast<uint4*>(dst[u]) + c1) = in[u][1];
+        }
+        if (kPairs) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                if (l * V < half) {                         // (a lane's pairs are turned together: rot is a multiple of 2 V)
+                    const float2 e = turn[i / 2], g = turn[V / 2 + i / 2];
+                    float p = x[i], q = x[i + 1];
+                    x[i] = p * e.x - q * e.y;
+                    x[i + 1] = p * e.y + q * e.x;
+                    p = y[i], q = y[i + 1];
+                    y[i] = p * g.x - q * g.y;
+                    y[i + 1] = p * g.y + q * g.x;
+                }
+            }
+        } else if (l < turned) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float p = x[i], q = y[i];
+                x[i] = p * turn[i].x - q * turn[i].y;
+                y[i] = p * turn[i].y + q * turn[i].x;
+            }
+        }
+        in[0] = pack(x);
+        in[1] = pack(y);
+    };
+
+    // queries
+    weights(a.q_weight);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (size_t)tok * a.q_stride);
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + (size_t)tok * a.heads * D);
+    for (int r0 = part * U * ROWS; r0 < a.heads; r0 += each * U * ROWS) {
+        uint4 in[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * ROWS + sub;
+            in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
+            if (r < a.heads) {
+                in[u][0] = src[r * CH + c0];
+                in[u][1] = src[r * CH + c1];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * ROWS + sub;
+            apply(in[u]);
+            if (r < a.heads) {
+                dst[r * CH + c0] = in[u][0];
+                dst[r * CH + c1] = in[u][1];
+            }
+        }
+    }
+    // keys, and the values that go to the same slot
+    const long long slot = a.slots[tok];
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        if (part == 0 && lane == 0) report_status(a.status, kDevBadSeqlens);
+        return;
+    }
+    weights(a.k_weight);
+    const long long page = slot / a.page_size;
+    const size_t in_page = (size_t)(slot - page * a.page_size) * a.kv_heads * D;
+    const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + (size_t)tok * a.k_stride);
+    const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + (size_t)tok * a.v_stride);
+    uint4* kd = reinterpret_cast<uint4*>(static_cast<T*>(a.k_cache) + (size_t)page * a.k_page_stride + in_page);
+    uint4* vd = reinterpret_cast<uint4*>(static_cast<T*>(a.v_cache) + (size_t)page * a.v_page_stride + in_page);
+    for (int r0 = part * ROWS; r0 < a.kv_heads; r0 += each * ROWS) {
+        const int r = r0 + sub;
+        const bool there = r < a.kv_heads;
+        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, y[2];
+        if (there) {
+            x[0] = ks[r * CH + c0];
+            x[1] = ks[r * CH + c1];
+            y[0] = vs[r * CH + c0];
+            y[1] = vs[r * CH + c1];
+        }
+        apply(x);
+        if (there) {
+            kd[r * CH + c0] = x[0];
+            kd[r * CH + c1] = x[1];
+            vd[r * CH + c0] = y[0];
+            vd[r * CH + c1] = y[1];
         }
     }
 }

@@ -148,25 +148,37 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(PageForkArgs a)
 }
 
 // ------------------------------------------------------------------ releases
-// One cluster of CTAs in three steps with its barrier between them:
+// Three steps with a barrier of all threads between them:
 //   1. what each row keeps (a row that would cut a page which others hold too is refused: appending to it would write
 //      into their tokens; decided before any share changes);
 //   2. shares - 1 for every entry given back;
-//   3. the pages whose entry is below zero, in ascending order: each warp counts those of its stretch of pages, the cluster
-//      exchanges the counts, each warp writes its own behind those of the warps before it.
+//   3. the pages whose entry is below zero, in ascending order: each warp counts those of its stretch of pages, the counts
+//      are exchanged, each warp writes its own behind those of the warps before it.
 // Integer sums only, and no order of arrival shows in the outputs.
-constexpr int kCluster = 16, kReleaseThreads = 1024, kReleaseWarps = kReleaseThreads / 32;
+// One CTA for what it does in a few microseconds, else a cooperative grid: see launch_page_release.
+constexpr int kReleaseThreads = 1024, kReleaseWarps = kReleaseThreads / 32, kReleaseCtas = 152;
+// One CTA alone up to these (GPU time): 4096 pages, 16 rows 8.4 us (a grid 13.9); 16384 pages, 64 rows of 128 14.0 (12.4), 512 rows
+// 32.9 (14.4); 600000 pages, 2048 rows of 512 315 (32.8).
+constexpr int kAlonePages = 8192;
+constexpr long long kAloneEntries = 8192;
 
+template <bool kGrid>
 __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageReleaseArgs a)
 {
     __shared__ int warp_count[kReleaseWarps];
-    __shared__ int cta_count;
-    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ int s_before, s_total;
+    const auto sync = [] {
+        if constexpr (kGrid) cg::this_grid().sync();
+        else __syncthreads();
+    };
     const int t = threadIdx.x, lane = t & 31, w = t >> 5, ps = a.page_size;
-    const int rank = (int)cluster.block_rank(), all_t = rank * kReleaseThreads + t, all_w = rank * kReleaseWarps + w;
+    const int ctas = kGrid ? gridDim.x : 1, cta = kGrid ? blockIdx.x : 0;
+    const long long threads = (long long)ctas * kReleaseThreads, warps = (long long)ctas * kReleaseWarps;
+    // (warp by warp over the CTAs, so that few items spread over all SMs)
+    const int all_w = w * ctas + cta, all_t = all_w * 32 + lane;
     bool bad = false;
 
-    for (int r = all_t; r < a.rows; r += kCluster * kReleaseThreads) {
+    for (long long r = all_t; r < a.rows; r += threads) {
         const int keep = a.keep_lens[r], held = a.pages_held[r];
         int left = held;
         if (keep < 0 || held < 0 || held > a.table_cols) {
@@ -186,45 +198,36 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
         }
         a.pages_held_out[r] = left;
     }
-    cluster.sync();
+    sync();
 
-    // a warp to kBlock columns of a row; the rows' numbers are read by a lane each, 32 items at a time
+    // a warp to kBlock columns of a row
     const int blocks = (a.table_cols + kBlock - 1) / kBlock;
     const long long items = (long long)a.rows * blocks;
-    for (long long i0 = (long long)all_w * 32; i0 < items; i0 += (long long)kCluster * kReleaseWarps * 32) {
-        const long long mine = i0 + lane;
-        int lo = 0, hi = 0;
-        if (mine < items) {
-            const int r = (int)(mine / blocks), j0 = (int)(mine % blocks) * kBlock;
-            const int held = a.pages_held[r];
-            lo = max(__ldcg(a.pages_held_out + r), j0);
-            hi = held <= a.table_cols ? min(held, j0 + kBlock) : 0;
+    for (long long i = all_w; i < items; i += warps) {
+        const int r = (int)(i / blocks), j0 = (int)(i % blocks) * kBlock, held = a.pages_held[r];
+        const int from = max(__ldcg(a.pages_held_out + r), j0), to = held <= a.table_cols ? min(held, j0 + kBlock) : 0;
+        if (from >= to) continue;
+        const int32_t* row = a.block_table + (size_t)r * a.table_cols;
+        int id[kBlock / 32];
+#pragma unroll
+        for (int x = 0; x < kBlock / 32; ++x) {
+            const int j = from + 32 * x + lane;
+            id[x] = j < to ? row[j] : -1;
         }
-        for (unsigned left = __ballot_sync(0xffffffffu, lo < hi); left; left &= left - 1) {
-            const int k = __ffs(left) - 1;
-            const int from = __shfl_sync(0xffffffffu, lo, k), to = __shfl_sync(0xffffffffu, hi, k);
-            const int32_t* row = a.block_table + (size_t)((i0 + k) / blocks) * a.table_cols;
-            int id[kBlock / 32];
 #pragma unroll
-            for (int x = 0; x < kBlock / 32; ++x) {
-                const int j = from + 32 * x + lane;
-                id[x] = j < to ? row[j] : -1;
-            }
-#pragma unroll
-            for (int x = 0; x < kBlock / 32; ++x) {
-                if (id[x] >= 0 && id[x] < a.num_pages) atomicSub(a.shares + id[x], 1);
-                else bad |= from + 32 * x + lane < to;
-            }
+        for (int x = 0; x < kBlock / 32; ++x) {
+            if (id[x] >= 0 && id[x] < a.num_pages) atomicSub(a.shares + id[x], 1);
+            else bad |= from + 32 * x + lane < to;
         }
     }
-    cluster.sync();
+    sync();
 
-    // this warp's pages [p0, p1)
-    const long long warps = (long long)kCluster * kReleaseWarps;
+    // this warp's pages [p0, p1), in the order of the CTAs and of their warps
     const int each = (int)(((long long)a.num_pages + warps * 32 - 1) / (warps * 32)) * 32;
-    const int p0 = (int)min((long long)a.num_pages, (long long)all_w * each), p1 = (int)min((long long)a.num_pages, (long long)p0 + each);
+    const long long mine = (long long)cta * kReleaseWarps + w;
+    const int p0 = (int)min((long long)a.num_pages, mine * each), p1 = (int)min((long long)a.num_pages, (long long)p0 + each);
     int count = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int p = p0 + lane; p < p1; p += 32) count += __ldcg(a.shares + p) < 0;
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) warp_count[w] = count;
@@ -238,15 +241,34 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
             if (lane >= o) incl += u;
         }
         warp_count[lane] = incl - n;
-        if (lane == 31) cta_count = incl;
+        if (lane == 31) {
+            s_before = 0;
+            s_total = incl;
+            if (kGrid && cta < a.num_pages) a.freed[cta] = incl;    // (as scratch: the list is written once all have read it)
+        }
     }
-    cluster.sync();
-    int before = warp_count[w], total = 0;
-    for (int c = 0; c < kCluster; ++c) {
-        const int n = *cluster.map_shared_rank(&cta_count, c);
-        if (c < rank) before += n;
-        total += n;
+    if constexpr (kGrid) {
+        sync();
+        if (w == 0) {
+            int before = 0, total = 0;
+#pragma unroll
+            for (int c = lane; c < kReleaseCtas; c += 32) {
+                const int n = c < min(ctas, a.num_pages) ? __ldcg(a.freed + c) : 0;
+                total += n;
+                before += c < cta ? n : 0;
+            }
+            before = __reduce_add_sync(0xffffffffu, before);
+            total = __reduce_add_sync(0xffffffffu, total);
+            if (lane == 0) {
+                s_before = before;
+                s_total = total;
+            }
+        }
     }
+    sync();
+    int before = s_before + warp_count[w];
+    const int total = s_total;
+#pragma unroll 4
     for (int q = p0; q < p1; q += 32) {
         const int p = q + lane, s = p < p1 ? __ldcg(a.shares + p) : 0;
         const unsigned gone = __ballot_sync(0xffffffffu, s < 0);
@@ -257,10 +279,9 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
         }
         before += __popc(gone);
     }
-    for (int i = total + all_t; i < a.num_pages; i += kCluster * kReleaseThreads) a.freed[i] = -1;
+    for (long long i = total + (long long)cta * kReleaseThreads + t; i < a.num_pages; i += threads) a.freed[i] = -1;
     if (all_t == 0) a.num_freed[0] = total;
     if (bad) report_status(a.status, kDevBadSeqlens);
-    cluster.sync();                    // no CTA ends while another reads its count
 }
 
 }  // namespace
@@ -279,25 +300,20 @@ cudaError_t launch_page_fork(const PageForkArgs& a, cudaStream_t stream)
 
 cudaError_t launch_page_release(const PageReleaseArgs& a, cudaStream_t stream)
 {
-    static unsigned long long done = 0;     // a bit per device: more CTAs to a cluster than the portable eight are allowed
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_RELAXED) >> dev & 1)) {
-        if ((e = cudaFuncSetAttribute(page_release_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-        if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELAXED);
+    if (a.num_pages <= kAlonePages && (long long)a.rows * a.table_cols <= kAloneEntries) {
+        page_release_kernel<false><<<1, kReleaseThreads, 0, stream>>>(a);
+        return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
+    cfg.gridDim = dim3(a.num_pages < kReleaseCtas ? (a.num_pages < 1 ? 1 : a.num_pages) : kReleaseCtas);   // (a word of scratch each)
     cfg.blockDim = dim3(kReleaseThreads);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, page_release_kernel, a);
+    return cudaLaunchKernelEx(&cfg, page_release_kernel<true>, a);
 }
 
 }  // namespace kda
