@@ -30,8 +30,18 @@ using attn::Shape;
 constexpr int kMostTokens = 0x7fffffff - 8191;
 constexpr int kMaxWaves = 8;
 // Bytes of keys and values that the CTAs may be at work on together, and the least tiles to a range of several waves.
-constexpr double kResident = 48e6;
+constexpr float kResident = 48e6f;
 constexpr int kLeastTiles = 24;
+
+// floor(a / b) for a >= 0, b > 0.  Not in line: the setting-up of a range has five of them, every CTA waits for it, and code
+// that runs once costs its way from memory.
+static __device__ __noinline__ long long quotient(long long a, long long b)
+{
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
+// (tiles are powers of two)
+__device__ __forceinline__ int tile_bits(const Shape& sh) { return 31 - __clz(sh.BN); }
 
 // One sequence of the call: its chunk and context, and the line's numbers for one of its (sequence, head)s.
 struct Seq {
@@ -82,11 +92,6 @@ struct Line {
     int N, range, TB, b, hk, j;
     Seq s;
 
-    __device__ __forceinline__ long long start(int c) const
-    {
-        const long long q = T / N, r = T - q * N;
-        return q * c + r * c / N;
-    }
     // the range with place x
     __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * N - 1) / T); }
 
@@ -96,14 +101,17 @@ struct Line {
         head = (long long)sh.head * sh.BN;
         TB = sh.BM / (a.heads / a.kv_heads);
         range = range_;
-        long long sum = 0, again = 0;           // (again: tokens that several blocks read)
+        long long sum = 0, mine = 0;            // places of a head: all sequences', of this lane's among the first 32
+        float again = 0.f;                      // tokens that several blocks read
         bool good = true;
         for (int i = lane; i < a.batch; i += 32) {
             Seq x;
             x.read(a, i, TB);
             good = good && x.n >= 0 && (i > 0 || x.tok0 == 0) && (i < a.batch - 1 || (long long)x.tok0 + x.n <= a.tokens);
-            sum += x.per_head(head);
-            again += x.blocks > 1 ? x.last : 0;
+            const long long p = x.per_head(head);
+            if (i == lane) mine = p;
+            sum += p;
+            again += x.blocks > 1 ? (float)x.last : 0.f;
         }
         lo = hi = us = 0;              // (nothing for a range of which this returns early: `next` ends at once)
         T = 0;
@@ -114,24 +122,31 @@ struct Line {
             again += __shfl_xor_sync(0xffffffffu, again, o);
         }
         T = sum * a.kv_heads;
-        const double bytes = (double)again * a.kv_heads * a.dim * (a.bf16 ? 4 : 8);
-        const int waves = (int)max(1., min(min((double)(sh.ctas / ctas), ceil(bytes / kResident)), (double)(T / ((long long)ctas * kLeastTiles * sh.BN))));
+        // as many waves as their keys and values ask for, of kLeastTiles at least to a range
+        const float bytes = again * a.kv_heads * a.dim * (a.bf16 ? 4.f : 8.f);
+        int waves = 1;
+        while ((waves + 1) * ctas <= sh.ctas && waves * kResident < bytes && (waves + 1ll) * ctas * kLeastTiles * sh.BN <= T) ++waves;
         // (at least a tile's places to a range, so that each one between a unit's first and last has a tile of it)
-        N = (int)min((long long)ctas * waves, T / sh.BN);
+        N = (int)min((long long)ctas * waves, T >> tile_bits(sh));
         if (N < 1) N = 1;
         if (T == 0 || range >= N) return true;
-        lo = start(range);
-        hi = start(range + 1);
+        const long long q = quotient(T, N), over = T - q * N, c0 = quotient(over * range, N), c1 = quotient(over * (range + 1), N);
+        lo = q * range + c0;
+        hi = q * (range + 1) + c1;
         // the sequence that holds place lo, and where it begins
         long long b0 = 0;
         b = a.batch - 1;
         for (int i0 = 0; i0 < a.batch; i0 += 32) {
-            Seq x;
-            long long m = 0;
-            if (i0 + lane < a.batch) {
-                x.read(a, i0 + lane, TB);
-                m = x.per_head(head) * a.kv_heads;
+            long long m = mine;
+            if (i0 > 0) {
+                Seq x;
+                m = 0;
+                if (i0 + lane < a.batch) {
+                    x.read(a, i0 + lane, TB);
+                    m = x.per_head(head);
+                }
             }
+            m *= a.kv_heads;
             long long incl = m;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -149,7 +164,7 @@ struct Line {
         }
         s.read(a, b, TB);
         const long long per = s.per_head(head), in = lo - b0;
-        hk = (int)(in / per);
+        hk = (int)quotient(in, per);
         const long long rest = in - hk * per;
         int l = 0, r = s.blocks - 1;    // the last block that begins at or before `rest`
         while (l < r) {
@@ -176,11 +191,11 @@ struct Line {
             p.seen = s.ok ? s.ctx + p.tok + p.tokens : 0;
             p.common = s.ok ? s.ctx + p.tok + 1 : 0;
             p.range = range;
-            p.tiles = s.ok ? (p.seen - 1) / sh.BN + 1 : 1;
+            p.tiles = s.ok ? ((p.seen - 1) >> tile_bits(sh)) + 1 : 1;
             p.at = us + head;
             const long long x = lo - p.at, y = hi - p.at;
-            p.first = x <= 0 ? 0 : (int)min((long long)p.tiles, (x + sh.BN - 1) / sh.BN);
-            p.last = y <= 0 ? 0 : (int)min((long long)p.tiles, (y + sh.BN - 1) / sh.BN);
+            p.first = x <= 0 ? 0 : (int)min((long long)p.tiles, (x + sh.BN - 1) >> tile_bits(sh));
+            p.last = y <= 0 ? 0 : (int)min((long long)p.tiles, (y + sh.BN - 1) >> tile_bits(sh));
             p.slot = 2 * range + (p.first == 0 ? 1 : 0);
             // on to the next unit
             const long long places = head + (j == s.blocks - 1 ? s.last : s.base + s.step * (j + 1));
