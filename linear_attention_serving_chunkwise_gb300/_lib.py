@@ -170,6 +170,23 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     return lib
 
 
+_bind = None
+
+
+def _bound():
+    """The compiled part of the binding (csrc/kda_bind.cpp), once the library is loaded."""
+    global _bind
+    if _bind is None:
+        load()
+        try:
+            from . import _bind as module
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is missing or of another PyTorch: run "
+                               "`python -m linear_attention_serving_chunkwise_gb300.build`") from e
+        _bind = module
+    return _bind
+
+
 def status_string(status: int) -> str:
     return load().kda_status_string(int(status)).decode()
 
@@ -628,49 +645,21 @@ def chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, 
     values are in the cache already (``norm_rotate``).  ``scale`` defaults to 1 / sqrt(D); ``workspace``: uint8 scratch of
     ``chunk_attention_workspace_bytes``, allocated if not given.  Returns out [T,Hq,D] of q's type; rows behind
     the last chunk are not written, so in a tensor allocated here they are undefined."""
-    T, H, D = q.shape
-    P, ps, Hk, _ = k_cache.shape
-    dt, dev, at = q.dtype, q.device, q.get_device()
-    code = _dtype_code(q)
-    qp = _expect("q", q, dt, (T, H, D), at)
-    kp, ks = _cache("k_cache", k_cache, dt, (P, ps, Hk, D), at)
-    vp, vs = _cache("v_cache", v_cache, dt, (P, ps, Hk, D), at)
-    B, cols = block_table.shape
-    table = _expect("block_table", block_table, _I32, (B, cols), at)
-    ctx = _expect("context_lens", context_lens, _I32, (B,), at)
-    cu = _expect("cu_seqlens", cu_seqlens, _I32, (B + 1,), at)
-    queue = _stream_on(stream, at)
-    desc = ctypes.byref(ChunkAttentionDesc(B, T, H, Hk, D, code, P, ps, cols, D ** -0.5 if scale is None else scale, ks, vs))
-    if out is None:
-        out = _fresh((T, H, D), dt, dev, stream)
-        op = out.data_ptr()
-    else:
-        op = _expect("out", out, dt, (T, H, D), at)
-    lib = load()
-    if workspace is None:
-        workspace = _fresh((lib.kda_chunk_attention_workspace_bytes(desc),), torch.uint8, dev, stream)
-    elif workspace.get_device() != at or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous and on the device of the other tensors")
-    st = lib.kda_chunk_attention(desc, qp, kp, vp, table, ctx, cu, op, workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), queue)
+    handle = None
+    if stream is not None:
+        handle = _stream_on(stream, q.get_device())
+        if workspace is None:
+            desc = make_chunk_attention_desc(block_table.shape[0], *q.shape[:2], k_cache.shape[2], q.shape[2], _dtype_code(q), *k_cache.shape[:2],
+                                             block_table.shape[1], 0.0, k_cache.stride(0), v_cache.stride(0))
+            workspace = _fresh((chunk_attention_workspace_bytes(desc),), torch.uint8, q.device, stream)
+    st, made = (_bind or _bound()).chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out, scale, workspace, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_chunk_attention")
-    return out
-
-
-def _tokens(name: str, t: torch.Tensor, dtype, shape, device: int):
-    """(address, elements from token to token) of a tensor [T, heads, dim] whose tokens are contiguous each."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
-    T, h, d = shape
-    stride = t.stride()
-    if T > 0 and stride[1:] != (d, 1) and not t[0].is_contiguous():
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), stride[0] if T > 1 else h * d
+    if out is not None:
+        return out
+    if stream is not None:
+        _keep_until_done(made, stream)
+    return made
 
 
 def norm_rotate(q, k, v, positions, inv_freq, slots, k_cache, v_cache, out=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -683,33 +672,16 @@ def norm_rotate(q, k, v, positions, inv_freq, slots, k_cache, v_cache, out=None,
     rotation); slots [T] int64 as ``page_tables`` returns them (negative: not written); k_cache, v_cache as for
     ``tree_attention``, written in place; q_weight, k_weight [D] fp32 or None for ones; ``norm=False``: rotation only;
     ``interleaved``: pairs of neighbouring channels instead of (i, i + R/2).  Returns the queries [T,Hq,D]."""
-    T, H, D = q.shape
-    Hk = k.shape[1]
-    P, ps = k_cache.shape[:2]
-    dt, dev, at = q.dtype, q.device, q.get_device()
-    code, R = _dtype_code(q), 2 * inv_freq.numel()
-    qp, qs = _tokens("q", q, dt, (T, H, D), at)
-    kp, kst = _tokens("k", k, dt, (T, Hk, D), at)
-    vp, vst = _tokens("v", v, dt, (T, Hk, D), at)
-    kc, kps = _cache("k_cache", k_cache, dt, (P, ps, Hk, D), at)
-    vc, vps = _cache("v_cache", v_cache, dt, (P, ps, Hk, D), at)
-    pos = _expect("positions", positions, _I32, (T,), at)
-    freq = _expect("inv_freq", inv_freq, _F32, (R // 2,), at)
-    slot = _expect("slots", slots, torch.int64, (T,), at)
-    wq = None if q_weight is None else _expect("q_weight", q_weight, _F32, (D,), at)
-    wk = None if k_weight is None else _expect("k_weight", k_weight, _F32, (D,), at)
-    queue = _stream_on(stream, at)
-    if out is None:
-        out = _fresh((T, H, D), dt, dev, stream)
-        op = out.data_ptr()
-    else:
-        op = _expect("out", out, dt, (T, H, D), at)
     flags = (KDA_ROTATE_INTERLEAVED if interleaved else 0) | (0 if norm else KDA_ROTATE_NO_NORM)
-    desc = NormRotateDesc(T, H, Hk, D, code, R, flags, P, ps, eps, qs, kst, vst, kps, vps)
-    st = load().kda_norm_rotate(ctypes.byref(desc), qp, kp, vp, wq, wk, freq, pos, slot, op, kc, vc, queue)
+    handle = None if stream is None else _stream_on(stream, q.get_device())
+    st, made = (_bind or _bound()).norm_rotate(q, k, v, positions, inv_freq, slots, k_cache, v_cache, out, q_weight, k_weight, eps, flags, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_norm_rotate")
-    return out
+    if out is not None:
+        return out
+    if stream is not None:
+        _keep_until_done(made, stream)
+    return made
 
 
 def page_fork(parents, children, lens, pages_held, block_table, shares, free_pages, *, page_size: int, stream=None, check=True):
@@ -718,21 +690,13 @@ def page_fork(parents, children, lens, pages_held, block_table, shares, free_pag
     block_table [R, cols] int32 and shares [num_pages] int32 (holders of a page beyond the first), both updated in place; free_pages
     [F] int32, taken from index 0 on, one for every length that is no multiple of ``page_size``.  Returns (pages_held after
     the call [R] int32, copies [n, 3] int32 for ``cache_copy``, pages_taken [1] int32)."""
-    dev, (R, cols) = block_table.device, block_table.shape
-    at, n, F, P = block_table.get_device(), parents.numel(), free_pages.numel(), shares.numel()
-    par = _expect("parents", parents, _I32, (n,), at)
-    chi = _expect("children", children, _I32, (n,), at)
-    length = _expect("lens", lens, _I32, (n,), at)
-    had = _expect("pages_held", pages_held, _I32, (R,), at)
-    table = _expect("block_table", block_table, _I32, (R, cols), at)
-    sha = _expect("shares", shares, _I32, (P,), at)
-    free = _expect("free_pages", free_pages, _I32, (F,), at)
-    queue = _stream_on(stream, at)
-    held, copies, taken = _fresh((R,), _I32, dev, stream), _fresh((n, 3), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
-    st = load().kda_page_fork(n, R, cols, P, F, page_size, par, chi, length, had, table, sha, free, held.data_ptr(), copies.data_ptr(),
-                              taken.data_ptr(), queue)
+    handle = None if stream is None else _stream_on(stream, block_table.get_device())
+    st, held, copies, taken = (_bind or _bound()).page_fork(parents, children, lens, pages_held, block_table, shares, free_pages, page_size, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_page_fork")
+    if stream is not None:
+        for t in (held, copies, taken):
+            _keep_until_done(t, stream)
     return held, copies, taken
 
 
@@ -741,51 +705,22 @@ def page_release(keep_lens, pages_held, block_table, shares, *, page_size: int, 
     int32; block_table [R, cols] int32, only read; shares [num_pages] int32, updated in place.  Returns (pages_held after the
     call [R] int32, freed [num_pages] int32: the pages that nobody holds any more in ascending order, then -1, num_freed
     [1] int32)."""
-    dev, (R, cols) = block_table.device, block_table.shape
-    at, P = block_table.get_device(), shares.numel()
-    keep = _expect("keep_lens", keep_lens, _I32, (R,), at)
-    had = _expect("pages_held", pages_held, _I32, (R,), at)
-    table = _expect("block_table", block_table, _I32, (R, cols), at)
-    sha = _expect("shares", shares, _I32, (P,), at)
-    queue = _stream_on(stream, at)
-    held, freed, count = _fresh((R,), _I32, dev, stream), _fresh((P,), _I32, dev, stream), _fresh((1,), _I32, dev, stream)
-    st = load().kda_page_release(R, cols, P, page_size, keep, had, table, sha, held.data_ptr(), freed.data_ptr(), count.data_ptr(), queue)
+    handle = None if stream is None else _stream_on(stream, block_table.get_device())
+    st, held, freed, count = (_bind or _bound()).page_release(keep_lens, pages_held, block_table, shares, page_size, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_page_release")
+    if stream is not None:
+        for t in (held, freed, count):
+            _keep_until_done(t, stream)
     return held, freed, count
-
-
-def _cache_layers(k_cache, v_cache, device: int):
-    """(descriptor, addresses) of the caches of all layers, [layers, pages, page_size, heads, dim], or of one, without the first."""
-    dt, shape = k_cache.dtype, k_cache.shape
-    code = _dtype_code(k_cache)
-    if len(shape) not in (4, 5):
-        raise ValueError("k_cache must be [pages, page_size, heads, dim], or that for each layer")
-    L, (P, ps, h, d) = (1 if len(shape) == 4 else shape[0]), shape[-4:]
-    at, strides = [], []
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dtype is not dt:
-            raise TypeError(f"{name} must be {dt}, got {c.dtype}")
-        if c.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(c.shape)}")
-        if c.get_device() != device:
-            raise ValueError(f"{name} is on {c.device}, not on the device of the other tensors")
-        stride = c.stride()
-        if stride[-3:] != (h * d, d, 1) and L > 0 and P > 0 and not (c[0, 0] if len(shape) == 5 else c[0]).is_contiguous():
-            raise ValueError(f"{name}: each page must be contiguous")
-        at.append(c.data_ptr())
-        strides.append((stride[0] if len(shape) == 5 else 0, stride[-4]))
-    return CacheDesc(L, P, ps, h, d, code, strides[0][0], strides[1][0], strides[0][1], strides[1][1]), at
 
 
 def cache_copy(copies, k_cache, v_cache, *, stream=None, check=True):
     """Rows of pages copied in every layer, through ``kda_cache_copy``: copies [n, 3] int32 (source page, target page,
     rows) as ``page_fork`` returns them; k_cache, v_cache [layers, pages, page_size, Hk, D] (or one layer's, without
     the first) of fp32 or bf16, each page contiguous, in place."""
-    at, n = copies.get_device(), copies.shape[0]
-    pairs = _expect("copies", copies, _I32, (n, 3), at)
-    desc, (kp, vp) = _cache_layers(k_cache, v_cache, at)
-    st = load().kda_cache_copy(ctypes.byref(desc), n, pairs, kp, vp, _stream_on(stream, at))
+    handle = None if stream is None else _stream_on(stream, copies.get_device())
+    st, = (_bind or _bound()).cache_copy(copies, k_cache, v_cache, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_cache_copy")
 
@@ -794,12 +729,8 @@ def cache_keep_path(slots, path, n_accept, k_cache, v_cache, *, stream=None, che
     """The kept nodes' rows of a draft step moved to the front of the step's tokens in every layer, through
     ``kda_cache_keep_path``: slots [B,K] int64, where the nodes are in the cache; path [B,K] and n_accept [B] int32 as
     ``verify_drafts`` returns them; k_cache, v_cache as for ``cache_copy``, in place."""
-    at, (B, K) = slots.get_device(), slots.shape
-    where = _expect("slots", slots, torch.int64, (B, K), at)
-    kept = _expect("path", path, _I32, (B, K), at)
-    count = _expect("n_accept", n_accept, _I32, (B,), at)
-    desc, (kp, vp) = _cache_layers(k_cache, v_cache, at)
-    st = load().kda_cache_keep_path(ctypes.byref(desc), B, K, where, kept, count, kp, vp, _stream_on(stream, at))
+    handle = None if stream is None else _stream_on(stream, slots.get_device())
+    st, = (_bind or _bound()).cache_keep_path(slots, path, n_accept, k_cache, v_cache, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_cache_keep_path")
 

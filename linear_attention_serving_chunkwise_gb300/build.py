@@ -1,7 +1,8 @@
 """Build the KDA CUDA library in-tree for sm_103a with nvcc (no cmake, no torch extension).
 
 ``python -m linear_attention_serving_chunkwise_gb300.build`` or ``build()`` compiles each
-``csrc/*.cu`` translation unit in parallel and links ``libkda_gb300.so`` beside this file.
+``csrc/*.cu`` translation unit in parallel and links ``libkda_gb300.so`` beside this file, and ``_bind.so``, the
+compiled part of the Python binding (``csrc/kda_bind.cpp``, with the installed PyTorch's headers).
 ``build(phase_clocks=True)`` builds a separate instrumented library,
 ``libkda_gb300_clocks.so``, with the per-phase cycle marks compiled in (see phase_clocks.py);
 the library everything else loads never has them.
@@ -19,6 +20,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda_gb300.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "kda_bind.cpp")
 OBJ_CLOCKS = os.path.join(PKG, "_build_clocks")
 LIB_CLOCKS = os.path.join(PKG, "libkda_gb300_clocks.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,9 +54,54 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def bind_up_to_date() -> bool:
+    """Newer than its sources, and built with the PyTorch that is installed."""
+    import torch
+    stamp = os.path.join(OBJ, "bind.torch")
+    if not os.path.exists(BIND) or not os.path.exists(stamp) or open(stamp).read() != torch.__version__:
+        return False
+    return all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in _deps() + [BIND_SRC])
+
+
+def _compile_bind() -> str:
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")]
+    obj = os.path.join(OBJ, "kda_bind.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in includes:
+        cmd += ["-isystem", i]
+    r = subprocess.run(cmd + ["-c", BIND_SRC, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on kda_bind.cpp")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", obj, "-o", BIND + ".tmp", "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L", libs,
+           f"-Wl,-rpath,{libs}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("linking _bind.so failed")
+    os.replace(BIND + ".tmp", BIND)
+    with open(os.path.join(OBJ, "bind.torch"), "w") as f:
+        f.write(torch.__version__)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, phase_clocks: bool = False) -> str:
     lib_path, obj_dir = (LIB_CLOCKS, OBJ_CLOCKS) if phase_clocks else (LIB, OBJ)
-    if not force and up_to_date(lib_path):
+    current = not force and up_to_date(lib_path)
+    bind = not phase_clocks and (force or not current or not bind_up_to_date())
+    if current and not bind:
+        return lib_path
+    if current:
+        _link_bind(_compile_bind())
         return lib_path
     nvcc = _nvcc()
     os.makedirs(obj_dir, exist_ok=True)
@@ -75,6 +123,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, pha
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(_sources()))) as ex:
+        bind_obj = ex.submit(_compile_bind) if bind else None
         objs = list(ex.map(compile_one, _sources()))
     libdir = _cuda_lib_dir(nvcc)
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", lib_path + ".tmp"] + objs + \
@@ -84,6 +133,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, pha
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"linking {os.path.basename(lib_path)} failed")
     os.replace(lib_path + ".tmp", lib_path)
+    if bind:
+        _link_bind(bind_obj.result())
     return lib_path
 
 

@@ -184,35 +184,21 @@ def _calls(**over):
     }
 
 
-class _Never:
-    """Stands in for the library: any call of it is a failure."""
-
-    def __getattr__(self, name):
-        if name.endswith("_workspace_bytes"):
-            return lambda *a: 64
-
-        def called(*a):
-            raise AssertionError(f"{name} was called")
-        return called
-
-
 @pytest.mark.parametrize("name", sorted(_calls()))
-def test_tensors_on_the_cpu_are_refused(monkeypatch, name):
-    monkeypatch.setattr(_lib, "_raw_stream", lambda device: 0)
-    monkeypatch.setattr(_lib, "_lib", _Never())
+def test_tensors_on_the_cpu_are_refused(name):
     with pytest.raises(ValueError, match="CUDA device"):
         _calls()[name]()
 
 
 @pytest.mark.parametrize("name", sorted(_calls()))
-def test_every_call_asks_for_its_stream(monkeypatch, name):
-    """With the check of the device taken for passed, the library is reached: no call goes there without it."""
+def test_a_given_stream_is_looked_at_first(monkeypatch, name):
+    """Its handle reaches the call by way of the check of its device only."""
     asked = []
     monkeypatch.setattr(_lib, "_stream_on", lambda stream, device: asked.append((stream, device)) or 0)
-    monkeypatch.setattr(_lib, "_lib", _Never())
-    with pytest.raises(AssertionError, match=f"kda_{name} was called"):
-        _calls()[name]()
-    assert asked == [(None, -1)]
+    more = {"workspace": _z(64, dt=torch.uint8)} if name == "chunk_attention" else {}
+    with pytest.raises(ValueError, match="CUDA device"):
+        _calls()[name](stream="one", **more)
+    assert asked == [("one", -1)]
 
 
 WRONG = [("chunk_attention", dict(q=_z(6, 4, 64).half()), TypeError), ("chunk_attention", dict(kc=_z(5, 8, 2, 64).bfloat16()), TypeError),
@@ -232,16 +218,29 @@ WRONG = [("chunk_attention", dict(q=_z(6, 4, 64).half()), TypeError), ("chunk_at
 
 
 @pytest.mark.parametrize("name,over,error", WRONG, ids=[f"{n}-{next(iter(o))}-{i}" for i, (n, o, _) in enumerate(WRONG)])
-def test_wrong_tensors_are_refused(monkeypatch, name, over, error):
+def test_wrong_tensors_are_refused(name, over, error):
     """Shapes, types and strides that the C calls cannot see."""
-    monkeypatch.setattr(_lib, "_stream_on", lambda stream, device: 0)
-    monkeypatch.setattr(_lib, "_lib", _Never())
-    with pytest.raises(error):
+    with pytest.raises(error) as e:
         _calls(**over)[name]()
+    assert "CUDA device" not in str(e.value)
 
 
-def test_a_workspace_with_gaps_is_refused(monkeypatch):
-    monkeypatch.setattr(_lib, "_stream_on", lambda stream, device: 0)
-    monkeypatch.setattr(_lib, "_lib", _Never())
-    with pytest.raises(ValueError, match="workspace"):
-        _calls()["chunk_attention"](workspace=_z(64, 2, dt=torch.uint8)[:, 0])
+def test_wrong_arguments_are_refused():
+    calls = _calls()
+    lens, table, shares = _z(2, dt=I32), _z(2, 2, dt=I32), _z(9, dt=I32)
+    for bad, error in ((1 << 40, ValueError), (-1 << 40, ValueError), (1 << 80, ValueError), (2.5, TypeError), (None, TypeError)):
+        with pytest.raises(error):
+            kda.page_release(lens, lens, table, shares, page_size=bad)
+    with pytest.raises(TypeError):
+        kda.page_release(None, lens, table, shares, page_size=8)
+    with pytest.raises(TypeError):
+        kda.cache_copy([[0, 1, 2]], _z(5, 8, 2, 64), _z(5, 8, 2, 64))
+    for kw, error in (({"scale": "x"}, TypeError), ({"out": _z(5, 4, 64)}, ValueError), ({"out": _z(6, 4, 64).bfloat16()}, TypeError),
+                      ({"workspace": _z(64, 2, dt=torch.uint8)[:, 0]}, ValueError), ({"workspace": 5}, TypeError)):
+        with pytest.raises(error) as e:
+            calls["chunk_attention"](**kw)
+        assert "CUDA device" not in str(e.value)
+    for kw, error in (({"eps": None}, TypeError), ({"q_weight": _z(63)}, ValueError), ({"k_weight": _z(64).double()}, TypeError), ({"out": _z(6, 4, 32)}, ValueError)):
+        with pytest.raises(error) as e:
+            calls["norm_rotate"](**kw)
+        assert "CUDA device" not in str(e.value)
