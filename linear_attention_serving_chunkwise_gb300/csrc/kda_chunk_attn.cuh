@@ -54,7 +54,7 @@ struct Seq {
     __device__ __forceinline__ void read(const ChunkAttnArgs& a, int b, int TB)
     {
         tok0 = __ldg(a.cu_seqlens + b);
-        n = __ldg(a.cu_seqlens + b + 1) - tok0;
+        n = (int)((uint32_t)__ldg(a.cu_seqlens + b + 1) - (uint32_t)tok0);
         ctx = __ldg(a.context_lens + b);
         ok = ctx >= 0 && n >= 0 && ctx <= kMostTokens - n && (long long)ctx + n <= (long long)a.table_cols * a.page_size;
         blocks = n > 0 ? (n - 1) / TB + 1 : 0;
@@ -107,7 +107,7 @@ struct Line {
         for (int i = lane; i < a.batch; i += 32) {
             Seq x;
             x.read(a, i, TB);
-            good = good && x.n >= 0 && (i > 0 || x.tok0 == 0) && (i < a.batch - 1 || (long long)x.tok0 + x.n <= a.tokens);
+            good = good && x.n >= 0 && x.tok0 >= 0 && (i > 0 || x.tok0 == 0) && (long long)x.tok0 + x.n <= a.tokens;   // (of each: n may have wrapped)
             const long long p = x.per_head(head);
             if (i == lane) mine = p;
             sum += p;

@@ -172,7 +172,8 @@ def test_bad_input_is_reported_and_the_rest_goes_on(cuda_lib, dtype):
         mine[int(cu[b]):int(cu[b + 1])] = True
         assert not out.cpu()[mine].any()
         assert ((out.cpu().double() - ref).abs() <= bound)[~mine].all()
-    for ends in ([1, 70, 75, 205, 206], [0, 70, 60, 205, 206], [0, 70, 75, 205, 207], [0, -1, 75, 205, 206], [0, 70, 75, 0x7fffffff, 206]):
+    for ends in ([1, 70, 75, 205, 206], [0, 70, 60, 205, 206], [0, 70, 75, 205, 207], [0, -1, 75, 205, 206], [0, 70, 75, 0x7fffffff, 206], [0, 0x7fffffff, -2, 205, 206],
+                 [0, 70, -0x80000000, 205, 206]):
         out = torch.full_like(q, 5.0).cuda()
         _run(cuda_lib, q, kv, table, c, torch.tensor(ends, dtype=I32), out=out)
         assert cuda_lib.last_device_status() == bad and (out == 5.0).all(), ends
