@@ -19,6 +19,36 @@ struct Tile {
     static constexpr size_t kSmem = (size_t)(kBM * LD + 2 * BN * LD + kBM * LP) * 4;
 };
 
+// o += p v over a tile: eight rows of weights from sp on, four channels of every 16 from sv on.  kSome: a weight of 0 is
+// skipped (a test for each, so not where all rows see the whole tile).
+template <int D, bool kSome>
+__device__ __forceinline__ void add_values(float (&o)[kTM][Tile<D>::CD], const float* sp, const float* sv)
+{
+    using L = Tile<D>;
+#pragma unroll 2
+    for (int j = 0; j < L::BN; j += 4) {
+        float4 p4[kTM];
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + i * L::LP + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v[L::CD];
+#pragma unroll
+            for (int k = 0; k < L::CD; k += 4) {
+                const float4 v4 = *reinterpret_cast<const float4*>(sv + (j + e) * L::LD + 16 * k);
+                v[k] = v4.x; v[k + 1] = v4.y; v[k + 2] = v4.z; v[k + 3] = v4.w;
+            }
+#pragma unroll
+            for (int i = 0; i < kTM; ++i) {
+                const float p = e == 0 ? p4[i].x : e == 1 ? p4[i].y : e == 2 ? p4[i].z : p4[i].w;
+                if (kSome && p == 0.f) continue;
+#pragma unroll
+                for (int k = 0; k < L::CD; ++k) o[i][k] = fmaf(p, v[k], o[i][k]);
+            }
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_kernel(ChunkAttnArgs a, attn::Shape sh)
 {
@@ -143,27 +173,10 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                 for (int k = 0; k < CD; ++k) o[i][k] *= f;
             }
             __syncwarp();             // a row's weights are written and read by the same half warp
-            const bool partial = t0 + BN > pc.ctx + pc.tok + 1;      // (for the first row)
-            for (int j = 0; j < BN; j += 4) {
-                float4 p4[kTM];
-#pragma unroll
-                for (int i = 0; i < kTM; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty * kTM + i) * LP + j);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v[CD];
-#pragma unroll
-                    for (int k = 0; k < CD; k += 4) {
-                        const float4 v4 = *reinterpret_cast<const float4*>(sv + (j + e) * LD + tx * 4 + 16 * k);
-                        v[k] = v4.x; v[k + 1] = v4.y; v[k + 2] = v4.z; v[k + 3] = v4.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kTM; ++i) {
-                        const float p = e == 0 ? p4[i].x : e == 1 ? p4[i].y : e == 2 ? p4[i].z : p4[i].w;
-                        if (partial && p == 0.f) continue;
-#pragma unroll
-                        for (int k = 0; k < CD; ++k) o[i][k] = fmaf(p, v[k], o[i][k]);
-                    }
-                }
+            if (t0 + BN > pc.ctx + pc.tok + 1) {     // (some rows do not see all of it)
+                add_values<D, true>(o, sp + ty * kTM * LP, sv + tx * 4);
+            } else {
+                add_values<D, false>(o, sp + ty * kTM * LP, sv + tx * 4);
             }
         }
         // the unit is done here, or its part goes to the workspace

@@ -28,6 +28,8 @@
 // of range are zero in shared memory.  The values of the block's own tokens may be seen by some rows only, so
 // non-finite ones are replaced by zero in the tile and added back in the epilogue of the
 // rows that see the token (a positive weight times infinity or NaN is itself).
+#include <type_traits>
+
 #include "kda_attn_tc.cuh"
 #include "kda_chunk_attn.cuh"
 
@@ -316,7 +318,8 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
             if (i == items - 1) umma_commit(&sm.q_empty);
         };
         // The values of item i, and the stream's next scores right behind them: all that they need is waited for before the
-        // weights are, and slots are given back after both.
+        // weights are, and slots are given back after both.  (Not the next keys where the streams take the tiles in turn: they are
+        // four slots on, and few rows are bound by the loads: 1317 -> 1249 us for 64 tokens after 4096 to 32768 each.)
         auto step = [&](int i, int w) {
             const bool last = !kWide || w == 1, more = i + 2 < items;
             const uint32_t s = vs_;
@@ -326,7 +329,7 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
                 if (pieces[w]) wait(&sm.o_free[w], (pieces[w] - 1) & 1);
                 ++pieces[w];
             }
-            const uint32_t k = more ? next_k(w) : 0;
+            uint32_t k = kWide && more ? next_k(w) : 0;
             const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
@@ -336,6 +339,7 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
                 for (int ks = 0; ks < kBN / 16; ++ks)
                     umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
             }
+            if (!kWide && more) k = next_k(w);
             if (more) scores(w, k);
             else umma_commit(&sm.o_done[w]);
             if (last) umma_commit(&sm.kv_empty[s]);
@@ -401,18 +405,31 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
 
         for (int i = kWide ? 0 : w; i < tiles; i += kWide ? 1 : 2) {
             const int t0 = (pc.first + i) * kBN;
-            // (no maximum to begin with, or one out of kTame's range)
-            bool again = !begun || __any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame));
             wait(&sm.s_full[w], used & 1);
             ++used;
             __syncwarp();
             tc_fence_after_sync();
             if (busy) {
                 float xa[32], xb[32];
-                tmem_ld32(tS, xa);                  // (of use to the first of the two forms only)
+                tmem_ld32(tS, xa);
                 const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
-                again |= t0 + kBN > pc.common || (missing.x | missing.y | missing.z | missing.w);
+                const bool all = t0 + kBN <= pc.common && !(missing.x | missing.y | missing.z | missing.w);
+                auto hide = [&](float (&x)[32], uint32_t on) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
+                };
+                uint32_t mw[4] = {~0u, ~0u, ~0u, ~0u};     // which of the tokens the row sees
+                if (!all) tile_mask(see, t0, missing, mw);
                 tmem_wait_ld();
+                // The quick form wants a maximum to begin with, in kTame's range.  Units of few rows have few tiles that hide nothing, so
+                // there it takes masks too, and that of 32 tokens to begin with (64 tokens after 4096 to 32768 each: 1249 -> 1007 us);
+                // wide units have many, and a second form in their loop costs more than it gives (0.412 -> 0.424 ms for 2048 tokens after 16384).
+                bool again = kWide && !(all && begun);
+                if (!kWide) {
+                    if (!all) hide(xa, mw[0]);
+                    if (!begun) m = see ? max_of(xa) : INFINITY;
+                }
+                again = again || __any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame));
                 if (!again) {
                     // The weights are formed from the last maximum and stored over the scores unless one is past what
                     // may stand, which their sum tells: no maximum is looked for.
@@ -428,36 +445,44 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                             p[k] = pack_bf16x2(e.x, e.y);
                         }
                     };
-                    float2 sum = make_float2(0.f, 0.f);
-                    uint32_t p[4][16];
-                    tmem_ld32(tS + 32, xb);
-                    weigh(xa, sum, p[0]);
-                    tmem_wait_ld();
-                    tmem_ld32(tS + 64, xa);
-                    weigh(xb, sum, p[1]);
-                    tmem_wait_ld();
-                    tmem_ld32(tS + 96, xb);
-                    weigh(xa, sum, p[2]);
-                    tmem_wait_ld();
-                    weigh(xb, sum, p[3]);
-                    again = __any_sync(0xffffffffu, sum.x + sum.y > kMostSum);
-                    if (!again) {
+                    auto form = [&](auto masked) {
+                        float2 sum = make_float2(0.f, 0.f);
+                        uint32_t p[4][16];
+                        tmem_ld32(tS + 32, xb);
+                        weigh(xa, sum, p[0]);
+                        tmem_wait_ld();
+                        tmem_ld32(tS + 64, xa);
+                        if (masked) hide(xb, mw[1]);
+                        weigh(xb, sum, p[1]);
+                        tmem_wait_ld();
+                        tmem_ld32(tS + 96, xb);
+                        if (masked) hide(xa, mw[2]);
+                        weigh(xa, sum, p[2]);
+                        tmem_wait_ld();
+                        if (masked) hide(xb, mw[3]);
+                        weigh(xb, sum, p[3]);
+                        again = __any_sync(0xffffffffu, sum.x + sum.y > kMostSum);
+                        if (!again) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
-                        l += sum.x + sum.y;
+                            for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
+                            l += sum.x + sum.y;
+                        }
+                    };
+                    if constexpr (kWide) {
+                        form(std::false_type());
+                    } else {
+                        if (all) form(std::false_type());
+                        else form(std::true_type());
                     }
                 }
                 if (again) {
                     // masks, a first maximum, or one that has grown or is out of kTame's range: the maximum first, then the weights
                     // (word c's go to columns 16 c, over scores that have been read)
-                    uint32_t mw[4];                 // which of the tokens the row sees
-                    tile_mask(see, t0, missing, mw);
+                    if (!begun) m = see ? -INFINITY : INFINITY;
                     auto read = [&](int c, float (&x)[32]) {
                         tmem_ld32(tS + 32 * c, x);
                         tmem_wait_ld();
-                        const uint32_t on = c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
+                        hide(x, c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3]);
                     };
                     float top = -INFINITY, x[32];
 #pragma unroll 1
