@@ -29,7 +29,8 @@ using attn::Shape;
 // Tokens that a sequence may have: positions are 32-bit, and the copies number a little past the last tile.
 constexpr int kMostTokens = 0x7fffffff - 8191;
 constexpr int kMaxWaves = 8;
-// Bytes of keys and values that the CTAs may be at work on together, and the least tiles to a range of several waves.
+// Bytes of keys and values that the CTAs may be at work on together (24, 48 and 96 MB: 3.03, 3.03, 3.32 ms for 2048 tokens after 131072;
+// 4.29, 4.29, 4.25 for 12 sequences after up to 16384), and the least tiles to a range of several waves.
 constexpr float kResident = 48e6f;
 constexpr int kLeastTiles = 24;
 
