@@ -252,3 +252,32 @@ def test_one_chunk_equals_its_chain_in_the_tree_attention(cuda_lib, D):
     b = cuda_lib.tree_attention(q.view(2, 40, 8, D).cuda(), dev[:, 0], dev[:, 1], table.cuda(), ctx.cuda(), chain).cpu().double()
     _, bound, _ = R.chunk_attention(q, kv[:, 0], kv[:, 1], table, ctx, cu, D ** -0.5)
     assert ((a - b.view(80, 8, D)).abs() <= 2 * bound).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_two_streams_at_once(cuda_lib, dtype):
+    """Calls of different shapes on two streams, each with its own workspace; every result is that of the call alone."""
+    xs = [[t.cuda() for t in _make([300, 0, 77], [200, 513, 1], 8, 2, 128, dtype, ps=16, seed=1)],
+          [t.cuda() for t in _make([50, 900], [1, 1], 6, 2, 64, dtype, ps=20, seed=2)]]
+    call = lambda x: cuda_lib.chunk_attention(x[0], x[1][:, 0], x[1][:, 1], *x[2:])
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(8):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, call(xs[k])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want[k]) for k, out in got)
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def test_several_waves(cuda_lib):
+    """Keys and values past what the ranges of one wave may share, read by several blocks: the line is cut in two waves (the
+    workspace holds as many ranges), and units cross the ranges of both."""
+    ctx, new, H, Hk, D, ps = 50000, 300, 16, 4, 128, 64
+    x = _make([ctx], [new], H, Hk, D, torch.bfloat16, ps=ps, seed=5, poison=False)
+    a = _check(cuda_lib, *x)
+    assert torch.equal(a, _run(cuda_lib, *x, scale=D ** -0.5))
+    desc = lambda pages: cuda_lib.make_chunk_attention_desc(1, new, H, Hk, D, cuda_lib.KDA_BF16, pages, ps, x[2].shape[1], 0.1, ps * Hk * D, ps * Hk * D)
+    assert cuda_lib.chunk_attention_workspace_bytes(desc(x[1].shape[0])) == 2 * cuda_lib.chunk_attention_workspace_bytes(desc(100))

@@ -301,3 +301,56 @@ def test_upkeep_in_graphs_and_on_another_stream(cuda_lib):
     side.synchronize()
     assert o2.tolist() == h and b2.tolist() == h2 and f2.tolist()[:n2.item()] == free2
     assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def test_releases_of_large_pools_in_graphs_and_on_two_streams(cuda_lib):
+    """The form with a barrier of the whole grid: captured and replayed, then two calls on two streams at once."""
+    P, cols, rows = 50000, 700, 60
+    r = np.random.default_rng(3)
+    ids = r.permutation(P).astype(np.int32)
+    tables = [_gpu(ids[:rows * cols].reshape(rows, cols)), _gpu(ids[-rows * cols:].reshape(rows, cols))]
+    keep, held = _gpu([0 if i % 4 else 320 * 16 for i in range(rows)]), _gpu([cols] * rows)
+    want = [np.sort(np.concatenate([t[i, (0 if i % 4 else 320):] for i in range(rows)])) for t in (x.cpu().numpy() for x in tables)]
+    shares = torch.zeros(P, dtype=I32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, freed, n = cuda_lib.page_release(keep, held, tables[0], shares, page_size=16)
+    for _ in range(2):
+        freed.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert n.item() == len(want[0]) and np.array_equal(freed.cpu().numpy()[:n.item()], want[0]) and (freed[n.item():] == -1).all() and not shares.any()
+        assert h.tolist() == [0 if i % 4 else 320 for i in range(rows)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, cuda_lib.page_release(keep, held, tables[k], torch.zeros(P, dtype=I32, device="cuda"), page_size=16)))
+    torch.cuda.synchronize()
+    for k, (_, freed, n) in got:
+        assert n.item() == len(want[k]) and np.array_equal(freed.cpu().numpy()[:n.item()], want[k])
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def test_forks_and_copies_on_two_streams(cuda_lib):
+    """Two tables and caches at once; each call's shared memory and outputs are its own."""
+    r = np.random.default_rng(8)
+    cases = []
+    for k in range(2):
+        held = [5, 0, 0, 0]
+        table, shares, free = _rows(r, 4, 6, 8, held, spare=9)
+        cases.append((table, shares, free, held, _cache(3, len(shares), 8, 2, 64, torch.bfloat16, seed=k)))
+    streams, done = [torch.cuda.Stream() for _ in range(2)], []
+    for (table, shares, free, held, cache), s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            t, sh, c = _gpu(table), _gpu(shares), cache.cuda()
+            out, copies, taken = cuda_lib.page_fork(_gpu([0, 0, 0]), _gpu([1, 3, 2]), _gpu([33, 8, 39]), _gpu(held), t, sh, _gpu(free), page_size=8)
+            cuda_lib.cache_copy(copies, c[:, :, 0], c[:, :, 1])
+            done.append((out, copies, t, sh, c))
+    torch.cuda.synchronize()
+    for (table, shares, free, held, cache), (out, copies, t, sh, c) in zip(cases, done):
+        h, tab, want, cop, _, bad = R.page_fork([0, 0, 0], [1, 3, 2], [33, 8, 39], held, table, shares, free, 8)
+        assert not bad and out.tolist() == h and copies.tolist() == [list(x) for x in cop] and np.array_equal(t.cpu().numpy(), tab) and sh.tolist() == list(want)
+        assert torch.equal(c.cpu(), R.cache_copy(cop, cache, 8))
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
