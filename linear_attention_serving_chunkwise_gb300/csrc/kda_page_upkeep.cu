@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(PageForkArgs a)
 //      are exchanged, each warp writes its own behind those of the warps before it.
 // Integer sums only, and no order of arrival shows in the outputs.
 // One CTA for what it does in a few microseconds, else a cooperative grid: see kAlonePages.  Bound: latency, of the reads and
-// of four grid barriers: 2048 rows in a pool of 600000 pages 37 us (63 us in one cluster of 16 CTAs).
+// of four grid barriers: 2048 rows in a pool of 600000 pages 18 us; a launch for each step, the last one a cluster of 16 CTAs, 27.
 constexpr int kReleaseThreads = 1024, kReleaseWarps = kReleaseThreads / 32, kReleaseCtas = 152;
 // One CTA alone up to these (GPU time): 4096 pages, 16 rows 8.4 us (a grid 13.9); 16384 pages, 64 rows of 128 14.0 (12.4), 512 rows
-// 32.9 (14.4); 600000 pages, 2048 rows of 512 315 (32.8).
+// 32.9 (12.7); 600000 pages, 2048 rows of 512 315 (18.6).
 constexpr int kAlonePages = 8192;
 constexpr long long kAloneEntries = 8192;
 
@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
     }
     for (long long i = total + (long long)cta * kReleaseThreads + t; i < a.num_pages; i += threads) a.freed[i] = -1;
     if (all_t == 0) a.num_freed[0] = total;
-    if (bad) report_status(a.status, kDevBadSeqlens);
+    // (one thread of a CTA reports: 150 thousand on one word took 20 us)
+    if (__syncthreads_or(bad) && t == 0) report_status(a.status, kDevBadSeqlens);
 }
 
 }  // namespace
