@@ -5,11 +5,9 @@
 // The query rows of a block of tokens -- tokens x the G heads of a cache head -- fill the 128 lanes of an
 // accumulator: S = Q K^T per tile of 128 tokens, the weights overwrite half of S in tensor
 // memory as the bf16 A operand of O += P V, and O stays in tensor memory for the whole piece.  Two
-// streams of S and O share the tensor core, so that one stream's softmax runs under the
-// other's products:
-//     wide     they take 128 rows each of a 256-row unit, and every tile serves both;
-//     narrow   (chunks of 128 rows at most, on average) the streams take the tiles in turn over the same rows, and
-//              their two parts are joined in the epilogue.
+// streams of S and O, of 128 rows each, share the tensor core and every tile, so that one stream's softmax runs under the
+// other's products.  (Units of 128 rows, whose tiles the streams take in turn, lose where there is work: 32 single tokens after 8192 252 us
+// instead of 214, 40 tokens 537 instead of 236; for 129 tokens after none they win, 17.7 us instead of 20.5.)
 // A row's maximum is set anew, and O multiplied, only when its weights of a tile sum to more than 2^15 (until then no
 // weight is more, which bf16 and the fp32 sums hold as well).
 //
@@ -38,8 +36,6 @@
 // of range are zero in shared memory.  The values of the block's own tokens may be seen by some rows only, so
 // non-finite ones are replaced by zero in the tile and added back in the epilogue of the
 // rows that see the token (a positive weight times infinity or NaN is itself).
-#include <type_traits>
-
 #include "kda_attn_tc.cuh"
 #include "kda_chunk_attn.cuh"
 
@@ -48,7 +44,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kBN = kTileTokens;
+constexpr int kBN = kTileTokens, kBM = 256;
 constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmaxThreads + kProducerThreads + 128;
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads start with 128 each
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
@@ -83,14 +79,13 @@ struct Walk {
     }
 };
 
-template <int D, bool kWide>
+template <int D>
 struct Layout {
     static constexpr int kTile = kBN * D * 2;                   // bytes of a K or V tile, and of 128 rows of Q
-    static constexpr int kQ = kTile * (kWide ? 2 : 1);
+    static constexpr int kQ = 2 * kTile;
     static constexpr int kSlots = D == 128 ? 5 : 10;            // ring: K and V tiles in turn
     static constexpr int kLag = kSlots - 2;                     // gathered: slots in flight before the oldest is waited for
-    static constexpr int kStats = kQ + kSlots * kTile;          // streams in turn: their maxima and sums, by piece parity
-    static constexpr int kShared = kStats + (kWide ? 0 : 2 * 2 * 2 * 128 * 4);
+    static constexpr int kShared = kQ + kSlots * kTile;
     static constexpr int kBytes = kShared + (int)sizeof(Shared);
     static constexpr uint32_t kColS = 0, kColO = 256;           // stream w: S at 128 w, O at 256 + D w
     static_assert(kBytes <= 232448, "shared memory");
@@ -100,11 +95,11 @@ struct Layout {
 // By TMA.  Warp 0 of the four issues the boxes, a lane to a box; a V tile with tokens that not
 // all rows see is handed over by the other three once they have cleaned it.  A tile with tokens that have no
 // page passes through registers, by all four.
-template <int D, bool kWide>
+template <int D>
 __device__ __forceinline__ void produce_boxes(const ChunkAttnArgs& a, const Shape& sh, const Maps& maps, int waves, Shared& sm,
                                               uint8_t* base, int t)
 {
-    using L = Layout<D, kWide>;
+    using L = Layout<D>;
     const int lane = t & 31, w = t >> 5, box = maps.box_rows;
     Waiter wait{a.status};
     Walk walk(sm, waves);
@@ -180,10 +175,10 @@ __device__ __forceinline__ void produce_boxes(const ChunkAttnArgs& a, const Shap
 }
 
 // By 16-byte asynchronous copies, all four warps.
-template <int D, bool kWide>
+template <int D>
 __device__ __forceinline__ void produce_gather(const ChunkAttnArgs& a, const Shape& sh, int waves, Shared& sm, uint8_t* base, int t)
 {
-    using L = Layout<D, kWide>;
+    using L = Layout<D>;
     constexpr int CH = D / 8, RPI = 32 / CH;
     const int lane = t & 31, w = t >> 5;
     // (a cache without pages may be a null pointer: copies of no bytes then start at q)
@@ -254,10 +249,10 @@ __device__ __forceinline__ void produce_gather(const ChunkAttnArgs& a, const Sha
 // they are (no row's result depends on another row); scale 0 is a zero Q (every score is then 0).
 constexpr int kQueryThreads = 96;
 
-template <int D, bool kWide>
+template <int D>
 __device__ __forceinline__ void query(const ChunkAttnArgs& a, const Shape& sh, int waves, Shared& sm, uint8_t* base, int t)
 {
-    using L = Layout<D, kWide>;
+    using L = Layout<D>;
     constexpr int CH = D / 8, STEP = kQueryThreads / CH;   // chunks of a row; rows copied at once
     const int G = a.heads / a.kv_heads, c = t % CH;
     const int step_token = STEP / G, step_head = STEP - step_token * G;
@@ -288,10 +283,10 @@ __device__ __forceinline__ void query(const ChunkAttnArgs& a, const Shape& sh, i
 }
 
 // ------------------------------------------------------------------ the products
-template <int D, bool kWide>
+template <int D>
 __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh, int waves, Shared& sm, uint8_t* base)
 {
-    using L = Layout<D, kWide>;
+    using L = Layout<D>;
     Waiter wait{a.status};
     Walk walk(sm, waves);
     chunk::Piece pc;
@@ -305,17 +300,17 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
     };
     uint32_t piece = 0;
     for (; walk.next(a, sh, pc); ++piece) {
-        const int tiles = pc.last - pc.first, items = kWide ? 2 * tiles : tiles;
+        const int tiles = pc.last - pc.first, items = 2 * tiles;
         wait(&sm.q_full, piece & 1);
-        // item i: stream i % 2; its tile is i (streams in turn) or i / 2 (each tile for both)
+        // item i: stream i % 2, tile i / 2
         auto next_k = [&](int w) {                  // the slot of the item's keys, once they are there
             const uint32_t s = ks_;
-            if (!kWide || w == 0) wait(&sm.kv_full[s], kp);
-            if (!kWide || w == 1) advance(ks_, kp);
+            if (w == 0) wait(&sm.kv_full[s], kp);
+            else advance(ks_, kp);
             return s;
         };
         auto scores = [&](int w, uint32_t s) {
-            const uint64_t qd = kmajor_base(q0 + (kWide ? w * L::kTile : 0)), kd = kmajor_base(ring + s * L::kTile);
+            const uint64_t qd = kmajor_base(q0 + w * L::kTile), kd = kmajor_base(ring + s * L::kTile);
             if (wait.alive) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
@@ -324,22 +319,21 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
             umma_commit(&sm.s_full[w]);
         };
         auto scored = [&](int i, int w, uint32_t s) {
-            if (!kWide || w == 1) umma_commit(&sm.kv_empty[s]);
+            if (w == 1) umma_commit(&sm.kv_empty[s]);
             if (i == items - 1) umma_commit(&sm.q_empty);
         };
         // The values of item i, and the stream's next scores right behind them: all that they need is waited for before the
-        // weights are, and slots are given back after both.  (Not the next keys where the streams take the tiles in turn: they are
-        // four slots on, and few rows are bound by the loads: 1317 -> 1249 us for 64 tokens after 4096 to 32768 each.)
+        // weights are, and slots are given back after both.
         auto step = [&](int i, int w) {
-            const bool last = !kWide || w == 1, more = i + 2 < items;
+            const bool more = i + 2 < items;
             const uint32_t s = vs_;
-            if (!kWide || w == 0) wait(&sm.kv_full[s], vp);
-            if (last) advance(vs_, vp);
+            if (w == 0) wait(&sm.kv_full[s], vp);
+            else advance(vs_, vp);
             if (i == w) {                           // the stream's first products of the piece overwrite O
                 if (pieces[w]) wait(&sm.o_free[w], (pieces[w] - 1) & 1);
                 ++pieces[w];
             }
-            uint32_t k = kWide && more ? next_k(w) : 0;
+            const uint32_t k = more ? next_k(w) : 0;
             const uint64_t vd = mnmajor_base(ring + s * L::kTile, kBN);
             wait(&sm.p_full[w], used[w] & 1);
             ++used[w];
@@ -349,24 +343,23 @@ __device__ __forceinline__ void multiply(const ChunkAttnArgs& a, const Shape& sh
                 for (int ks = 0; ks < kBN / 16; ++ks)
                     umma_bf16_tmem_a(tm + L::kColO + D * w, tm + L::kColS + 128 * w + 8 * ks, desc_off(vd, mnmajor_off(ks)), id_o, i > 1 || ks > 0);
             }
-            if (!kWide && more) k = next_k(w);
             if (more) scores(w, k);
             else umma_commit(&sm.o_done[w]);
-            if (last) umma_commit(&sm.kv_empty[s]);
+            if (w == 1) umma_commit(&sm.kv_empty[s]);
             if (more) scored(i + 2, w, k);
         };
         // (one thread for all of it: with the whole warp in the waits and a thread elected for each
         // group of products their issue took 3000 cycles a tile; with a thread to each stream the streams' products mix, and each
         // waits longer for its own: 0.42 -> 0.50 ms for 2048 tokens after 16384)
-        for (int w = 0; w < 2 && w < items; ++w) {
+        for (int w = 0; w < 2; ++w) {
             const uint32_t k = next_k(w);
             tc_fence_after_sync();
             scores(w, k);
             scored(w, w, k);
         }
-        for (int i = 0; i < items; i += 2) {        // both streams in turn
+        for (int i = 0; i < items; i += 2) {
             step(i, 0);
-            if (i + 1 < items) step(i + 1, 1);
+            step(i + 1, 1);
         }
     }
     for (int w = 0; w < 2; ++w)                     // no product or commit is in flight after this
@@ -386,26 +379,25 @@ __device__ __forceinline__ void tile_mask(int sees, int t0, uint4 lost, uint32_t
     }
 }
 
-template <int D, bool kWide>
-__device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh, int waves, Shared& sm, uint8_t* base, int t)
+template <int D>
+__device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh, int waves, Shared& sm, int t)
 {
-    using L = Layout<D, kWide>;
-    float* stats = reinterpret_cast<float*>(base + L::kStats);        // [stream][m, l][128]
+    using L = Layout<D>;
     const int lane = t & 31, warp = t >> 5, w = t >> 7, r = t & 127;   // stream and lane of tensor memory
     const int G = a.heads / a.kv_heads;
     const uint32_t quad = 32 * (warp & 3);                            // the lanes this warp reaches
-    const uint32_t tS = tmem_addr(sm.tmem, quad, L::kColS + 128 * w), tO = tmem_addr(sm.tmem, quad, L::kColO);
+    const uint32_t tS = tmem_addr(sm.tmem, quad, L::kColS + 128 * w), tO = tmem_addr(sm.tmem, quad, L::kColO + D * w);
     const float sc = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;  // scores in powers of two
     const float2 sc2 = make_float2(sc, sc);
     Waiter wait{a.status};
     Walk walk(sm, waves);
     chunk::Piece pc;
-    uint32_t used = 0, done = 0, pieces[2] = {0, 0};   // items of this stream, tiles, pieces of each stream so far
+    uint32_t used = 0, done = 0;                       // items of this stream, tiles so far
     for (uint32_t piece = 0; walk.next(a, sh, pc); ++piece) {
         const int tiles = pc.last - pc.first;
         if (!pc.ok && t == 0) report_status(a.status, kDevBadSeqlens);
         // this thread's row of the unit, its token of the block, and how many tokens it sees
-        const int rl = (kWide ? 128 * w : 0) + r, token = rl / G;
+        const int rl = 128 * w + r, token = rl / G;
         const bool mine = token < pc.tokens;
         const int see = mine && pc.ok ? pc.common + token : 0;
         const bool busy = __any_sync(0xffffffffu, see != 0);
@@ -413,7 +405,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
         float m = see ? -INFINITY : INFINITY, l = 0.f;
         bool begun = false;
 
-        for (int i = kWide ? 0 : w; i < tiles; i += kWide ? 1 : 2) {
+        for (int i = 0; i < tiles; ++i) {
             const int t0 = (pc.first + i) * kBN;
             wait(&sm.s_full[w], used & 1);
             ++used;
@@ -424,22 +416,10 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                 tmem_ld32(tS, xa);
                 const uint4 missing = *reinterpret_cast<const uint4*>(sm.missing[(done + i) & 7]);
                 const bool all = t0 + kBN <= pc.common && !(missing.x | missing.y | missing.z | missing.w);
-                auto hide = [&](float (&x)[32], uint32_t on) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
-                };
-                uint32_t mw[4] = {~0u, ~0u, ~0u, ~0u};     // which of the tokens the row sees
-                if (!all) tile_mask(see, t0, missing, mw);
                 tmem_wait_ld();
-                // The quick form wants a maximum to begin with, in kTame's range.  Units of few rows have few tiles that hide nothing, so
-                // there it takes masks too, and that of 32 tokens to begin with (64 tokens after 4096 to 32768 each: 1249 -> 1007 us);
-                // wide units have many, and a second form in their loop costs more than it gives (0.412 -> 0.424 ms for 2048 tokens after 16384).
-                bool again = kWide && !(all && begun);
-                if (!kWide) {
-                    if (!all) hide(xa, mw[0]);
-                    if (!begun) m = see ? max_of(xa) : INFINITY;
-                }
-                again = again || __any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame));
+                // The quick form wants a maximum to begin with, in kTame's range, and no masks: a second form with masks costs the
+                // loop more than it gives (0.412 -> 0.424 ms for 2048 tokens after 16384).
+                bool again = !all || !begun || __any_sync(0xffffffffu, see && !(fabsf(m) * sc <= kTame));
                 if (!again) {
                     // The weights are formed from the last maximum and stored over the scores unless one is past what
                     // may stand, which their sum tells: no maximum is looked for.
@@ -455,44 +435,36 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                             p[k] = pack_bf16x2(e.x, e.y);
                         }
                     };
-                    auto form = [&](auto masked) {
-                        float2 sum = make_float2(0.f, 0.f);
-                        uint32_t p[4][16];
-                        tmem_ld32(tS + 32, xb);
-                        weigh(xa, sum, p[0]);
-                        tmem_wait_ld();
-                        tmem_ld32(tS + 64, xa);
-                        if (masked) hide(xb, mw[1]);
-                        weigh(xb, sum, p[1]);
-                        tmem_wait_ld();
-                        tmem_ld32(tS + 96, xb);
-                        if (masked) hide(xa, mw[2]);
-                        weigh(xa, sum, p[2]);
-                        tmem_wait_ld();
-                        if (masked) hide(xb, mw[3]);
-                        weigh(xb, sum, p[3]);
-                        again = __any_sync(0xffffffffu, sum.x + sum.y > kMostSum);
-                        if (!again) {
+                    float2 sum = make_float2(0.f, 0.f);
+                    uint32_t p[4][16];
+                    tmem_ld32(tS + 32, xb);
+                    weigh(xa, sum, p[0]);
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 64, xa);
+                    weigh(xb, sum, p[1]);
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 96, xb);
+                    weigh(xa, sum, p[2]);
+                    tmem_wait_ld();
+                    weigh(xb, sum, p[3]);
+                    again = __any_sync(0xffffffffu, sum.x + sum.y > kMostSum);
+                    if (!again) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
-                            l += sum.x + sum.y;
-                        }
-                    };
-                    if constexpr (kWide) {
-                        form(std::false_type());
-                    } else {
-                        if (all) form(std::false_type());
-                        else form(std::true_type());
+                        for (int c = 0; c < 4; ++c) tmem_st16u(tS + 16 * c, p[c]);
+                        l += sum.x + sum.y;
                     }
                 }
                 if (again) {
                     // masks, a first maximum, or one that has grown or is out of kTame's range: the maximum first, then the weights
                     // (word c's go to columns 16 c, over scores that have been read)
-                    if (!begun) m = see ? -INFINITY : INFINITY;
+                    uint32_t mw[4];                 // which of the tokens the row sees
+                    tile_mask(see, t0, missing, mw);
                     auto read = [&](int c, float (&x)[32]) {
                         tmem_ld32(tS + 32 * c, x);
                         tmem_wait_ld();
-                        hide(x, c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3]);
+                        const uint32_t on = c == 0 ? mw[0] : c == 1 ? mw[1] : c == 2 ? mw[2] : mw[3];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = on >> k & 1 ? x[k] : -INFINITY;
                     };
                     float top = -INFINITY, x[32];
 #pragma unroll 1
@@ -506,11 +478,11 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                     if (begun && __any_sync(0xffffffffu, grow)) {      // (S is ready: the stream's last products into O are done)
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
-                            tmem_ld32(tO + D * w + c, x);
+                            tmem_ld32(tO + c, x);
                             tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 32; ++k) x[k] *= f;
-                            tmem_st32(tO + D * w + c, x);
+                            tmem_st32(tO + c, x);
                         }
                     }
                     if (grow) m = top;
@@ -546,35 +518,17 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
             m = -INFINITY;
             l = 0.f;
         }
-        const bool two = !kWide && tiles > 1;       // stream 1 has a part of the same rows
-        float* st = stats + (kWide ? 0 : 512 * (piece & 1));
-        if (!kWide) {
-            st[256 * w + r] = m;
-            st[256 * w + 128 + r] = l;
-        }
-        for (int k = 0; k < 2; ++k)                 // the streams this thread reads: its own, or both of the piece
-            if (kWide ? k == w : k == 0 || two) wait(&sm.o_done[k], pieces[k]++ & 1);
+        wait(&sm.o_done[w], piece & 1);
         __syncwarp();
         tc_fence_after_sync();
-        if (!kWide) bar_sync(1, kSoftmaxThreads);
         bool bad = false;                           // non-finite values among the block's own tokens
         if (pc.last * kBN > pc.common) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) bad |= *const_cast<volatile uint32_t*>(&sm.bad[piece & 7][k]) != 0;
         }
-        // this thread's columns [c0, c1) of the row: stream 1's part is joined when it has one
-        const int c0 = kWide ? 0 : w * (D / 2), c1 = kWide ? D : c0 + D / 2;
-        float f0 = 1.f, f1 = 0.f;
-        if (!kWide) {
-            const float m0 = st[r], m1 = two ? st[256 + r] : -INFINITY, l0 = st[128 + r], l1 = two ? st[384 + r] : 0.f;
-            m = fmaxf(m0, m1);
-            f0 = m0 == -INFINITY ? 0.f : ex2((m0 - m) * sc);
-            f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * sc);
-            l = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
-        }
         const float norm = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
-        if (mine && !pc.whole() && c0 == 0) {
+        if (mine && !pc.whole()) {
             ws[rl] = m == -INFINITY ? m : m * sc;
             ws[sh.BM + rl] = l;
         }
@@ -583,23 +537,12 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
         int orows[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) orows[k] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + k);
-        for (int c = c0; c < c1; c += 32) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
             float o[32];
             if (busy) {
-                tmem_ld32(tO + (kWide ? D * w : 0) + c, o);
+                tmem_ld32(tO + c, o);
                 tmem_wait_ld();
-                if (!kWide) {
-                    if (two) {
-                        float o1[32];
-                        tmem_ld32(tO + D + c, o1);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + o1[k] * f1;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f0;
-                    }
-                }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = l == 0.f ? 0.f : o[k] * norm;
             } else {
@@ -646,18 +589,15 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
-            if (kWide || w == 0 || two) mbar_arrive(&sm.o_free[w]);
-            if (!kWide && (w == 1 || two)) mbar_arrive(&sm.o_free[w ^ 1]);
-        }
+        if (lane == 0) mbar_arrive(&sm.o_free[w]);
     }
     wait.finish();
 }
 
-template <int D, bool kWide, bool kBoxes>
+template <int D, bool kBoxes>
 __global__ void __launch_bounds__(kThreads, 1) chunk_attn_tc_kernel(ChunkAttnArgs a, Shape sh, const __grid_constant__ Maps maps)
 {
-    using L = Layout<D, kWide>;
+    using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t base[];   // all of it: the swizzled tiles start at 0
     Shared& sm = *reinterpret_cast<Shared*>(base + L::kShared);
     const int t = threadIdx.x, warp = t >> 5;
@@ -682,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_tc_kernel(ChunkAttnArg
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_done[i], 1);
-            mbar_init(&sm.o_free[i], kWide ? 4 : 8);
+            mbar_init(&sm.o_free[i], 4);
         }
         mbar_init(&sm.q_full, kQueryThreads);
         mbar_init(&sm.q_empty, 1);
@@ -694,16 +634,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_tc_kernel(ChunkAttnArg
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax<D, kWide>(a, sh, waves, sm, base, t);
+        softmax<D>(a, sh, waves, sm, t);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < 12) {
-            if constexpr (kBoxes) produce_boxes<D, kWide>(a, sh, maps, waves, sm, base, t - kSoftmaxThreads);
-            else produce_gather<D, kWide>(a, sh, waves, sm, base, t - kSoftmaxThreads);
+            if constexpr (kBoxes) produce_boxes<D>(a, sh, maps, waves, sm, base, t - kSoftmaxThreads);
+            else produce_gather<D>(a, sh, waves, sm, base, t - kSoftmaxThreads);
         } else if (warp == 12) {
-            if (elect_one()) multiply<D, kWide>(a, sh, waves, sm, base);
+            if (elect_one()) multiply<D>(a, sh, waves, sm, base);
         } else {
-            query<D, kWide>(a, sh, waves, sm, base, t - 13 * 32);
+            query<D>(a, sh, waves, sm, base, t - 13 * 32);
         }
     }
     __syncwarp();
@@ -713,27 +653,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_tc_kernel(ChunkAttnArg
     if (warp == 12) tmem_dealloc(sm.tmem, 512);
 }
 
-// Units of 128 rows where the chunks have no more on average, of 256 otherwise: every tile is then read and turned into operands
-// for twice the rows.
-bool wide_rows(const ChunkAttnArgs& a) { return (long long)a.tokens * (a.heads / a.kv_heads) > 128ll * a.batch; }
-
 // Several waves (see kda_chunk_attn.cuh) where the cache is larger than what they keep together, and blocks enough
 // for it: a unit is cut in 16 parts at most.
 Shape shape_of(const ChunkAttnArgs& a)
 {
-    const bool wide = wide_rows(a);
-    const int BM = wide ? 256 : 128, TB = BM / (a.heads / a.kv_heads);
+    const int TB = kBM / (a.heads / a.kv_heads);
     const double cache = 4. * a.num_pages * a.page_size * a.kv_heads * a.dim, units = ((double)a.tokens / TB + a.batch) * a.kv_heads;
     int waves = 1;
     while (waves < chunk::kMaxWaves && waves * chunk::kResident < cache && 2 * waves * kCtas <= 16 * units) waves *= 2;
-    return {BM, kBN, kCtas * waves, kHead};
+    return {kBM, kBN, kCtas * waves, kHead};
 }
 
-template <int D, bool kWide, bool kBoxes>
+template <int D, bool kBoxes>
 cudaError_t launch(const ChunkAttnArgs& a, cudaStream_t stream)
 {
-    using L = Layout<D, kWide>;
-    const auto kernel = chunk_attn_tc_kernel<D, kWide, kBoxes>;
+    using L = Layout<D>;
+    const auto kernel = chunk_attn_tc_kernel<D, kBoxes>;
     const Shape sh = shape_of(a);
     Maps maps = {};
     if (kBoxes) {
@@ -747,15 +682,13 @@ cudaError_t launch(const ChunkAttnArgs& a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     kernel<<<kCtas, kThreads, L::kBytes, stream>>>(a, sh, maps);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return attn::launch_join<__nv_bfloat16, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, sh.BM, stream);
+    return attn::launch_join<__nv_bfloat16, D>({a.workspace, a.out, a.heads, a.kv_heads}, sh, kBM, stream);
 }
 
 template <int D>
 cudaError_t launch_dim(const ChunkAttnArgs& a, cudaStream_t stream)
 {
-    const bool wide = wide_rows(a);
-    if (in_boxes(a)) return wide ? launch<D, true, true>(a, stream) : launch<D, false, true>(a, stream);
-    return wide ? launch<D, true, false>(a, stream) : launch<D, false, false>(a, stream);
+    return in_boxes(a) ? launch<D, true>(a, stream) : launch<D, false>(a, stream);
 }
 
 }  // namespace

@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(NormRotateArgs
 template <typename T, int D>
 cudaError_t launch(const NormRotateArgs& a, cudaStream_t stream)
 {
-    // eight tokens to a CTA once that fills the GPU, one before
-    const int per = a.tokens >= 152 * kMostTokens ? kMostTokens : 1, grid = (a.tokens + per - 1) / per;
+    // Fewer warps to a token as tokens fill the GPU (1, 2, 4, 8 tokens to a CTA; us, 32 and 8 heads): 256 tokens 6.4, 6.4, 8.4, 10.5;
+    // 608 10.5, 8.4, 8.4, 10.4; 1024 14.6, 12.5, 10.5, 10.5; 2432 24.7, 16.7, 16.6, 14.6; 32768 291, 187, 146, 140.
+    const int per = a.tokens <= 304 ? 1 : a.tokens <= 608 ? 2 : a.tokens <= 1216 ? 4 : kMostTokens, grid = (a.tokens - 1) / per + 1;
     if (a.interleaved) norm_rotate_kernel<T, D, true><<<grid, kThreads, 0, stream>>>(a, per);
     else norm_rotate_kernel<T, D, false><<<grid, kThreads, 0, stream>>>(a, per);
     return cudaGetLastError();
