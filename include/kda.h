@@ -598,7 +598,7 @@ size_t kda_chunk_attention_workspace_bytes(const kda_chunk_attention_desc* desc)
  *   out           [T, Hq, dim] dtype; rows from cu_seqlens[B] on are left as they are
  *   workspace     kda_chunk_attention_workspace_bytes(desc) bytes (bf16, 128 channels: 20 to 324 MB, by the tokens and the cache),
  *                 16-byte aligned, clobbered; two calls in flight at once need two
- * Sequences of a few tokens each are served, but at 0.7 of kda_tree_attention's rate.
+ * Sequences of a few tokens each are served, but at 0.9 of kda_tree_attention's rate.
  * Whatever lies in the cache where a token may not look (behind it, pages of others) does not change its
  * output, NaN included.  A sequence whose context_lens is negative, or with its chunk exceeds its table row or
  * 2^31 - 8192 tokens, gets zeros; a token whose page id is outside [0, num_pages) is left out (a row that has nothing

@@ -8,7 +8,7 @@
 // must not be NaN.
 // Bound: the CUDA cores' issue (6600 warp instructions a tile and warp, 4096 of them multiply-adds, 70 % of the slots used):
 // 5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 201 us, 33 TFLOP/s; 2048 tokens after 2048, 32 heads on
-// 8 1.38 ms (D = 64, 37 TFLOP/s), 2.87 ms (D = 128).  Two multiply-adds at a time (199 us), a second buffer for the tiles (226) and
+// 8 1.33 ms (D = 64, 39 TFLOP/s), 2.79 ms (D = 128).  Two multiply-adds at a time (199 us), a second buffer for the tiles (226) and
 // other rows to a thread (216) gave nothing.
 #include "kda_chunk_attn.cuh"
 

@@ -18,17 +18,17 @@
 // Bound, for many rows: not the tensor pipe alone (67 % busy: 2048 of some 2900 cycles a tile of 256 rows x 128 tokens,
 // D = 128) but each stream's chain scores - softmax - values, which the other one's products cover only in part.  The softmax's way
 // from scores to weights takes 1200 cycles, of which 750 form 128 weights a thread, and the products' thread adds waits and commits.
-// 2048 tokens after 131072, 32 heads on 8: 2.95 ms, 1500 TFLOP/s (0.78 of cuBLAS's burst); 12 sequences of 1 to 2048 tokens after
-// up to 16384, 96 heads on 8: 4.10 ms, 1420; a prompt of 8192: 406 us, 1355; 512 after 131072: 740 us, 1490; 16 prompts of
-// 512: 102 us, 337 (a unit of three tiles costs 11 us: its first tile, masks and epilogue); 64 tokens after 4096 to 32768
-// each: 1019 us, 4.9 TB/s (kda_tree_attention is for those); D = 64: 2048 after 131072 2.27 ms, 975 (the same
+// 2048 tokens after 131072, 32 heads on 8: 2.90 to 2.95 ms, 1500 to 1530 TFLOP/s (0.79 of cuBLAS's burst); 12 sequences of 1 to 2048 tokens
+// after up to 16384, 96 heads on 8: 4.05 to 4.10 ms, 1420 to 1440; a prompt of 8192: 399 us, 1380; 512 after 131072: 735 us, 1500; 16
+// prompts of 512: 98 us, 350 (a unit of three tiles costs 11 us: its first tile, masks and epilogue); 64 tokens after 4096 to 32768
+// each: 790 to 810 us, 6.2 TB/s; D = 64: 2048 after 131072 2.2 ms, 1000 (the same
 // softmax for half the products).  In one wave instead of eight the first two took 3.52 and 4.83 ms instead of 3.03 and 4.27;
 // with the weights handed over in two parts 2.99 and 4.37 instead of 3.00 and 4.20.
 //
 // The cache rows come by TMA where the page size is a multiple of 8: a tile is a stack of boxes
 // of 8 to 128 rows (the largest power of two in the page size), and 8 rows are one swizzle
 // atom, so boxes of any pages stack into the tile the products read.  Other page sizes are
-// gathered with 16-byte asynchronous copies, a row to half a warp (2.94 ms by boxes, 4.41 gathered for 2048 after 131072).
+// gathered with 16-byte asynchronous copies, a row to half a warp (2.95 ms by boxes, 4.30 gathered for 2048 after 131072).
 // Every wait is bounded; a thread that gave up goes through the rest of its schedule without
 // waiting and without touching the tensor core, and the status word says so.
 //
@@ -49,7 +49,8 @@ constexpr int kSoftmaxThreads = 256, kProducerThreads = 128, kThreads = kSoftmax
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // a thread; 512 threads start with 128 each
 static_assert(kSoftmaxThreads * kSoftmaxRegs + (kThreads - kSoftmaxThreads) * kOtherRegs <= kThreads * 128, "register split");
 constexpr int kCtas = 152;                          // one to an SM
-constexpr int kHead = 4;                            // a unit's fixed cost (Q, first tile, epilogue), in tiles
+// A unit's fixed cost (Q, first tile, epilogue), in tiles: with 1, 2, 4 and 6 a prompt of 8192 took 477, 443, 399 and 405 us.
+constexpr int kHead = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTame = 4096.f;                     // largest m sc of the form with one operation
 constexpr float kMostSum = 32768.f;                 // most that a row's weights of a tile may sum to before its maximum is set anew
