@@ -596,7 +596,7 @@ size_t kda_chunk_attention_workspace_bytes(const kda_chunk_attention_desc* desc)
  *   k_cache, v_cache, block_table, context_lens   as kda_tree_attention's
  *   cu_seqlens    [B + 1] int32: 0 first, not decreasing, T at most (kda_page_tables' output)
  *   out           [T, Hq, dim] dtype; rows from cu_seqlens[B] on are left as they are
- *   workspace     kda_chunk_attention_workspace_bytes(desc) bytes (bf16, 128 channels: 20 to 324 MB, by the tokens and the cache),
+ *   workspace     kda_chunk_attention_workspace_bytes(desc) bytes (bf16, 128 channels: 40 to 324 MB, by the tokens and the cache),
  *                 16-byte aligned, clobbered; two calls in flight at once need two
  * Sequences of a few tokens each are served, but at 0.9 of kda_tree_attention's rate.
  * Whatever lies in the cache where a token may not look (behind it, pages of others) does not change its
