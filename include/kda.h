@@ -683,7 +683,7 @@ kda_status kda_page_fork(int32_t num_forks, int32_t rows, int32_t table_cols, in
                          int32_t* pages_held_out, int32_t* copies, int32_t* pages_taken, void* stream);
 
 /*
- * kda_page_release -- table rows cut to their first keep_lens tokens (0: given up; at least what is held: untouched).
+ * kda_page_release -- table rows cut to their first keep_lens tokens (0: given up; what the held pages hold, or more: untouched).
  * The pages behind those are given back: each loses a share, and those that no row holds any more are returned.
  *
  *   keep_lens, pages_held  [rows] int32

@@ -186,9 +186,9 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
             bad = true;
         } else {
             const int pages = (int)(((long long)keep + ps - 1) / ps);
-            if (pages < held) {
+            if (pages <= held) {
                 left = pages;
-                if (keep % ps) {
+                if (keep % ps) {       // (inside the last page that is held, too)
                     const int id = a.block_table[(size_t)r * a.table_cols + pages - 1];
                     if (id < 0 || id >= a.num_pages || a.shares[id] > 0) {
                         bad = true;

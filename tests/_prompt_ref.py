@@ -129,7 +129,7 @@ def page_release(keep, held, table, shares, ps):
             bad = True
             continue
         pages = -(-k // ps)
-        if pages >= h:
+        if pages > h:
             continue
         if k % ps:
             last = int(table[r][pages - 1])

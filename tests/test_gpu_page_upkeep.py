@@ -138,6 +138,9 @@ def test_a_page_that_others_hold_is_not_cut(cuda_lib):
     assert _release(cuda_lib, [5, 8, 4], [3, 3, 2], table, shares, 4)        # row 0 inside page 1
     assert not _release(cuda_lib, [9, 8, 5], [3, 3, 2], table, shares, 4)    # inside their own last pages
     assert not _release(cuda_lib, [0, 0, 0], [3, 3, 2], table, shares, 4)
+    table = np.array([[0, 1], [0, 1], [2, 3]], np.int32)                     # inside the last page that is held: no page goes, but what
+    assert _release(cuda_lib, [7, 8, 8], [2, 2, 2], table, [1, 1, 0, 0], 4)  # the row appends there would be row 1's
+    assert not _release(cuda_lib, [8, 9, 7], [2, 2, 2], table, [1, 1, 0, 0], 4)
 
 
 def test_releases_of_bad_rows(cuda_lib):
