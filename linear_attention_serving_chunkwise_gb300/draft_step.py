@@ -97,22 +97,31 @@ class HybridLayers:
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
         """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages
         shared, the last one copied.  The KDA state is that of the parent's whole context, so a shorter child has to replay its
-        tokens into it.  Where the free pages do not reach: RuntimeError, and the children they reach for are forked."""
+        tokens into it.  Where the free pages do not reach, or a child is not empty: RuntimeError, and the other children are forked."""
+        rows, p, c, ps = self.context_lens.numel(), parents.long(), children.long(), self.cache.shape[2]
+        if bool(((p < 0) | (p >= rows) | (c < 0) | (c >= rows)).any()):
+            raise ValueError(f"there are {rows} sequences")
+        empty = self.pages_held[c] == 0
         self.pages_held, copies, taken = page_fork(parents, children, lens, self.pages_held, self.block_table, self.shares, self.free_pages,
-                                                   page_size=self.cache.shape[2])
+                                                   page_size=ps)
         cache_copy(copies, self.cache[:, 0], self.cache[:, 1])
-        p, c, ps = parents.long(), children.long(), self.cache.shape[2]
-        got = self.pages_held[c] == (lens + ps - 1) // ps
+        got = empty & (lens >= 0) & (self.pages_held[c] == (lens + ps - 1) // ps)
         self.state[c] = torch.where(got[:, None, None, None], self.state[p], self.state[c])
         self.context_lens[c] = torch.where(got, lens, self.context_lens[c])
         taken, refused = torch.stack([taken[0], (~got).any().int()]).tolist()
         self.free_pages = self.free_pages[taken:]
         if refused:
-            raise RuntimeError("out of cache pages, or a fork of a row that holds pages")
+            raise RuntimeError("out of cache pages, or forks of what a row does not hold, or into rows that are not empty")
 
     def release(self, keep_lens: torch.Tensor) -> None:
-        """Every sequence's pages behind its first ``keep_lens`` [B] tokens given back (0: the sequence ends, its state becomes zero)."""
-        self.pages_held, freed, count = page_release(keep_lens, self.pages_held, self.block_table, self.shares, page_size=self.cache.shape[2])
+        """Every sequence's pages behind its first ``keep_lens`` [B] tokens given back (0: the sequence ends, its state becomes zero; cut
+        elsewhere, the KDA state stays that of all tokens).  A cut inside a page that others hold: RuntimeError, and nothing changes."""
+        ps = self.cache.shape[2]
+        pages = (keep_lens + ps - 1) // ps
+        last = self.block_table.gather(1, (pages - 1).clamp(0, self.block_table.shape[1] - 1).long()[:, None])[:, 0].clamp_min(0).long()
+        if bool(((keep_lens < 0) | ((keep_lens % ps > 0) & (pages <= self.pages_held) & (self.shares[last] > 0))).any()):
+            raise RuntimeError("a sequence cannot be cut inside a page that others hold")
+        self.pages_held, freed, count = page_release(keep_lens, self.pages_held, self.block_table, self.shares, page_size=ps)
         self.context_lens = torch.minimum(self.context_lens, keep_lens)
         self.state[keep_lens == 0] = 0
         self.free_pages = torch.cat([self.free_pages, freed[:count.item()]])

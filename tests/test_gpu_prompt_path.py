@@ -159,3 +159,29 @@ def test_the_models_forks_go_on_alike(cuda_lib):
     with pytest.raises(RuntimeError):
         m.mem.fork(_i32([0]), _i32([1]), _i32([3]))           # nothing to fork from
     cuda_lib.last_device_status()
+
+
+def test_the_models_memory_refuses_what_would_break_it(cuda_lib):
+    """Rows that do not exist, children that hold pages, cuts inside shared pages: an error, and everything as it was."""
+    m = draft_step.HybridLayers(3, 2, 64, 1, 20, 8, 6)
+    m.reserve(16)                                             # two pages each
+    m.context_lens += 16
+    m.state.normal_()
+    m.release(_i32([16, 0, 16]))
+    m.fork(_i32([0]), _i32([1]), _i32([16]))                  # both pages shared
+    before = [t.clone() for t in (m.pages_held, m.context_lens, m.shares, m.free_pages, m.state)]
+    same = lambda: all(torch.equal(a, b) for a, b in zip(before, (m.pages_held, m.context_lens, m.shares, m.free_pages, m.state)))
+    for parents, children in (([0], [3]), ([-1], [1]), ([7], [1])):
+        with pytest.raises(ValueError):
+            m.fork(_i32(parents), _i32(children), _i32([3]))
+        assert same()
+    with pytest.raises(RuntimeError):
+        m.fork(_i32([0]), _i32([2]), _i32([16]))              # holds as many pages already
+    assert same()
+    for keep in ([13, 16, 16], [5, 0, 0], [16, -1, 16]):
+        with pytest.raises(RuntimeError):
+            m.release(_i32(keep))
+        assert same()
+    m.release(_i32([8, 16, 3]))
+    assert m.context_lens.tolist() == [8, 16, 3] and m.pages_held.tolist() == [1, 2, 1] and m.shares.sum() == 1
+    assert cuda_lib.last_device_status() in (cuda_lib.KDA_OK, cuda_lib.KDA_ERR_INVALID_ARG)
