@@ -11,11 +11,14 @@
 // 8 1.33 ms (D = 64, 39 TFLOP/s), 2.79 ms (D = 128).  Two multiply-adds at a time (199 us), a second buffer for the tiles (226) and
 // other rows to a thread (216) gave nothing.
 #include "kda_chunk_attn.cuh"
+#include "kda_draft_sm100.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 128, kBM = 64, kTM = 8;
+constexpr float kTame = 4096.f;        // largest maximum (in powers of two) of the quick form
+constexpr float kMostSum = 32768.f;    // most that a thread's weights of a tile's row may sum to before the maximum is set anew
 
 template <int D>
 struct Tile {
@@ -113,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                 at[i] = ((size_t)(pos - pg * a.page_size) * a.kv_heads + pc.hk) * D + c;
                 id[i] = pos < pc.seen ? __ldg(a.block_table + (size_t)pc.b * a.table_cols + pg) : -1;
             }
+            bool there = true;        // all of this thread's tokens
 #pragma unroll
             for (int i0 = 0; i0 < kRows; i0 += 4) {
                 float4 k4[4], v4[4];
@@ -131,11 +135,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                     const bool on = p >= 0 && p < a.num_pages;
                     bad |= !on && t0 + j < pc.seen;
                     if (c == 0) s_on[j] = on;
+                    there &= on;
                     *reinterpret_cast<float4*>(sk + j * LD + c) = k4[i];
                     *reinterpret_cast<float4*>(sv + j * LD + c) = v4[i];
                 }
             }
-            __syncthreads();
+            // (every row sees the whole tile)
+            const bool all = __syncthreads_and(there) && t0 + BN <= pc.ctx + pc.tok + 1;
             float s[kTM][TN] = {};
 #pragma unroll 2
             for (int ch = 0; ch < D; ch += 4) {
@@ -150,39 +156,70 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                         s[i][j] = fmaf(q4.x, k4[j].x, fmaf(q4.y, k4[j].y, fmaf(q4.z, k4[j].z, fmaf(q4.w, k4[j].w, s[i][j]))));
                 }
             }
+            // The weights are formed from the last maximum, and stand unless one is past what may, which their sums tell: then, and in
+            // tiles that some rows see in part, the row's maximum first.  (s sc - m in one operation: m's own rounding is a factor
+            // that a row's weights share.)
+            float p[kTM][TN], part[kTM];
+            bool again = !all;
+            if (!again) {
+                bool wild = false;
 #pragma unroll
-            for (int i = 0; i < kTM; ++i) {
-                float top = -INFINITY;
+                for (int i = 0; i < kTM; ++i) {
+                    float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    s[i][j] = s_on[tx + 16 * j] && t0 + tx + 16 * j < seen[i] ? s[i][j] * sc : -INFINITY;
-                    top = fmaxf(top, s[i][j]);
+                    for (int j = 0; j < TN; ++j) {
+                        p[i][j] = ex2(fmaf(s[i][j], sc, -m[i]));
+                        sum += p[i][j];
+                    }
+                    wild |= sum > kMostSum || (seen[i] && !(fabsf(m[i]) <= kTame));
+                    part[i] = sum;
                 }
+                again = __any_sync(0xffffffffu, wild);
+                if (!again) {
 #pragma unroll
-                for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float nm = fmaxf(m[i], top), base = nm == -INFINITY ? 0.f : nm;
-                const float f = exp2f(m[i] - base);
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const float p = exp2f(s[i][j] - base);
-                    sum += p;
-                    sp[(ty * kTM + i) * LP + tx + 16 * j] = p;
+                    for (int i = 0; i < kTM; ++i) l[i] += part[i];
                 }
-#pragma unroll
-                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                l[i] = l[i] * f + sum;
-                m[i] = nm;
-#pragma unroll
-                for (int k = 0; k < CD; ++k) o[i][k] *= f;
             }
+            if (again) {
+#pragma unroll
+                for (int i = 0; i < kTM; ++i) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        s[i][j] = s_on[tx + 16 * j] && t0 + tx + 16 * j < seen[i] ? s[i][j] * sc : -INFINITY;
+                        top = fmaxf(top, s[i][j]);
+                    }
+#pragma unroll
+                    for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float nm = fmaxf(m[i], top), base = nm == -INFINITY ? 0.f : nm;
+                    const float f = exp2f(m[i] - base);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        p[i][j] = exp2f(s[i][j] - base);
+                        sum += p[i][j];
+                    }
+                    l[i] = l[i] * f + sum;           // (of this thread's tokens: the row's are summed at the end)
+                    m[i] = nm;
+#pragma unroll
+                    for (int k = 0; k < CD; ++k) o[i][k] *= f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kTM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) sp[(ty * kTM + i) * LP + tx + 16 * j] = p[i][j];
             __syncwarp();             // a row's weights are written and read by the same half warp
-            if (t0 + BN > pc.ctx + pc.tok + 1) {     // (some rows do not see all of it)
+            if (t0 + BN > pc.ctx + pc.tok + 1) {
                 add_values<D, true>(o, sp + ty * kTM * LP, sv + tx * 4);
             } else {
                 add_values<D, false>(o, sp + ty * kTM * LP, sv + tx * 4);
             }
         }
+#pragma unroll
+        for (int i = 0; i < kTM; ++i)
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
         // the unit is done here, or its part goes to the workspace
         float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
 #pragma unroll
