@@ -6,10 +6,10 @@
 // and sum of the softmax.  A tile's values are zeroed where no row of the unit may see the token (past its last one, a page
 // out of range); in the tiles that only some rows see whole, a weight of 0 is skipped: 0 times whatever lies there
 // must not be NaN.
-// Bound: the CUDA cores' issue (6600 warp instructions a tile and warp, 4096 of them multiply-adds, 70 % of the slots used):
-// 5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 201 us, 33 TFLOP/s; 2048 tokens after 2048, 32 heads on
-// 8 1.33 ms (D = 64, 39 TFLOP/s), 2.79 ms (D = 128).  Two multiply-adds at a time (199 us), a second buffer for the tiles (226) and
-// other rows to a thread (216) gave nothing.
+// Bound: the CUDA cores, half of their multiply-adds; without the scores' loop the kernel takes 0.62 of its time, without the values'
+// 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 197 us, 33 TFLOP/s; 2048 tokens after
+// 2048, 32 heads on 8 1.25 ms (D = 64, 41 TFLOP/s), 2.68 ms (D = 128).  Two multiply-adds at a time (198 us, 1.23 and 2.48 ms), a second buffer
+// for the tiles (226 instead of 201 us), other rows to a thread (216) and operands fetched a step ahead (204) gave little or nothing.
 #include "kda_chunk_attn.cuh"
 #include "kda_draft_sm100.cuh"
 
