@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                         p[i][j] = ex2(fmaf(s[i][j], sc, -m[i]));
                         sum += p[i][j];
                     }
-                    wild |= sum > kMostSum || (seen[i] && !(fabsf(m[i]) <= kTame));
+                    wild |= seen[i] && (sum > kMostSum || !(fabsf(m[i]) <= kTame));    // (what a row that is none gets goes nowhere)
                     part[i] = sum;
                 }
                 again = __any_sync(0xffffffffu, wild);
