@@ -660,7 +660,8 @@ kda_status kda_norm_rotate(const kda_norm_rotate_desc* desc, const void* q, cons
 /*
  * kda_page_fork -- table rows that share another row's first tokens.  Fork i gives the empty row children[i] the
  * first lens[i] tokens of row parents[i]: its whole pages by reference, and for a last page that they fill only partly a page of its
- * own, into which kda_cache_copy copies the rows.  `shares` counts the rows that hold a page beyond the first, so that
+ * own, into which kda_cache_copy copies the rows.  lens[i] is at most what the parent has written: pages that it
+ * holds past that (for drafts) cannot be told from others here, and a whole one would be shared although the parent appends to it.  `shares` counts the rows that hold a page beyond the first, so that
  * kda_page_release knows when it is free; pages of kda_page_tables start at 0.
  *
  *   parents, children, lens  [num_forks] int32; a parent may come many times, a child once

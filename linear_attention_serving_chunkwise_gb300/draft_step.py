@@ -97,21 +97,26 @@ class HybridLayers:
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
         """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages
         shared, the last one copied.  The KDA state is that of the parent's whole context, so a shorter child has to replay its
-        tokens into it.  Where the free pages do not reach, or a child is not empty: RuntimeError, and the other children are forked."""
+        tokens into it.  Rows that do not exist: ValueError; more tokens than a parent has: RuntimeError; nothing changes then.  Where the
+        free pages do not reach, or a child is not empty: RuntimeError, and the other children are forked."""
         rows, p, c, ps = self.context_lens.numel(), parents.long(), children.long(), self.cache.shape[2]
         if bool(((p < 0) | (p >= rows) | (c < 0) | (c >= rows)).any()):
             raise ValueError(f"there are {rows} sequences")
+        # (pages are held past the context too, for drafts: nothing that was kept lies there, and a parent still appends to them)
+        has = self.context_lens[p]
+        if bool(((lens < 0) | (lens > has)).any()):
+            raise RuntimeError("forks of more tokens than a sequence has")
         empty = self.pages_held[c] == 0
         self.pages_held, copies, taken = page_fork(parents, children, lens, self.pages_held, self.block_table, self.shares, self.free_pages,
                                                    page_size=ps)
         cache_copy(copies, self.cache[:, 0], self.cache[:, 1])
-        got = empty & (lens >= 0) & (self.pages_held[c] == (lens + ps - 1) // ps)
+        got = empty & (self.pages_held[c] == (lens + ps - 1) // ps)
         self.state[c] = torch.where(got[:, None, None, None], self.state[p], self.state[c])
         self.context_lens[c] = torch.where(got, lens, self.context_lens[c])
         taken, refused = torch.stack([taken[0], (~got).any().int()]).tolist()
         self.free_pages = self.free_pages[taken:]
         if refused:
-            raise RuntimeError("out of cache pages, or forks of what a row does not hold, or into rows that are not empty")
+            raise RuntimeError("out of cache pages, or forks into rows that are not empty")
 
     def release(self, keep_lens: torch.Tensor) -> None:
         """Every sequence's pages behind its first ``keep_lens`` [B] tokens given back (0: the sequence ends, its state becomes zero; cut

@@ -1,0 +1,42 @@
+"""The memories of ``draft_step.HybridLayers`` at the ends of what its calls allow: what they refuse leaves everything as it was."""
+import pytest
+import torch
+
+from linear_attention_serving_chunkwise_gb300 import draft_step
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=I32, device="cuda")
+
+
+def _kept(m):
+    return [t.clone() for t in (m.pages_held, m.context_lens, m.shares, m.free_pages, m.block_table, m.state)]
+
+
+def _same(m, before):
+    return all(torch.equal(a, b) for a, b in zip(before, (m.pages_held, m.context_lens, m.shares, m.free_pages, m.block_table, m.state)))
+
+
+def _after_a_draft_step():
+    """Four sequences, the first of 20 tokens with three pages of 16 held, the others empty; every row's state is its own."""
+    m = draft_step.HybridLayers(4, 2, 64, 1, 40, 16, 8)
+    m.reserve(20)
+    m.context_lens += 20
+    m.reserve(28)                                   # a step's nodes: pages up to token 48
+    m.release(_i32([48, 0, 0, 0]))
+    assert m.context_lens.tolist() == [20, 0, 0, 0] and m.pages_held.tolist() == [3, 0, 0, 0]
+    m.state.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    return m
+
+
+@pytest.mark.parametrize("lens", [21, 32, 48, 49, 2 ** 31 - 1, -1])
+def test_no_fork_of_more_than_the_parent_has(cuda_lib, lens):
+    """Pages are held past the context: rows that nobody wrote, and a page that the parent still appends to."""
+    m = _after_a_draft_step()
+    before = _kept(m)
+    with pytest.raises(RuntimeError):
+        m.fork(_i32([0, 0]), _i32([1, 2]), _i32([20, lens]))
+    assert _same(m, before) and cuda_lib.last_device_status() == cuda_lib.KDA_OK
