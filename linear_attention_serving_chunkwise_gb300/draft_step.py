@@ -97,11 +97,15 @@ class HybridLayers:
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
         """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages
         shared, the last one copied.  The KDA state is that of the parent's whole context, so a shorter child has to replay its
-        tokens into it.  Rows that do not exist: ValueError; more tokens than a parent has: RuntimeError; nothing changes then.  Where the
-        free pages do not reach, or a child is not empty: RuntimeError, and the other children are forked."""
+        tokens into it.  Rows that do not exist, a child named twice, a parent that is itself a child: ValueError; more tokens than a
+        parent has: RuntimeError; nothing changes then.  Where the free pages do not reach, or a child is not empty: RuntimeError, and
+        the other children are forked."""
         rows, p, c, ps = self.context_lens.numel(), parents.long(), children.long(), self.cache.shape[2]
-        if bool(((p < 0) | (p >= rows) | (c < 0) | (c >= rows)).any()):
+        whose, kids = torch.stack([p, c]).tolist()
+        if not all(0 <= r < rows for r in whose + kids):
             raise ValueError(f"there are {rows} sequences")
+        if len(set(kids)) < len(kids) or not set(kids).isdisjoint(whose):
+            raise ValueError("a child may come once, and is no parent in the same call")
         # (pages are held past the context too, for drafts: nothing that was kept lies there, and a parent still appends to them)
         has = self.context_lens[p]
         if bool(((lens < 0) | (lens > has)).any()):

@@ -40,3 +40,14 @@ def test_no_fork_of_more_than_the_parent_has(cuda_lib, lens):
     with pytest.raises(RuntimeError):
         m.fork(_i32([0, 0]), _i32([1, 2]), _i32([20, lens]))
     assert _same(m, before) and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("parents,children", [([0, 0], [1, 1]), ([0, 1], [1, 2]), ([0, 2], [2, 1]), ([3], [3])])
+@pytest.mark.parametrize("lens", [0, 5])
+def test_forks_that_contradict_each_other(cuda_lib, parents, children, lens):
+    """A child named twice, a parent that is a child: refused whatever the lengths, the empty one among them."""
+    m = _after_a_draft_step()
+    before = _kept(m)
+    with pytest.raises(ValueError):
+        m.fork(_i32(parents), _i32(children), _i32([lens if p == 0 else 0 for p in parents]))
+    assert _same(m, before) and cuda_lib.last_device_status() == cuda_lib.KDA_OK
