@@ -96,10 +96,10 @@ class HybridLayers:
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
         """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages
-        shared, the last one copied.  The KDA state is that of the parent's whole context, so a shorter child has to replay its
-        tokens into it.  Rows that do not exist, a child named twice, a parent that is itself a child: ValueError; more tokens than a
-        parent has: RuntimeError; nothing changes then.  Where the free pages do not reach, or a child is not empty: RuntimeError, and
-        the other children are forked."""
+        shared, the last one copied.  A child of all its parent's tokens gets the parent's KDA state; one of fewer begins with an empty state,
+        into which its tokens have to be replayed.  Rows that do not exist, a child named twice, a parent that is itself a child:
+        ValueError; more tokens than a parent has: RuntimeError; nothing changes then.  Where the free pages do not reach, or a child is not
+        empty: RuntimeError, and the other children are forked."""
         rows, p, c, ps = self.context_lens.numel(), parents.long(), children.long(), self.cache.shape[2]
         whose, kids = torch.stack([p, c]).tolist()
         if not all(0 <= r < rows for r in whose + kids):
@@ -115,7 +115,8 @@ class HybridLayers:
                                                    page_size=ps)
         cache_copy(copies, self.cache[:, 0], self.cache[:, 1])
         got = empty & (self.pages_held[c] == (lens + ps - 1) // ps)
-        self.state[c] = torch.where(got[:, None, None, None], self.state[p], self.state[c])
+        state = torch.where((lens == has)[:, None, None, None], self.state[p], 0.0)
+        self.state[c] = torch.where(got[:, None, None, None], state, self.state[c])
         self.context_lens[c] = torch.where(got, lens, self.context_lens[c])
         taken, refused = torch.stack([taken[0], (~got).any().int()]).tolist()
         self.free_pages = self.free_pages[taken:]

@@ -51,3 +51,13 @@ def test_forks_that_contradict_each_other(cuda_lib, parents, children, lens):
     with pytest.raises(ValueError):
         m.fork(_i32(parents), _i32(children), _i32([lens if p == 0 else 0 for p in parents]))
     assert _same(m, before) and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def test_the_state_of_a_fork(cuda_lib):
+    """All of the parent's tokens: its state.  Fewer: an empty one, into which they are replayed (they would count twice in the parent's)."""
+    m = _after_a_draft_step()
+    whole = m.state[0].clone()
+    m.fork(_i32([0, 0, 0]), _i32([1, 2, 3]), _i32([20, 19, 0]))
+    assert m.context_lens.tolist() == [20, 20, 19, 0] and m.pages_held.tolist() == [3, 2, 2, 0]
+    assert torch.equal(m.state[0], whole) and torch.equal(m.state[1], whole) and not m.state[2].any() and not m.state[3].any()
+    assert m.shares.sum() == 2 and cuda_lib.last_device_status() == cuda_lib.KDA_OK
