@@ -61,3 +61,16 @@ def test_the_state_of_a_fork(cuda_lib):
     assert m.context_lens.tolist() == [20, 20, 19, 0] and m.pages_held.tolist() == [3, 2, 2, 0]
     assert torch.equal(m.state[0], whole) and torch.equal(m.state[1], whole) and not m.state[2].any() and not m.state[3].any()
     assert m.shares.sum() == 2 and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("most", [2 ** 31 - 1, 2 ** 31 - 15, 2 ** 31 - 16, 1 << 30])
+def test_a_release_that_keeps_everything(cuda_lib, most):
+    """Lengths up to the largest that int32 holds leave a row as it is, also where its first page is another's too."""
+    m = _after_a_draft_step()
+    m.fork(_i32([0]), _i32([1]), _i32([20]))
+    before = _kept(m)
+    m.release(_i32([most, most, most, 1 << 20]))
+    assert _same(m, before)
+    m.release(_i32([0, most, 0, 0]))
+    assert m.context_lens.tolist() == [0, 20, 0, 0] and m.pages_held.tolist() == [0, 2, 0, 0] and not m.shares.any()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
