@@ -127,9 +127,12 @@ class HybridLayers:
         """Every sequence's pages behind its first ``keep_lens`` [B] tokens given back (0: the sequence ends, its state becomes zero; cut
         elsewhere, the KDA state stays that of all tokens).  A cut inside a page that others hold: RuntimeError, and nothing changes."""
         ps = self.cache.shape[2]
-        pages = (keep_lens.long() + (ps - 1)) // ps            # (any length that 32 bits hold)
-        last = self.block_table.gather(1, (pages - 1).clamp(0, self.block_table.shape[1] - 1)[:, None])[:, 0].clamp_min(0).long()
-        if bool(((keep_lens < 0) | ((keep_lens % ps > 0) & (pages <= self.pages_held) & (self.shares[last] > 0))).any()):
+        bad = keep_lens < 0
+        if self.shares.numel() and self.block_table.shape[1]:
+            pages = (keep_lens.long() + (ps - 1)) // ps        # (any length that 32 bits hold)
+            last = self.block_table.gather(1, (pages - 1).clamp(0, self.block_table.shape[1] - 1)[:, None])[:, 0].clamp_min(0).long()
+            bad |= (keep_lens % ps > 0) & (pages <= self.pages_held) & (self.shares[last] > 0)
+        if bool(bad.any()):
             raise RuntimeError("a sequence cannot be cut inside a page that others hold")
         self.pages_held, freed, count = page_release(keep_lens, self.pages_held, self.block_table, self.shares, page_size=ps)
         self.context_lens = torch.minimum(self.context_lens, keep_lens)

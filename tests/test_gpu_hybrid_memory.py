@@ -74,3 +74,14 @@ def test_a_release_that_keeps_everything(cuda_lib, most):
     m.release(_i32([0, most, 0, 0]))
     assert m.context_lens.tolist() == [0, 20, 0, 0] and m.pages_held.tolist() == [0, 2, 0, 0] and not m.shares.any()
     assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("pages,cols", [(0, 4), (5, 0), (0, 0)])
+def test_a_release_where_nothing_can_be_held(cuda_lib, pages, cols):
+    """No pages, or no columns for them: there is no entry to look at."""
+    m = draft_step.HybridLayers(3, 2, 64, 1, pages, 16, cols)
+    m.release(_i32([0, 5, 2 ** 31 - 1]))
+    assert m.pages_held.tolist() == [0, 0, 0] and m.free_pages.numel() == pages
+    with pytest.raises(RuntimeError):
+        m.release(_i32([0, -1, 0]))
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
