@@ -24,7 +24,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (KDA_PROLOGUE_ALL, KDA_TREE_PAD, cache_copy, cache_keep_path, chunk_attention, norm_rotate, page_fork, page_release,
+from . import (KDA_PROLOGUE_ALL, KDA_TREE_MAX_NODES, KDA_TREE_PAD, cache_copy, cache_keep_path, chunk_attention, norm_rotate, page_fork, page_release,
                page_tables, prefill, tree_attention, tree_commit, tree_decode, verify_drafts)
 
 
@@ -40,11 +40,27 @@ def with_pending_path(path: torch.Tensor, n_accept: torch.Tensor):
     return full, n_accept + 1
 
 
+def _rows_for_the_kernel(cache: torch.Tensor, nodes: int) -> bool:
+    """Whether ``cache_keep_path`` takes the rows of a cache [pages, 2, page_size, heads, dim] and steps of that many nodes."""
+    row, size = cache.shape[3] * cache.shape[4], cache.element_size()
+    return (cache.is_cuda and cache.get_device() == torch.cuda.current_device() and cache.dtype in (torch.bfloat16, torch.float32)
+            and 1 <= nodes <= KDA_TREE_MAX_NODES and cache.numel() > 0 and cache[0, 0].is_contiguous()
+            and all(x * size % 16 == 0 for x in (row, cache.stride(0), cache.stride(1))) and cache.data_ptr() % 16 == 0)
+
+
 def keep_path(cache: torch.Tensor, slots: torch.Tensor, path: torch.Tensor, n: torch.Tensor) -> None:
     """The kept nodes' rows of ``cache`` [pages, 2, page_size, heads, dim] moved to the front of the step's
     tokens.  slots [B, K]: where the nodes were written.  Entry e of a path is node e or a later
-    one, so every row moves towards the front, as if all were read before any is written."""
-    cache_keep_path(slots.contiguous(), path.contiguous(), n, cache[:, 0], cache[:, 1])
+    one, so every row moves towards the front, as if all were read before any is written.  Caches that the kernel does not
+    take (other types or devices, rows of no whole 16 bytes or that lie apart) are moved by indexing."""
+    if _rows_for_the_kernel(cache, path.shape[1]):
+        cache_keep_path(slots.to(torch.int64).contiguous(), path.to(torch.int32).contiguous(), n.to(torch.int32).contiguous(),
+                        cache[:, 0], cache[:, 1])
+        return
+    rows = cache.shape[2]
+    on = torch.arange(path.shape[1], device=path.device) < n[:, None]
+    src, dst = slots.gather(1, path.clamp_min(0).long())[on], slots[on]
+    cache[dst // rows, :, dst % rows] = cache[src // rows, :, src % rows]
 
 
 class HybridLayers:
