@@ -63,6 +63,14 @@ def keep_path(cache: torch.Tensor, slots: torch.Tensor, path: torch.Tensor, n: t
     cache[dst // rows, :, dst % rows] = cache[src // rows, :, src % rows]
 
 
+def _tokens(t: torch.Tensor) -> torch.Tensor:
+    """Tokens [T, heads, dim] as ``norm_rotate`` takes them: each token's heads side by side, tokens a multiple of 16 bytes apart."""
+    size = t.element_size()
+    if t.stride()[1:] == (t.shape[2], 1) and t.stride(0) >= t.shape[1] * t.shape[2] and t.stride(0) * size % 16 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class HybridLayers:
     """The memories of one KDA layer (state) and one attention layer (paged cache) for B sequences."""
 
@@ -93,11 +101,12 @@ class HybridLayers:
     def write(self, q, k, v, slots, positions=None, inv_freq=None, **norms) -> torch.Tensor:
         """Keys and values of any tokens into their slots.  With positions (shaped as the slots) and ``inv_freq``: queries and
         keys rotated first; with q_weight, k_weight or eps: normed before that.  Returns the queries."""
-        flat = lambda t: t.reshape(-1, *t.shape[-2:])
         kc, vc = self.cache.unbind(1)
+        flat = lambda t: _tokens(t.reshape(-1, *t.shape[-2:]))
         if positions is None:
             positions, inv_freq = slots.to(torch.int32), self.no_turns       # (nothing is rotated)
-        out = norm_rotate(flat(q), flat(k), flat(v), positions.reshape(-1), inv_freq, slots.reshape(-1), kc, vc, norm=bool(norms), **norms)
+        out = norm_rotate(flat(q), flat(k), flat(v), positions.reshape(-1), inv_freq, slots.reshape(-1).to(torch.int64), kc, vc,
+                          norm=bool(norms), **norms)
         return out.view(q.shape)
 
     def attend(self, q, k, v, slots, parents, **turn) -> torch.Tensor:

@@ -85,3 +85,37 @@ def test_a_release_where_nothing_can_be_held(cuda_lib, pages, cols):
     with pytest.raises(RuntimeError):
         m.release(_i32([0, -1, 0]))
     assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def _off(t):
+    """The same values, one element past where they would be aligned."""
+    return torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape).copy_(t)
+
+
+# keys and values [B, K, heads, dim] as a model may have them
+LAYOUTS = {"heads outside": lambda t: t.transpose(1, 2).contiguous().transpose(1, 2), "channels outside": lambda t: t.transpose(2, 3).contiguous().transpose(2, 3),
+           "unaligned": _off, "parts of odd rows": lambda t: torch.cat([t.flatten(2), t[..., 0, :1]], 2)[..., :-1].unflatten(2, t.shape[2:]),
+           "one row for all": lambda t: t[:, :1].expand(t.shape), "tokens outside": lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)}
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("B,K", [(1, 5), (3, 4), (2, 1)])
+def test_keys_and_values_of_any_layout(cuda_lib, layout, B, K):
+    """Strides and alignments that norm_rotate does not take are the memory's to mend."""
+    H, D, ps = 2, 64, 4
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda h: torch.randn(B, K, h, D, generator=gen, device="cuda").to(torch.bfloat16)
+    m = draft_step.HybridLayers(B, 4, D, H, 20, ps, 6)
+    q, k, v = rnd(4), LAYOUTS[layout](rnd(H)), LAYOUTS[layout](rnd(H))
+    slots = m.reserve(K)
+    chain = torch.arange(-1, K - 1, dtype=I32, device="cuda").expand(B, K).contiguous()
+    out = m.attend(q, k, v, slots.to(torch.int32) if K == 4 else slots, chain)
+    rows = m.cache[slots // ps, :, slots % ps]
+    assert torch.equal(rows[:, :, 0], k) and torch.equal(rows[:, :, 1], v)
+    s = torch.einsum("bihd,bjhd->bhij", q.double(), k.double().repeat_interleave(2, 2)) * D ** -0.5
+    w = torch.softmax(s.masked_fill(torch.ones(K, K, device="cuda", dtype=torch.bool).triu(1), float("-inf")), -1)
+    want = torch.einsum("bhij,bjhd->bihd", w, v.double().repeat_interleave(2, 2))
+    mass = torch.einsum("bhij,bjhd->bihd", w, v.double().abs().repeat_interleave(2, 2))
+    # bf16: the weights' rounding and that of the output, half a step each, and fp32's share
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * (mass + want.abs()) + 2.0 ** -16 * mass).all()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
