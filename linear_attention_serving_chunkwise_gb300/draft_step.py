@@ -24,7 +24,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (KDA_PROLOGUE_ALL, KDA_TREE_MAX_NODES, KDA_TREE_PAD, cache_copy, cache_keep_path, chunk_attention, norm_rotate, page_fork, page_release,
+from . import (KDA_CHUNK_MAX_GROUP, KDA_PROLOGUE_ALL, KDA_TREE_MAX_NODES, KDA_TREE_PAD, cache_copy, cache_keep_path, chunk_attention, norm_rotate, page_fork, page_release,
                page_tables, prefill, tree_attention, tree_commit, tree_decode, verify_drafts)
 
 
@@ -117,7 +117,10 @@ class HybridLayers:
     def attend_chunks(self, q, k, v, slots, cu_seqlens, **turn) -> torch.Tensor:
         """The same for chunks of prompts, packed: q [T, heads, dim], slots [T], cu_seqlens [B + 1]."""
         q = self.write(q, k, v, slots, **turn)
-        return chunk_attention(q, self.cache[:, 0], self.cache[:, 1], self.block_table, self.context_lens, cu_seqlens)
+        attend = lambda q: chunk_attention(q.flatten(1, 2), self.cache[:, 0], self.cache[:, 1], self.block_table, self.context_lens, cu_seqlens)
+        # query heads by their cache head, so many of each at a time as one call takes
+        groups = q.unflatten(1, (self.cache.shape[3], -1)).split(KDA_CHUNK_MAX_GROUP, 2)
+        return attend(groups[0]) if len(groups) == 1 else torch.cat([attend(g.contiguous()).view(g.shape) for g in groups], 2).flatten(1, 2)
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor) -> None:
         """Sequences ``children`` (empty) go on from the first ``lens`` tokens of ``parents`` ([n] int32 each): their whole pages

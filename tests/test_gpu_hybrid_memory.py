@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import _prompt_ref as R
 from linear_attention_serving_chunkwise_gb300 import draft_step
 
 pytestmark = pytest.mark.gpu
@@ -118,4 +119,23 @@ def test_keys_and_values_of_any_layout(cuda_lib, layout, B, K):
     mass = torch.einsum("bhij,bjhd->bihd", w, v.double().abs().repeat_interleave(2, 2))
     # bf16: the weights' rounding and that of the output, half a step each, and fp32's share
     assert ((out.double() - want).abs() <= 2.0 ** -8 * (mass + want.abs()) + 2.0 ** -16 * mass).all()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(96, 1, 64), (130, 2, 64), (128, 1, 128)])
+def test_prompts_of_more_heads_to_a_cache_head_than_one_call_takes(cuda_lib, heads, kv_heads, dim):
+    """The tree attention has no such limit, and the model's prompts went through it before."""
+    gen = torch.Generator(device="cuda").manual_seed(heads)
+    rnd = lambda h: torch.randn(90, h, dim, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v = rnd(heads), rnd(kv_heads), rnd(kv_heads)
+    new, ends = [41, 0, 49], _i32([0, 41, 41, 90])
+    m = draft_step.HybridLayers(3, heads, 64, kv_heads, 30, 16, 8)
+    m.cache = torch.empty((30, 2, 16, kv_heads, dim), dtype=torch.bfloat16, device="cuda")
+    slots, _, m.pages_held, _ = cuda_lib.page_tables(m.context_lens, _i32(new), m.pages_held, m.block_table, m.free_pages, page_size=16, max_tokens=90)
+    got = m.attend_chunks(q, k, v, slots, ends)
+    ref, bound, mass = R.chunk_attention(q, m.cache[:, 0], m.cache[:, 1], m.block_table.cpu(), m.context_lens.cpu(), ends.cpu(), dim ** -0.5)
+    # bf16: the weights' rounding and that of the output, half a step each
+    assert ((got.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (mass + ref.abs())).all()
+    m = draft_step.ToyHybrid(2, heads=heads, dim=64, kv_heads=kv_heads, most_tokens=96)
+    assert torch.isfinite(m.prompt(torch.randint(0, 211, (2, 70), generator=gen, device="cuda", dtype=I32))).all()
     assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
