@@ -100,11 +100,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, pha
     bind = not phase_clocks and (force or not current or not bind_up_to_date())
     if current and not bind:
         return lib_path
+    os.makedirs(obj_dir, exist_ok=True)
     if current:
         _link_bind(_compile_bind())
         return lib_path
     nvcc = _nvcc()
-    os.makedirs(obj_dir, exist_ok=True)
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                      "--expt-relaxed-constexpr", "-I", os.path.join(os.path.dirname(PKG), "include")]
     if phase_clocks:
