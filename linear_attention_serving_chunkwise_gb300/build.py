@@ -1,8 +1,9 @@
-"""Build the KDA CUDA library in-tree for sm_103a with nvcc (no cmake, no torch extension).
+"""Build the KDA CUDA library and its Python binding in-tree for sm_103a (no cmake, no setuptools).
 
 ``python -m linear_attention_serving_chunkwise_gb300.build`` or ``build()`` compiles each
-``csrc/*.cu`` translation unit in parallel and links ``libkda_gb300.so`` beside this file, and ``_bind.so``, the
-compiled part of the Python binding (``csrc/kda_bind.cpp``, with the installed PyTorch's headers).
+``csrc/*.cu`` translation unit in parallel with nvcc and links ``libkda_gb300.so`` beside this file, and ``_bind.so``, the
+compiled part of the Python binding (``csrc/kda_bind.cpp``, with g++ and the installed PyTorch's headers).  Where there is no PyTorch,
+``python build.py`` builds the library alone.
 ``build(phase_clocks=True)`` builds a separate instrumented library,
 ``libkda_gb300_clocks.so``, with the per-phase cycle marks compiled in (see phase_clocks.py);
 the library everything else loads never has them.
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -52,6 +54,13 @@ def up_to_date(lib: str = LIB) -> bool:
         return False
     t = os.path.getmtime(lib)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _has_torch() -> bool:
+    if importlib.util.find_spec("torch"):
+        return True
+    sys.stderr.write("PyTorch is not installed: the C library is built without its Python binding\n")
+    return False
 
 
 def bind_up_to_date() -> bool:
@@ -97,7 +106,7 @@ def _link_bind(obj: str) -> None:
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, phase_clocks: bool = False) -> str:
     lib_path, obj_dir = (LIB_CLOCKS, OBJ_CLOCKS) if phase_clocks else (LIB, OBJ)
     current = not force and up_to_date(lib_path)
-    bind = not phase_clocks and (force or not current or not bind_up_to_date())
+    bind = not phase_clocks and _has_torch() and (force or not current or not bind_up_to_date())
     if current and not bind:
         return lib_path
     os.makedirs(obj_dir, exist_ok=True)

@@ -29,3 +29,34 @@ def test_the_binding_alone_is_built_without_the_folder_of_objects(compilers, mon
     monkeypatch.setattr(B, "up_to_date", lambda lib=None: True)
     B.build()
     assert compilers == ["kda_bind.o", "_bind.so.tmp"] and os.path.exists(B.BIND)
+
+
+WITHOUT_TORCH = """
+import importlib.util, os, subprocess, sys
+sys.modules["torch"] = None
+spec = importlib.util.spec_from_file_location("build_alone", {path!r})
+B = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(B)
+for name in ("OBJ", "LIB", "BIND", "PKG"):
+    setattr(B, name, os.path.join({tmp!r}, name))
+made = []
+
+def run(cmd, **kw):
+    out = cmd[cmd.index("-o") + 1]
+    open(out, "w").close()
+    made.append(os.path.basename(out))
+    return subprocess.CompletedProcess(cmd, 0, "", "")
+
+subprocess.run = run
+B.build()
+assert os.path.exists(B.LIB) and "kda_bind.o" not in made and not os.path.exists(B.BIND), made
+B.build()                                                # and it is current
+assert made.count("LIB.tmp") == 1, made
+"""
+
+
+def test_the_library_is_built_without_pytorch(tmp_path):
+    """The C library needs nvcc alone; only its Python binding needs PyTorch."""
+    r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH.format(path=B.__file__, tmp=str(tmp_path))], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert "PyTorch" in r.stderr
