@@ -19,7 +19,7 @@ def compilers(monkeypatch, tmp_path):
         made.append(os.path.basename(out))
         return subprocess.CompletedProcess(cmd, 0, "", "")
 
-    for name, at in (("OBJ", "_build"), ("LIB", "libkda_gb300.so"), ("BIND", "_bind.so"), ("PKG", "")):
+    for name, at in (("OBJ", "_build"), ("LIB", "libkda_gb300.so"), ("BIND", "_bind.so")):
         monkeypatch.setattr(B, name, str(tmp_path / at))
     monkeypatch.setattr(subprocess, "run", run)
     return made
@@ -37,7 +37,7 @@ sys.modules["torch"] = None
 spec = importlib.util.spec_from_file_location("build_alone", {path!r})
 B = importlib.util.module_from_spec(spec)
 spec.loader.exec_module(B)
-for name in ("OBJ", "LIB", "BIND", "PKG"):
+for name in ("OBJ", "LIB", "BIND"):
     setattr(B, name, os.path.join({tmp!r}, name))
 made = []
 
