@@ -63,11 +63,17 @@ def _has_torch() -> bool:
     return False
 
 
-def bind_up_to_date() -> bool:
-    """Newer than its sources, and built with the PyTorch that is installed."""
+def _bound_to() -> str:
+    """What the binding is compiled for: this PyTorch, where it lies (a search path of the binding), and this Python."""
+    import sysconfig
     import torch
+    return "\n".join([torch.__version__, os.path.dirname(torch.__file__), str(sysconfig.get_config_var("SOABI"))])
+
+
+def bind_up_to_date() -> bool:
+    """Newer than its sources, and built for the PyTorch and the Python that run."""
     stamp = os.path.join(OBJ, "bind.torch")
-    if not os.path.exists(BIND) or not os.path.exists(stamp) or open(stamp).read() != torch.__version__:
+    if not os.path.exists(BIND) or not os.path.exists(stamp) or open(stamp).read() != _bound_to():
         return False
     return all(os.path.getmtime(p) <= os.path.getmtime(BIND) for p in _deps() + [BIND_SRC])
 
@@ -100,7 +106,7 @@ def _link_bind(obj: str) -> None:
         raise RuntimeError("linking _bind.so failed")
     os.replace(BIND + ".tmp", BIND)
     with open(os.path.join(OBJ, "bind.torch"), "w") as f:
-        f.write(torch.__version__)
+        f.write(_bound_to())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, phase_clocks: bool = False) -> str:

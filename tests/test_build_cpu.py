@@ -60,3 +60,26 @@ def test_the_library_is_built_without_pytorch(tmp_path):
     r = subprocess.run([sys.executable, "-c", WITHOUT_TORCH.format(path=B.__file__, tmp=str(tmp_path))], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert "PyTorch" in r.stderr
+
+
+@pytest.mark.parametrize("what", ["version", "folder", "interpreter"])
+def test_a_binding_of_another_pytorch_or_python_is_built_anew(compilers, monkeypatch, what):
+    """The stamp names all that the binding was compiled for; PyTorch's folder is in its search path."""
+    import sysconfig
+    import torch
+    B.build()
+    compilers.clear()
+    B.build()
+    assert compilers == []
+    if what == "version":
+        monkeypatch.setattr(torch, "__version__", "0.1")
+    elif what == "folder":
+        monkeypatch.setattr(torch, "__file__", "/elsewhere/torch/__init__.py")
+    else:
+        of = sysconfig.get_config_var
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else of(name))
+    B.build()
+    assert "_bind.so.tmp" in compilers
+    compilers.clear()
+    B.build()
+    assert compilers == []
