@@ -645,21 +645,16 @@ def chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, 
     values are in the cache already (``norm_rotate``).  ``scale`` defaults to 1 / sqrt(D); ``workspace``: uint8 scratch of
     ``chunk_attention_workspace_bytes``, allocated if not given.  Returns out [T,Hq,D] of q's type; rows behind
     the last chunk are not written, so in a tensor allocated here they are undefined."""
-    handle = None
-    if stream is not None:
-        handle = _stream_on(stream, q.get_device())
-        if workspace is None:
-            desc = make_chunk_attention_desc(block_table.shape[0], *q.shape[:2], k_cache.shape[2], q.shape[2], _dtype_code(q), *k_cache.shape[:2],
-                                             block_table.shape[1], 0.0, k_cache.stride(0), v_cache.stride(0))
-            workspace = _fresh((chunk_attention_workspace_bytes(desc),), torch.uint8, q.device, stream)
-    st, made = (_bind or _bound()).chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out, scale, workspace, handle)
+    handle = None if stream is None else _stream_on(stream, q.get_device())
+    st, made, scratch = (_bind or _bound()).chunk_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out, scale, workspace, handle)
     if check and st != KDA_OK:
         raise KDAError(st, "kda_chunk_attention")
-    if out is not None:
-        return out
     if stream is not None:
-        _keep_until_done(made, stream)
-    return made
+        if workspace is None:
+            _keep_until_done(scratch, stream)
+        if out is None:
+            _keep_until_done(made, stream)
+    return made if out is None else out
 
 
 def norm_rotate(q, k, v, positions, inv_freq, slots, k_cache, v_cache, out=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,

@@ -157,7 +157,7 @@ PyObject* answer(kda_status st, const T&... made)
 
 void arity(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, want, " arguments expected, got ", n); }
 
-// q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out, scale, workspace, stream -> status, out
+// q, k_cache, v_cache, block_table, context_lens, cu_seqlens, out, scale, workspace, stream -> status, out, workspace
 PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
@@ -196,7 +196,7 @@ PyObject* chunk_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
     wp = ws.data_ptr();
     void* const op = out.data_ptr();
     const kda_status st = without_gil([&] { return kda_chunk_attention(&d, qp, kp, vp, tp, cp, up, op, wp, bytes, queue); });
-    return answer(st, out);
+    return answer(st, out, ws);
     END_HANDLE_TH_ERRORS
 }
 
