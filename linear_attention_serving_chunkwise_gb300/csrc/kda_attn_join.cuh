@@ -70,10 +70,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a, Shape sh
     if (rec.last == 0 || r0 >= rows) return;
     const int parts = rec.last - c + 1, r = min(r0 + lane, sh.BM - 1), first4 = C4 * blockIdx.z;
     const auto part = [&](int i) { return slot_of(a.workspace, sh, D, i == 0 ? 2 * c + 1 : 2 * (c + i)); };
-    // nothing to attend to: zeros; NaN stays
-    const auto over = [](float4 x, float sum) {
-        const float inv = 1.f / sum;
-        return sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    // no maximum at all: nothing to attend to, zeros; NaN stays, and a sum of 0 with a maximum (scores of -inf only) becomes it
+    const auto over = [](float4 x, float sum, float m) {
+        const float inv = 1.f / sum, none = m == -INFINITY ? 0.f : NAN;
+        return sum == 0.f ? make_float4(none, none, none, none) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     };
     if (parts == 2) {
         float pm[2], pl[2];
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a, Shape sh
         const float f0 = exp2f(pm[0] - base), f1 = exp2f(pm[1] - base);
         s_out[lane][w] = over(make_float4(fmaf(f1, po[1].x, f0 * po[0].x), fmaf(f1, po[1].y, f0 * po[0].y),
                                           fmaf(f1, po[1].z, f0 * po[0].z), fmaf(f1, po[1].w, f0 * po[0].w)),
-                              fmaf(f1, pl[1], f0 * pl[0]));
+                              fmaf(f1, pl[1], f0 * pl[0]), m);
         __syncthreads();
     } else {
         float m = -INFINITY;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(JoinArgs a, Shape sh
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < kJoinWarps; ++i) sum += s_l[i][lane];
-                s_out[lane][k0 + w] = over(x, sum);
+                s_out[lane][k0 + w] = over(x, sum, m);
             }
             __syncthreads();
         }

@@ -10,6 +10,8 @@
 // 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 197 us, 33 TFLOP/s; 2048 tokens after
 // 2048, 32 heads on 8 1.25 ms (D = 64, 41 TFLOP/s), 2.68 ms (D = 128).  Two multiply-adds at a time (198 us, 1.23 and 2.48 ms), a second buffer
 // for the tiles (226 instead of 201 us), other rows to a thread (216) and operands fetched a step ahead (204) gave little or nothing.
+#include <float.h>
+
 #include "kda_chunk_attn.cuh"
 #include "kda_draft_sm100.cuh"
 
@@ -19,6 +21,9 @@ namespace {
 constexpr int kThreads = 128, kBM = 64, kTM = 8;
 constexpr float kTame = 4096.f;        // largest maximum (in powers of two) of the quick form
 constexpr float kMostSum = 32768.f;    // most that a thread's weights of a tile's row may sum to before the maximum is set anew
+// The maximum of a row that sees tokens whose scores are all -inf: its weights are 0 over 0, as by the definition, where a row that sees
+// no token (maximum -inf) becomes zero.
+constexpr float kLowest = -FLT_MAX;
 
 template <int D>
 struct Tile {
@@ -186,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < TN; ++j) {
-                        s[i][j] = s_on[tx + 16 * j] && t0 + tx + 16 * j < seen[i] ? s[i][j] * sc : -INFINITY;
-                        top = fmaxf(top, s[i][j]);
+                        const bool sees = s_on[tx + 16 * j] && t0 + tx + 16 * j < seen[i];
+                        s[i][j] = sees ? s[i][j] * sc : -INFINITY;
+                        top = fmaxf(top, fmaxf(s[i][j], sees ? kLowest : -INFINITY));
                     }
 #pragma unroll
                     for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -228,11 +234,11 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
             if (r >= rows) continue;
             if (pc.whole()) {
                 float* dst = static_cast<float*>(a.out) + ((size_t)(pc.row0 + r / G) * a.heads + pc.hk * G + r % G) * D;
-                const float inv = 1.f / l[i];
+                const float inv = 1.f / l[i], none = m[i] == -INFINITY ? 0.f : NAN;
 #pragma unroll
                 for (int k = 0; k < CD; k += 4) {
                     const float4 y = make_float4(o[i][k] * inv, o[i][k + 1] * inv, o[i][k + 2] * inv, o[i][k + 3] * inv);
-                    *reinterpret_cast<float4*>(dst + tx * 4 + 16 * k) = l[i] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : y;
+                    *reinterpret_cast<float4*>(dst + tx * 4 + 16 * k) = l[i] == 0.f ? make_float4(none, none, none, none) : y;
                 }
             } else {
                 if (tx == 0) { ws[r] = m[i]; ws[kBM + r] = l[i]; }

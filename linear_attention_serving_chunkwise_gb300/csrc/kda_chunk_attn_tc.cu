@@ -36,6 +36,8 @@
 // of range are zero in shared memory.  The values of the block's own tokens may be seen by some rows only, so
 // non-finite ones are replaced by zero in the tile and added back in the epilogue of the
 // rows that see the token (a positive weight times infinity or NaN is itself).
+#include <float.h>
+
 #include "kda_attn_tc.cuh"
 #include "kda_chunk_attn.cuh"
 
@@ -54,6 +56,9 @@ constexpr int kHead = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTame = 4096.f;                     // largest m sc of the form with one operation
 constexpr float kMostSum = 32768.f;                 // most that a row's weights of a tile may sum to before its maximum is set anew
+// The maximum of a row that sees tokens whose scores are all -inf: its weights are 0 over 0, as by the definition, where a row that sees
+// no token (maximum -inf) becomes zero.
+constexpr float kLowest = -FLT_MAX;
 
 struct Shared {
     uint64_t kv_full[10], kv_empty[10], v_raw[10], s_full[2], p_full[2], q_full, q_empty, o_done[2], o_free[2];
@@ -473,6 +478,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                         read(c, x);
                         top = fmaxf(top, max_of(x));
                     }
+                    if (top == -INFINITY && (mw[0] | mw[1] | mw[2] | mw[3])) top = kLowest;
                     const bool grow = top > m;
                     const float f = grow ? ex2((m - top) * sc) : 1.f;  // 0 for the first maximum
                     l *= f;
@@ -527,10 +533,10 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
 #pragma unroll
             for (int k = 0; k < 8; ++k) bad |= *const_cast<volatile uint32_t*>(&sm.bad[piece & 7][k]) != 0;
         }
-        const float norm = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const float norm = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f, none = pc.whole() && m != -INFINITY ? NAN : 0.f;
         float* ws = attn::slot_of(a.workspace, sh, D, pc.slot);
         if (mine && !pc.whole()) {
-            ws[rl] = m == -INFINITY ? m : m * sc;
+            ws[rl] = m == -INFINITY ? m : fmaxf(m * sc, kLowest);
             ws[sh.BM + rl] = l;
         }
         // out's row of this thread (in rows of D), and of the four rows of its group of four lanes
@@ -545,7 +551,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnArgs& a, const Shape& sh,
                 tmem_ld32(tO + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = l == 0.f ? 0.f : o[k] * norm;
+                for (int k = 0; k < 32; ++k) o[k] = l == 0.f ? none : o[k] * norm;
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = 0.f;

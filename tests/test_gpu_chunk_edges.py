@@ -34,3 +34,67 @@ def test_one_page_of_any_stride_on_another_stream(cuda_lib, dtype, D):
     out = cuda_lib.chunk_attention(*args, out=torch.empty_like(q), stream=side)
     side.synchronize()
     assert torch.equal(got, want) and torch.equal(out, want) and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+def _paged(kda, k, v, lens, new, ps):
+    """Rows of keys and values per sequence (lists of [n, Hk, D]) in a cache whose other rows are NaN: what the call takes behind q."""
+    Hk, D = k[0].shape[1:]
+    kv, table = R.paged(lens, Hk, D, k[0].dtype, ps)
+    for b, n in enumerate(lens):
+        t = torch.arange(n)
+        where = table[b].long()[t // ps], t % ps
+        kv[where[0], 0, where[1]], kv[where[0], 1, where[1]] = k[b], v[b]
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    dev = kv.cuda()
+    return kv, table, [n - m for n, m in zip(lens, new)], cu, (dev[:, 0], dev[:, 1], table.cuda(), _i32([n - m for n, m in zip(lens, new)]), _i32(cu))
+
+
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+@pytest.mark.parametrize("H,Hk,ctx,new", [(2, 1, [0, 0, 5], [1, 140, 9]), (16, 2, [300, 129], [20, 1]), (2, 1, [9000, 128], [2, 3]), (3, 1, [6000], [130])])
+def test_scores_of_minus_infinity(cuda_lib, dtype, D, H, Hk, ctx, new):
+    """Rows all of whose visible scores are -inf are NaN; a single finite score among them is all that counts, wherever it lies."""
+    gen = torch.Generator().manual_seed(7)
+    lens = [c + n for c, n in zip(ctx, new)]
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(dtype)
+    q = rnd(sum(new), H, D)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    k, v = [rnd(n, Hk, D) for n in lens], [rnd(n, Hk, D) for n in lens]
+    for x in k:
+        x[..., 5] = -float("inf")
+    _, _, _, _, args = _paged(cuda_lib, k, v, lens, new, 16)
+    out = cuda_lib.chunk_attention(q.cuda(), *args)
+    assert out.isnan().all()
+    for at in (lambda n, m: 0, lambda n, m: n - m, lambda n, m: n // 2, lambda n, m: n - 1):
+        k2 = [x.clone() for x in k]
+        for x, n, m in zip(k2, lens, new):
+            x[at(n, m), :, 5] = 0.25
+        _, _, _, cu, args = _paged(cuda_lib, k2, v, lens, new, 16)
+        out = cuda_lib.chunk_attention(q.cuda(), *args).cpu()
+        for b, (n, m) in enumerate(zip(lens, new)):
+            got, first = out[cu[b]:cu[b + 1]], at(n, m) - (n - m)
+            assert got[:max(first, 0)].isnan().all()
+            want = v[b][at(n, m)].repeat_interleave(H // Hk, 0).expand(m, H, D)[max(first, 0):]
+            # one weight, of 1 or (a maximum kept) up to 2^15: its rounding to bf16 and the quotient's
+            assert ((got[max(first, 0):].double() - want.double()).abs() <= (2.0 ** -7 if dtype == torch.bfloat16 else 2.0 ** -22) * want.double().abs()).all()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+def test_rows_without_a_page_stay_zero_beside_them(cuda_lib, dtype, D):
+    """No page that exists: zeros and the error word, also where the part of a split row that has one holds -inf."""
+    gen = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(dtype)
+    lens, new = [7000, 200], [2, 3]
+    q, k, v = rnd(5, 2, D).abs() + 0.5, [rnd(n, 1, D) for n in lens], [rnd(n, 1, D) for n in lens]
+    k[0][...] = -float("inf")
+    _, _, _, _, (kc, vc, table, c, cu) = _paged(cuda_lib, k, v, lens, new, 16)
+    table[1] = -1
+    out = cuda_lib.chunk_attention(q.to(dtype).cuda(), kc, vc, table, c, cu)
+    assert out[:2].isnan().all() and not out[2:].any()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
+    table[0, 1:] = -1                                          # sixteen tokens of -inf are left, the other parts have none
+    out = cuda_lib.chunk_attention(q.to(dtype).cuda(), kc, vc, table, c, cu)
+    assert out[:2].isnan().all() and not out[2:].any()
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
