@@ -67,12 +67,13 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(NormRotateArgs
 
     for (int i = t; i < tokens * half; i += kThreads) {
         const int k = i / half, c = i - k * half;
-        double turn = (double)a.inv_freq[c] * 0.15915494309189533577;
+        const float freq = a.inv_freq[c];
+        double turn = (double)freq * 0.15915494309189533577;
         turn -= floor(turn);
         const unsigned long long f = (unsigned long long)(turn * 18446744073709551616.0) * (unsigned long long)(long long)a.positions[t0 + k];
         const float h = (float)(int)(f >> 32) * 4.656612873077393e-10f;   // half turns, from -1 to 1
-        // pair c is the (c % V)-th of lane c / V, in both orders
-        reinterpret_cast<float2*>(&s_turn[k][c % V / 2][c / V])[c & 1] = make_float2(cospif(h), sinpif(h));
+        // pair c is the (c % V)-th of lane c / V, in both orders (the conversions above make some angle of an infinite or NaN frequency too)
+        reinterpret_cast<float2*>(&s_turn[k][c % V / 2][c / V])[c & 1] = isfinite(freq) ? make_float2(cospif(h), sinpif(h)) : make_float2(NAN, NAN);
     }
     __syncthreads();
 
