@@ -648,7 +648,8 @@ typedef struct kda_norm_rotate_desc {
  *                 nowhere.  No slot may come twice.
  *   q_out         [T, Hq, dim] dtype
  *   k_cache, v_cache  as kda_tree_attention's; only the slots' rows are written
- * fp32 arithmetic, rounded once; angles are exact to 1e-8 of a turn for positions up to 2^24 whatever the frequency.
+ * fp32 arithmetic, rounded once; angles are exact to 1e-9 of a turn at any position, for frequencies up to 2^40 (a pair of an
+ * infinite or NaN frequency is NaN).
  * q_out overlaps nothing, the caches no input.  A slot past the caches is left out and makes
  * kda_last_device_status() return KDA_ERR_INVALID_ARG.
  */

@@ -9,7 +9,9 @@
 //
 // The angle: f / 2 pi as a 64-bit fraction of a turn, times the position as integers, so whole turns
 // drop out of the product by themselves and a far position costs no accuracy (fp32 radians are off by 0.06 at a
-// million tokens).  A CTA forms its tokens' sines and cosines once, for all heads.
+// million tokens).  1 / 2 pi is two doubles, so a high frequency costs none either: the fraction is within 2^-64 for frequencies
+// up to 2^40, the angle within 2^-33 of a turn for any position.  A CTA forms its pairs' fractions, then its tokens' sines and
+// cosines, once for all heads.
 //
 // A lane holds two 16-byte chunks of a row that are each other's partners (or lie side by side where nothing is
 // rotated), so a rotation needs no exchange and a norm three shuffles.  A warp has one token (or an eighth of one, where
@@ -26,6 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostTokens = 8;         // of a CTA: a warp each
+constexpr double kPerTurn = 0.15915494309189535, kPerTurnRest = -9.839338337591243e-18;    // 1 / 2 pi, to 2^-110
+constexpr double kTwo64 = 18446744073709551616.0;
 
 __device__ __forceinline__ void unpack(uint4 u, float (&x)[8])
 {
@@ -61,19 +65,29 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(NormRotateArgs
     constexpr int V = 16 / sizeof(T), CH = D / V, LANES = CH / 2, ROWS = 32 / LANES;   // a row's chunks and lanes, rows of a warp
     constexpr int U = 2;               // groups of rows whose loads are in flight together
     __shared__ float4 s_turn[kMostTokens][V / 2][LANES];    // cosine, sine of a lane's V pairs, two at a time
+    __shared__ unsigned long long s_frac[D / 2];            // a pair's turn a token, as a fraction of 2^64
+    __shared__ bool s_finite[D / 2];
+    __shared__ int s_pos[kMostTokens];
     const int t = threadIdx.x, lane = t & 31, l = lane % LANES, sub = lane / LANES;
     const int t0 = blockIdx.x * per_cta, tokens = min(per_cta, a.tokens - t0), half = a.rot / 2;
     const int turned = a.rot / (2 * V);                     // chunks of each of the halves
 
+    for (int c = t; c < half; c += kThreads) {
+        const float freq = a.inv_freq[c];
+        const double x = freq, hi = x * kPerTurn, lo = fma(x, kPerTurn, -hi) + x * kPerTurnRest;
+        s_frac[c] = (unsigned long long)__double2ll_rn((hi - rint(hi)) * kTwo64) + (unsigned long long)__double2ll_rn((lo - rint(lo)) * kTwo64);
+        s_finite[c] = isfinite(freq);                       // (the conversions make some angle of the others too)
+    }
+    if (half && t >= kThreads - tokens) s_pos[kThreads - 1 - t] = a.positions[t0 + kThreads - 1 - t];
+    __syncthreads();
     for (int i = t; i < tokens * half; i += kThreads) {
         const int k = i / half, c = i - k * half;
-        const float freq = a.inv_freq[c];
-        double turn = (double)freq * 0.15915494309189533577;
-        turn -= floor(turn);
-        const unsigned long long f = (unsigned long long)(turn * 18446744073709551616.0) * (unsigned long long)(long long)a.positions[t0 + k];
-        const float h = (float)(int)(f >> 32) * 4.656612873077393e-10f;   // half turns, from -1 to 1
-        // pair c is the (c % V)-th of lane c / V, in both orders (the conversions above make some angle of an infinite or NaN frequency too)
-        reinterpret_cast<float2*>(&s_turn[k][c % V / 2][c / V])[c & 1] = isfinite(freq) ? make_float2(cospif(h), sinpif(h)) : make_float2(NAN, NAN);
+        const unsigned long long f = s_frac[c] * (unsigned long long)(long long)s_pos[k];
+        // The upper 24 bits as half turns from -1 to 1, exact in fp32; the next 24 in radians, b: sin(h + b) = sin h + b cos h to 1e-13.
+        const float h = (float)((int)(f >> 32) & ~255) * 4.656612873077393e-10f, b = (float)(int)(f >> 16 & 0xffffff) * (6.2831853f / 281474976710656.f);
+        const float co = cospif(h), si = sinpif(h);
+        // pair c is the (c % V)-th of lane c / V, in both orders
+        reinterpret_cast<float2*>(&s_turn[k][c % V / 2][c / V])[c & 1] = s_finite[c] ? make_float2(fmaf(-si, b, co), fmaf(co, b, si)) : make_float2(NAN, NAN);
     }
     __syncthreads();
 
