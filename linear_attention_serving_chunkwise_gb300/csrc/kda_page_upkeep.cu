@@ -19,6 +19,9 @@ namespace cg = cooperative_groups;
 constexpr int kMaxRows = 16384;        // KDA_PAGE_TABLES_MAX_BATCH
 constexpr int kBlock = 256;            // table columns that a warp takes at a time: eight reads in flight a lane
 
+// (columns and pages go up to 2^31 - 1: what is added to them is added in 64 bits, or to an offset)
+__host__ __device__ __forceinline__ int blocks_of(int cols) { return (int)((cols + (long long)kBlock - 1) / kBlock); }
+
 // ------------------------------------------------------------------ forks
 // As in page_tables, every CTA works the forks out for itself (12 bytes each, from L2) and then does
 // its share of the table entries, so one launch does all.  Bound: latency, of the launch and of four dependent reads
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(PageForkArgs a)
     }
 
     // the children's entries: a warp to kBlock columns of a fork
-    const int blocks = (a.table_cols + kBlock - 1) / kBlock;
+    const int blocks = blocks_of(a.table_cols);
     const long long items = (long long)a.forks * blocks;
     for (long long it = (long long)blockIdx.x * kForkWarps + w; it < items; it += (long long)gridDim.x * kForkWarps) {
         const int i = (int)(it / blocks), page = sm.page[i];
@@ -202,34 +205,33 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
     sync();
 
     // a warp to kBlock columns of a row
-    const int blocks = (a.table_cols + kBlock - 1) / kBlock;
+    const int blocks = blocks_of(a.table_cols);
     const long long items = (long long)a.rows * blocks;
     for (long long i = all_w; i < items; i += warps) {
         const int r = (int)(i / blocks), j0 = (int)(i % blocks) * kBlock, held = a.pages_held[r];
-        const int from = max(__ldcg(a.pages_held_out + r), j0), to = held <= a.table_cols ? min(held, j0 + kBlock) : 0;
-        if (from >= to) continue;
-        const int32_t* row = a.block_table + (size_t)r * a.table_cols;
+        if (held > a.table_cols || held <= j0) continue;
+        const int from = max(__ldcg(a.pages_held_out + r), j0), n = min(held - j0, kBlock) - (from - j0);
+        if (n <= 0) continue;
+        const int32_t* row = a.block_table + (size_t)r * a.table_cols + from;
         int id[kBlock / 32];
 #pragma unroll
-        for (int x = 0; x < kBlock / 32; ++x) {
-            const int j = from + 32 * x + lane;
-            id[x] = j < to ? row[j] : -1;
-        }
+        for (int x = 0; x < kBlock / 32; ++x) id[x] = 32 * x + lane < n ? row[32 * x + lane] : -1;
 #pragma unroll
         for (int x = 0; x < kBlock / 32; ++x) {
             if (id[x] >= 0 && id[x] < a.num_pages) atomicSub(a.shares + id[x], 1);
-            else bad |= from + 32 * x + lane < to;
+            else bad |= 32 * x + lane < n;
         }
     }
     sync();
 
-    // this warp's pages [p0, p1), in the order of the CTAs and of their warps
+    // this warp's pages, `pages` from p0 on, in the order of the CTAs and of their warps
     const int each = (int)(((long long)a.num_pages + warps * 32 - 1) / (warps * 32)) * 32;
     const long long mine = (long long)cta * kReleaseWarps + w;
-    const int p0 = (int)min((long long)a.num_pages, mine * each), p1 = (int)min((long long)a.num_pages, (long long)p0 + each);
+    const int p0 = (int)min((long long)a.num_pages, mine * each), pages = min(a.num_pages - p0, each);
+    int32_t* const shares = a.shares + p0;
     int count = 0;
 #pragma unroll 8
-    for (int p = p0 + lane; p < p1; p += 32) count += __ldcg(a.shares + p) < 0;
+    for (int i = lane; i < pages; i += 32) count += __ldcg(shares + i) < 0;
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) warp_count[w] = count;
     __syncthreads();
@@ -270,12 +272,12 @@ __global__ void __launch_bounds__(kReleaseThreads, 1) page_release_kernel(PageRe
     int before = s_before + warp_count[w];
     const int total = s_total;
 #pragma unroll 4
-    for (int q = p0; q < p1; q += 32) {
-        const int p = q + lane, s = p < p1 ? __ldcg(a.shares + p) : 0;
+    for (int q = 0; q < pages; q += 32) {
+        const int i = q + lane, s = i < pages ? __ldcg(shares + i) : 0;
         const unsigned gone = __ballot_sync(0xffffffffu, s < 0);
         if (s < 0) {
-            a.freed[before + __popc(gone & ((1u << lane) - 1u))] = p;
-            a.shares[p] = 0;
+            a.freed[before + __popc(gone & ((1u << lane) - 1u))] = p0 + i;
+            shares[i] = 0;
             bad |= s < -1;             // given back more often than it was held
         }
         before += __popc(gone);
@@ -294,7 +296,7 @@ cudaError_t launch_page_fork(const PageForkArgs& a, cudaStream_t stream)
     static KernelSetup setup;
     const cudaError_t e = setup(page_fork_kernel, sizeof(ForkSmem) + kMaxRows * sizeof(int));
     if (e != cudaSuccess) return e;
-    const long long items = (long long)a.forks * ((a.table_cols + kBlock - 1) / kBlock), ctas = (items + kForkWarps - 1) / kForkWarps;
+    const long long items = (long long)a.forks * blocks_of(a.table_cols), ctas = (items + kForkWarps - 1) / kForkWarps;
     const int grid = (int)(ctas < 1 ? 1 : ctas > 152 ? 152 : ctas);
     page_fork_kernel<<<grid, kForkThreads, sizeof(ForkSmem) + (size_t)a.forks * sizeof(int), stream>>>(a);
     return cudaGetLastError();
