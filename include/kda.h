@@ -603,7 +603,9 @@ size_t kda_chunk_attention_workspace_bytes(const kda_chunk_attention_desc* desc)
  * output, NaN included.  A sequence whose context_lens is negative, or with its chunk exceeds its table row or
  * 2^31 - 8192 tokens, gets zeros; a token whose page id is outside [0, num_pages) is left out (a row that has nothing
  * else becomes zero); bad cu_seqlens leave out as it was; all make kda_last_device_status() return
- * KDA_ERR_INVALID_ARG.  A row whose visible scores are all -inf is NaN, as by the definition.  bf16: the softmax's weights are rounded to bf16 before they meet the values (their sum is
+ * KDA_ERR_INVALID_ARG.  A row whose visible scores are all -inf is NaN, as by the definition.
+ * Weighted sums of values up to 2^82 (5e24) in magnitude stay finite whatever the scores and lengths; those of larger ones may
+ * overflow where the definition does not.  bf16: the softmax's weights are rounded to bf16 before they meet the values (their sum is
  * kept in fp32), fp32: fp32 throughout.
  */
 kda_status kda_chunk_attention(const kda_chunk_attention_desc* desc,

@@ -20,7 +20,9 @@ namespace {
 
 constexpr int kThreads = 128, kBM = 64, kTM = 8;
 constexpr float kTame = 4096.f;        // largest maximum (in powers of two) of the quick form
-constexpr float kMostSum = 32768.f;    // most that a thread's weights of a tile's row may sum to before the maximum is set anew
+// Most that a thread's weights of a tile's row may sum to before the maximum is set anew.  16 threads and 2^26 tiles of 32 tokens make a
+// row's sum 2^45 at most, so sums with values up to 2^82 stay finite.  With 32 instead of 2^15 sharper scores cost 1 to 2 %.
+constexpr float kMostSum = 32768.f;
 // The maximum of a row that sees tokens whose scores are all -inf: its weights are 0 over 0, as by the definition, where a row that sees
 // no token (maximum -inf) becomes zero.
 constexpr float kLowest = -FLT_MAX;

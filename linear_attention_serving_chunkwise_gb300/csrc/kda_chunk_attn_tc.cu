@@ -9,7 +9,11 @@
 // other's products.  (Units of 128 rows, whose tiles the streams take in turn, lose where there is work: 32 single tokens after 8192 252 us
 // instead of 214, 40 tokens 537 instead of 236; for 129 tokens after none they win, 17.7 us instead of 20.5.)
 // A row's maximum is set anew, and O multiplied, only when its weights of a tile sum to more than 2^15 (until then no
-// weight is more, which bf16 and the fp32 sums hold as well).
+// weight is more, which bf16 and the fp32 sums hold as well).  That takes up to 15 bits of the range that O has for values: 2^24 tiles
+// of 2^15 make a row's sum 2^39 at most, so with values up to 2^82, the fp32 kernel's bound, nothing overflows.  A limit of 2^8
+// leaves seven bits more and costs four times sharper scores than a standard normal's 37 % (a prompt of 8192 400 -> 545 us).
+// The weights are rounded to bf16 because the tensor core takes both operands of a product in one 16-bit type, and the values
+// are bf16; their sum is that of the unrounded ones.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of stream 0 and 1, a row to a thread.  Warps 8-11:
 // the cache rows, into a ring of K and V tiles.  A thread of warp 12 issues the products, warps

@@ -98,3 +98,25 @@ def test_rows_without_a_page_stay_zero_beside_them(cuda_lib, dtype, D):
     out = cuda_lib.chunk_attention(q.to(dtype).cuda(), kc, vc, table, c, cu)
     assert out[:2].isnan().all() and not out[2:].any()
     assert cuda_lib.last_device_status() == cuda_lib.KDA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+@pytest.mark.parametrize("H,Hk,ctx,new", [(2, 1, [700] * 200, [1] * 200), (4, 1, [900, 0, 2000], [70, 650, 1]), (1, 1, [40000], [1])])
+def test_large_values_under_scores_that_grow_a_little(cuda_lib, dtype, D, H, Hk, ctx, new):
+    """Values of the largest size that is promised to stay finite; scores that grow behind the first tile by just less than what renews the
+    maximum, so that the weights are as large as they get (bf16: 128 of e^5.5, of 2^15 in all; fp32: 2 or 4 a thread of e^9)."""
+    gen = torch.Generator().manual_seed(6)
+    lens = [c + n for c, n in zip(ctx, new)]
+    q = torch.zeros(sum(new), H, D)
+    q[..., 3] = 1
+    k = [torch.zeros(n, Hk, D) for n in lens]
+    for x in k:
+        x[128:, :, 3] = 5.5 if dtype == torch.bfloat16 else 9.0
+    v = [(torch.rand(n, Hk, D, generator=gen) + 0.5) * torch.where(torch.rand(D, generator=gen) < 0.5, -1.0, 1.0) * 2.0 ** 81 for n in lens]
+    q, k, v = q.to(dtype), [x.to(dtype) for x in k], [x.to(dtype) for x in v]
+    kv, table, c, cu, args = _paged(cuda_lib, k, v, lens, new, 16)
+    assert max(float(x.abs().max()) for x in v) <= 2.0 ** 82
+    out = cuda_lib.chunk_attention(q.cuda(), *args, scale=1.0).cpu().double()
+    ref, bound, mass = R.chunk_attention(q, kv[:, 0], kv[:, 1], table, c, cu, 1.0)
+    more = 2.0 ** -8 * (mass + ref.abs()) if dtype == torch.bfloat16 else 0.0
+    assert ((out - ref).abs() <= bound + more).all() and cuda_lib.last_device_status() == cuda_lib.KDA_OK
