@@ -578,7 +578,7 @@ typedef struct kda_chunk_attention_desc {
     int32_t num_pages;      /* pages of the caches */
     int32_t page_size;      /* tokens of a page >= 1 */
     int32_t table_cols;     /* pages a sequence's table row can hold */
-    float scale;            /* factor of the scores, finite */
+    float scale;            /* factor of the scores, 2^126 in magnitude at most */
     int64_t k_page_stride;  /* elements from one page to the next, >= page_size * Hk * dim, */
     int64_t v_page_stride;  /*   a multiple of 16 bytes */
 } kda_chunk_attention_desc;

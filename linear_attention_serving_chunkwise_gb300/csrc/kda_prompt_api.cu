@@ -32,7 +32,8 @@ kda::ChunkAttnArgs chunk_args(const kda_chunk_attention_desc& d)
 kda_status validate_chunk(const kda_chunk_attention_desc* d)
 {
     if (!d || d->batch < 0 || d->total_tokens < 0 || d->num_heads < 1 || d->num_kv_heads < 1 || d->num_heads % d->num_kv_heads ||
-        d->num_pages < 0 || d->page_size < 1 || d->table_cols < 0 || !isfinite(d->scale))
+        d->num_pages < 0 || d->page_size < 1 || d->table_cols < 0 ||
+        !(fabsf(d->scale) <= 0x1p126f))     // (scores are kept in powers of two: scale / ln 2 is finite too)
         return KDA_ERR_INVALID_ARG;
     if (!known_dtype(d->dtype) || (d->dim != 64 && d->dim != 128) || d->num_heads / d->num_kv_heads > KDA_CHUNK_MAX_GROUP) return KDA_ERR_UNSUPPORTED;
     if ((size_t)d->total_tokens > 0x7fffffffull / d->num_heads) return KDA_ERR_INVALID_ARG;
