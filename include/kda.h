@@ -651,7 +651,7 @@ typedef struct kda_norm_rotate_desc {
  *   q_out         [T, Hq, dim] dtype
  *   k_cache, v_cache  as kda_tree_attention's; only the slots' rows are written
  * fp32 arithmetic, rounded once; angles are exact to 1e-9 of a turn at any position, for frequencies up to 2^40 (a pair of an
- * infinite or NaN frequency is NaN).
+ * infinite or NaN frequency is NaN).  A row's squares are summed in fp32: its elements stay below 1e18, and with eps 0 not all below 1e-18.
  * q_out overlaps nothing, the caches no input.  A slot past the caches is left out and makes
  * kda_last_device_status() return KDA_ERR_INVALID_ARG.
  */
@@ -664,8 +664,9 @@ kda_status kda_norm_rotate(const kda_norm_rotate_desc* desc, const void* q, cons
  * kda_page_fork -- table rows that share another row's first tokens.  Fork i gives the empty row children[i] the
  * first lens[i] tokens of row parents[i]: its whole pages by reference, and for a last page that they fill only partly a page of its
  * own, into which kda_cache_copy copies the rows.  lens[i] is at most what the parent has written: pages that it
- * holds past that (for drafts) cannot be told from others here, and a whole one would be shared although the parent appends to it.  `shares` counts the rows that hold a page beyond the first, so that
- * kda_page_release knows when it is free; pages of kda_page_tables start at 0.
+ * holds past that (for drafts) cannot be told from others here, and a whole one would be shared although the parent appends
+ * to it.  `shares` counts the rows that hold a page beyond the first, so that kda_page_release knows when it is free; pages of
+ * kda_page_tables start at 0.
  *
  *   parents, children, lens  [num_forks] int32; a parent may come many times, a child once
  *   pages_held     [rows] int32; 0 for a child
@@ -677,7 +678,7 @@ kda_status kda_norm_rotate(const kda_norm_rotate_desc* desc, const void* q, cons
  *   pages_taken    [1] int32: free_pages entries used up
  * A fork for which the free pages do not reach is refused: its child stays empty, its copy is none; no later one takes a page
  * then.  A row out of range, a length that is negative or that the parent's pages do not cover, a child that
- * holds pages, comes twice or is a parent in the same call: the fork does nothing.  A page id
+ * holds pages or comes twice, a parent that is a child in the same call: the fork does nothing.  A page id
  * out of range is passed on without a share.  Both make kda_last_device_status() return KDA_ERR_INVALID_ARG.
  * No output may overlap an input or another output.  num_forks <= rows <= KDA_PAGE_TABLES_MAX_BATCH.
  */

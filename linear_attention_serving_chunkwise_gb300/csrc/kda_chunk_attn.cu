@@ -2,14 +2,15 @@
 // (fp32 throughout).
 //
 // A thread has 8 query rows and BN / 16 tokens of a tile's scores, then 8 rows and D / 16 channels of
-// the output: 12 shared-memory reads to 128 multiply-adds.  One pass over the tiles with the running maximum
+// the output: 12 shared-memory reads to 128 multiply-adds (scores at D = 128: 10 to 64).  One pass over the tiles with the running maximum
 // and sum of the softmax.  A tile's values are zeroed where no row of the unit may see the token (past its last one, a page
 // out of range); in the tiles that only some rows see whole, a weight of 0 is skipped: 0 times whatever lies there
 // must not be NaN.
 // Bound: the CUDA cores, half of their multiply-adds; without the scores' loop the kernel takes 0.62 of its time, without the values'
 // 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 197 us, 33 TFLOP/s; 2048 tokens after
-// 2048, 32 heads on 8 1.25 ms (D = 64, 41 TFLOP/s), 2.68 ms (D = 128).  Two multiply-adds at a time (198 us, 1.23 and 2.48 ms), a second buffer
-// for the tiles (226 instead of 201 us), other rows to a thread (216) and operands fetched a step ahead (204) gave little or nothing.
+// 2048, 32 heads on 8 1.28 ms (D = 64, 40 TFLOP/s), 2.71 ms (D = 128).  Two multiply-adds at a time took 198 us, 1.23 and 2.48 ms beside 197 us, 1.25
+// and 2.68: 7 % at D = 128 and little at 64, not built in so far.  A second buffer for the tiles (226 instead of 201 us), other rows to a
+// thread (216) and operands fetched a step ahead (204) lost.
 #include <float.h>
 
 #include "kda_chunk_attn.cuh"

@@ -76,7 +76,7 @@ struct Piece {
     int b, hk;
     int tok, tokens;        // first token of the block within the chunk, and how many
     int row0;               // q's row of that token
-    int ctx, n;             // of the sequence
+    int ctx;                // of the sequence
     bool ok;
     int first, last, tiles;
     int range, slot;        // the range, and the workspace slot of the part when it is not the whole unit
@@ -187,7 +187,6 @@ struct Line {
             p.tokens = min(TB, s.n - p.tok);
             p.row0 = s.tok0 + p.tok;
             p.ctx = s.ctx;
-            p.n = s.n;
             p.ok = s.ok;
             p.seen = s.ok ? s.ctx + p.tok + p.tokens : 0;
             p.common = s.ok ? s.ctx + p.tok + 1 : 0;

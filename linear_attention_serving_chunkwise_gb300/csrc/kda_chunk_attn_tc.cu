@@ -19,12 +19,12 @@
 // the cache rows, into a ring of K and V tiles.  A thread of warp 12 issues the products, warps
 // 13-15 copy Q.  The last two groups give registers to the softmax.
 //
-// Bound, for many rows: not the tensor pipe alone (67 % busy: 2048 of some 2900 cycles a tile of 256 rows x 128 tokens,
+// Bound, for many rows: not the tensor pipe alone (69 % busy: 2048 of some 2960 cycles a tile of 256 rows x 128 tokens,
 // D = 128) but each stream's chain scores - softmax - values, which the other one's products cover only in part.  The softmax's way
 // from scores to weights takes 1200 cycles, of which 750 form 128 weights a thread, and the products' thread adds waits and commits.
 // 2048 tokens after 131072, 32 heads on 8: 2.90 to 2.95 ms, 1500 to 1530 TFLOP/s (0.79 of cuBLAS's burst); 12 sequences of 1 to 2048 tokens
 // after up to 16384, 96 heads on 8: 4.05 to 4.10 ms, 1420 to 1440; a prompt of 8192: 399 us, 1380; 512 after 131072: 735 us, 1500; 16
-// prompts of 512: 98 us, 350 (a unit of three tiles costs 11 us: its first tile, masks and epilogue); 64 tokens after 4096 to 32768
+// prompts of 512: 99 us, 350 (a unit of three tiles costs 11 us: its first tile, masks and epilogue); 64 tokens after 4096 to 32768
 // each: 790 to 810 us, 6.2 TB/s; D = 64: 2048 after 131072 2.2 ms, 1000 (the same
 // softmax for half the products).  In one wave instead of eight the first two took 3.52 and 4.83 ms instead of 3.03 and 4.27;
 // with the weights handed over in two parts 2.99 and 4.37 instead of 3.00 and 4.20.

@@ -17,8 +17,8 @@
 // rotated), so a rotation needs no exchange and a norm three shuffles.  A warp has one token (or an eighth of one, where
 // tokens are few), whose turns and weights stay in registers for all its rows: read from shared memory for every row
 // they were what bound it (364 us instead of 300 for 32768 tokens).
-// Bound: HBM.  32768 tokens, 96 query and 8 cache heads of 128 channels, bf16: 300 us, 6.3 TB/s (0.92 of a copy); fp32, 32 and 8
-// heads: 241 us, 6.7 TB/s; 64 tokens: 6.1 us, the launch and the chain of one row.  Two rows in flight a lane and three CTAs an SM:
+// Bound: HBM.  32768 tokens, 96 query and 8 cache heads of 128 channels, bf16: 295 us, 6.4 TB/s (0.94 of a copy); fp32, 32 and 8
+// heads: 240 us, 6.7 TB/s; 64 tokens: 6.1 us, the launch and the chain of one row.  Two rows in flight a lane and three CTAs an SM:
 // 299 us; four and two 303, one and four 321.
 #include "kda_common.cuh"
 #include "kda_prompt_launch.h"
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rotate_kernel(NormRotateArgs
 template <typename T, int D>
 cudaError_t launch(const NormRotateArgs& a, cudaStream_t stream)
 {
-    // Fewer warps to a token as tokens fill the GPU (1, 2, 4, 8 tokens to a CTA; us, 32 and 8 heads): 256 tokens 6.4, 6.4, 8.4, 10.5;
+    // Fewer warps to a token as tokens fill the GPU (1, 2, 4, 8 tokens to a CTA; us, 32 and 8 heads; turns formed token by token): 256 tokens 6.4, 6.4, 8.4, 10.5;
     // 608 10.5, 8.4, 8.4, 10.4; 1024 14.6, 12.5, 10.5, 10.5; 2432 24.7, 16.7, 16.6, 14.6; 32768 291, 187, 146, 140.
     const int per = a.tokens <= 304 ? 1 : a.tokens <= 608 ? 2 : a.tokens <= 1216 ? 4 : kMostTokens, grid = (a.tokens - 1) / per + 1;
     if (a.interleaved) norm_rotate_kernel<T, D, true><<<grid, kThreads, 0, stream>>>(a, per);

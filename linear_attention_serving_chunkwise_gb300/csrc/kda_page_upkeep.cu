@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(PageForkArgs a)
 //      are exchanged, each warp writes its own behind those of the warps before it.
 // Integer sums only, and no order of arrival shows in the outputs.
 // One CTA for what it does in a few microseconds, else a cooperative grid: see kAlonePages.  Bound: latency, of the reads and
-// of four grid barriers: 2048 rows in a pool of 600000 pages 18 us; a launch for each step, the last one a cluster of 16 CTAs, 27.
+// of four grid barriers: 2048 rows in a pool of 600000 pages 15.5 us (pages given back twice 16.0; from call to call 18.4); a launch for each step, the last one a cluster of 16 CTAs, 27.
 constexpr int kReleaseThreads = 1024, kReleaseWarps = kReleaseThreads / 32, kReleaseCtas = 152;
 // One CTA alone up to these (GPU time): 4096 pages, 16 rows 8.4 us (a grid 13.9); 16384 pages, 64 rows of 128 14.0 (12.4), 512 rows
 // 32.9 (12.7); 600000 pages, 2048 rows of 512 315 (18.6).

@@ -44,7 +44,8 @@ def _rows_for_the_kernel(cache: torch.Tensor, nodes: int) -> bool:
     """Whether ``cache_keep_path`` takes the rows of a cache [pages, 2, page_size, heads, dim] and steps of that many nodes."""
     row, size = cache.shape[3] * cache.shape[4], cache.element_size()
     return (cache.is_cuda and cache.get_device() == torch.cuda.current_device() and cache.dtype in (torch.bfloat16, torch.float32)
-            and 1 <= nodes <= KDA_TREE_MAX_NODES and cache.numel() > 0 and cache[0, 0].is_contiguous()
+            and 1 <= nodes <= KDA_TREE_MAX_NODES and cache.numel() > 0
+            and (cache.stride()[2:] == (row, cache.shape[4], 1) or cache[0, 0].is_contiguous())
             and all(x * size % 16 == 0 for x in (row, cache.stride(0), cache.stride(1))) and cache.data_ptr() % 16 == 0)
 
 
