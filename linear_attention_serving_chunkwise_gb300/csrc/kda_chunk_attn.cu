@@ -4,8 +4,8 @@
 // A thread has 8 query rows and BN / 16 tokens of a tile's scores, then 8 rows and D / 16 channels of
 // the output: 12 shared-memory reads to 128 multiply-adds (scores at D = 128: 10 to 64).  One pass over the tiles with the running maximum
 // and sum of the softmax.  A tile's values are zeroed where no row of the unit may see the token (past its last one, a page
-// out of range); in the tiles that only some rows see whole, a weight of 0 is skipped: 0 times whatever lies there
-// must not be NaN.
+// out of range); in the tiles that only some rows see whole, a token that the row does not see has the weight -1, which is skipped: 0
+// times whatever lies there must not be NaN.  (A weight of 0 is not: what a row sees shows, infinities and NaN too.)
 // Bound: the CUDA cores, half of their multiply-adds; without the scores' loop the kernel takes 0.62 of its time, without the values'
 // 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 197 us, 33 TFLOP/s; 2048 tokens after
 // 2048, 32 heads on 8 1.28 ms (D = 64, 40 TFLOP/s), 2.71 ms (D = 128).  Two multiply-adds at a time took 198 us, 1.23 and 2.48 ms beside 197 us, 1.25
@@ -34,7 +34,7 @@ struct Tile {
     static constexpr size_t kSmem = (size_t)(kBM * LD + 2 * BN * LD + kBM * LP) * 4;
 };
 
-// o += p v over a tile: eight rows of weights from sp on, four channels of every 16 from sv on.  kSome: a weight of 0 is
+// o += p v over a tile: eight rows of weights from sp on, four channels of every 16 from sv on.  kSome: a weight below 0 is
 // skipped (a test for each, so not where all rows see the whole tile).
 template <int D, bool kSome>
 __device__ __forceinline__ void add_values(float (&o)[kTM][Tile<D>::CD], const float* sp, const float* sv)
@@ -56,7 +56,7 @@ __device__ __forceinline__ void add_values(float (&o)[kTM][Tile<D>::CD], const f
 #pragma unroll
             for (int i = 0; i < kTM; ++i) {
                 const float p = e == 0 ? p4[i].x : e == 1 ? p4[i].y : e == 2 ? p4[i].z : p4[i].w;
-                if (kSome && p == 0.f) continue;
+                if (kSome && p < 0.f) continue;
 #pragma unroll
                 for (int k = 0; k < L::CD; ++k) o[i][k] = fmaf(p, v[k], o[i][k]);
             }
@@ -207,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 3) chunk_attn_simt_ke
                     for (int j = 0; j < TN; ++j) {
                         p[i][j] = exp2f(s[i][j] - base);
                         sum += p[i][j];
+                        // (on a page that is not there the value is 0, whatever the weight)
+                        if (t0 + tx + 16 * j >= seen[i]) p[i][j] = -1.f;
                     }
                     l[i] = l[i] * f + sum;           // (of this thread's tokens: the row's are summed at the end)
                     m[i] = nm;

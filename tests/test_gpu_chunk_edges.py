@@ -120,3 +120,29 @@ def test_large_values_under_scores_that_grow_a_little(cuda_lib, dtype, D, H, Hk,
     ref, bound, mass = R.chunk_attention(q, kv[:, 0], kv[:, 1], table, c, cu, 1.0)
     more = 2.0 ** -8 * (mass + ref.abs()) if dtype == torch.bfloat16 else 0.0
     assert ((out - ref).abs() <= bound + more).all() and cuda_lib.last_device_status() == cuda_lib.KDA_OK
+
+
+@pytest.mark.parametrize("dtype,D", TYPES, ids=IDS)
+@pytest.mark.parametrize("ps", [16, 20], ids=["boxes", "gathered"])
+def test_what_a_row_sees_shows_under_a_weight_of_nothing(cuda_lib, dtype, D, ps):
+    """An infinite or NaN value whose weight vanishes in fp32 (a score 300 below the others) is seen all the same: the rows from its token on are
+    not finite in its channel; all other rows and channels keep their bits."""
+    ctx, new = [70, 0, 250], [150, 130, 9]
+    lens, gen = [c + n for c, n in zip(ctx, new)], torch.Generator().manual_seed(9)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(dtype)
+    q, k, v = rnd(sum(new), 3, D), [rnd(n, 1, D) for n in lens], [rnd(n, 1, D) for n in lens]
+    q[..., 3] = 1
+    for b, i in ((0, 1), (0, 60), (0, 149), (0, -40), (1, 1), (1, 129), (2, 4), (2, -250)):
+        at = ctx[b] + i
+        k2, v2 = [x.clone() for x in k], [x.clone() for x in v]
+        k2[b][at, :, 3] = -300 * D ** 0.5
+        _, _, _, cu, args = _paged(cuda_lib, k2, v2, lens, new, ps)
+        clean = cuda_lib.chunk_attention(q.cuda(), *args)
+        for what in (float("inf"), float("nan")):
+            v2[b][at, 0, 5] = what
+            _, _, _, cu, args = _paged(cuda_lib, k2, v2, lens, new, ps)
+            out = cuda_lib.chunk_attention(q.cuda(), *args)
+            hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+            hit[cu[b] + max(i, 0):cu[b + 1], :, 5] = True
+            assert not out[hit].isfinite().any() and torch.equal(out[~hit], clean[~hit]), (b, i, what)
+    assert cuda_lib.last_device_status() == cuda_lib.KDA_OK
