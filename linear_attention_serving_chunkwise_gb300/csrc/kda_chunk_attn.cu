@@ -7,7 +7,7 @@
 // out of range); in the tiles that only some rows see whole, a token that the row does not see has the weight -1, which is skipped: 0
 // times whatever lies there must not be NaN.  (A weight of 0 is not: what a row sees shows, infinities and NaN too.)
 // Bound: the CUDA cores, half of their multiply-adds; without the scores' loop the kernel takes 0.62 of its time, without the values'
-// 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 197 us, 33 TFLOP/s; 2048 tokens after
+// 0.67, without either 0.32 (64 channels).  5 sequences of 1 to 701 tokens after up to 3001, 6 heads on 2, D = 64 200 us, 33 TFLOP/s; 2048 tokens after
 // 2048, 32 heads on 8 1.28 ms (D = 64, 40 TFLOP/s), 2.71 ms (D = 128).  Two multiply-adds at a time took 198 us, 1.23 and 2.48 ms beside 197 us, 1.25
 // and 2.68: 7 % at D = 128 and little at 64, not built in so far.  A second buffer for the tiles (226 instead of 201 us), other rows to a
 // thread (216) and operands fetched a step ahead (204) lost.
